@@ -1,0 +1,46 @@
+// What the gated delta rule's kernels share.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include "kv4_device.h"
+#include "mix_internal.h"
+#include "qmm_device.h"
+
+namespace qmm {
+
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr float kGdnEps = 1e-6f;
+
+struct GdnSeq {
+  int t0, len, slot;
+};
+// Sequence b: its tokens (held inside [0, T] whatever seq_start says) and its state's slot.
+__device__ __forceinline__ GdnSeq gdn_seq(const GdnArgs& g, int b) {
+  int64_t a = b, e = int64_t(b) + 1;
+  if (g.seq_start) {
+    a = g.seq_start[b], e = g.seq_start[b + 1];
+    a = a < 0 ? 0 : a > g.T ? g.T : a;
+    e = e < a ? a : e > g.T ? g.T : e;
+  }
+  GdnSeq s;
+  s.t0 = int(a);
+  s.len = int(e - a) < g.max_len ? int(e - a) : g.max_len;
+  s.slot = g.slots ? g.slots[b] : b;
+  return s;
+}
+
+// Sum over the lane's row of 16 (all of them active).
+__device__ __forceinline__ float sum16_lanes(float x) {
+  x += dpp_mov<kQuadXor1>(x);
+  x += dpp_mov<kQuadXor2>(x);
+  x += dpp_mov<kHalfMirror>(x);
+  return x + dpp_mov<kRowMirror>(x);
+}
+
+__device__ __forceinline__ void gdn_store(const GdnArgs& g, int64_t at, float y) {
+  if (g.f32_out) static_cast<float*>(g.y)[at] = y;
+  else static_cast<uint16_t*>(g.y)[at] = f32_to_bf16_bits(y);
+}
+
+}  // namespace qmm

@@ -1,0 +1,512 @@
+// Attention of few queries over the paged 4-bit cache (qmm_kv4_attn's serving form).
+//
+// Mathematics.  For a key t with group scales s, biases b and codes c the score is
+//   q.k_t = sum_g s_g (q_g . c_g) + b_g sum(q_g),
+// so the codes enter the matrix product exactly and each group's scale and bias are two
+// fp32 multiply-adds on the product.  The output is
+//   sum_t p_t v_t = sum_t (p_t s_t) c_t + sum_t p_t b_t,
+// with p_t s_t rounded to fp16 (relative 2^-12, an eighth of the output's own rounding) and
+// everything else in fp32.  A nibble c masked in place is the fp16 number c 2^-24 (or, in
+// the next four bits, 16 c 2^-24): a subnormal that the matrix cores take exactly, so a code
+// costs half a mask instruction and no conversion; the powers of two go into q (1/16 for the
+// odd places) and into the final factor.
+//
+// Bound: the cache's bytes (HBM) for long contexts, launch and latency for short ones.
+//
+// Split.  A block of 4 waves takes one KV head's up to 16 (query, head) rows and a range of
+// keys; its waves take 32 keys at a time and keep an online softmax of their own (maximum,
+// sum and output in registers, no barrier), joined once at the end.  Keys are the rows of
+// the first product (S^T = K Q^T) and dims the rows of the second (O^T = V^T P^T), so a lane
+// that gets the scores of keys 8h .. 8h+7 of its column holds exactly the probabilities
+// that the second product wants from it: nothing crosses lanes between the two.  A lane's
+// share of the scales is one word per group pair, read once and broadcast along the row by
+// the multiply-add itself (DPP row_newbcast).
+#include <hip/hip_runtime.h>
+
+#include <utility>
+
+#include "kv4_attn.h"
+#include "kv4_device.h"
+#include "qmm_device.h"
+#include "qmm_internal.h"
+
+namespace qmm {
+namespace {
+
+constexpr int kTile = 32;    // keys of a wave's step
+constexpr int kWaves = 4;
+constexpr float kFloor = -1e30f;  // maximum of a row that has seen no key yet
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int HD>
+struct Buf {
+  static constexpr int NG = HD / 64, NKL = HD == 256 ? 2 : 1, R = NG > 1 ? NG / 2 : 1;
+  u32x4_t k[2][NKL];  // key codes of the two 16-key tiles
+  u32x4_t v[NG];      // value codes: 8 keys x 4 dims of each group
+  uint32_t km[R], vm[R];
+};
+
+// Lane (of its row of 16) and register that hold the meta word of key tk (0..7), group g.
+template <int NG>
+constexpr int meta_lane(int tk, int g) { return NG == 1 ? tk : (tk * NG + g) / (NG / 2); }
+template <int NG>
+constexpr int meta_reg(int tk, int g) { return NG == 1 ? 0 : (tk * NG + g) % (NG / 2); }
+
+__device__ __forceinline__ float half_lo(uint32_t w) {
+  return float(__builtin_bit_cast(_Float16, uint16_t(w)));
+}
+__device__ __forceinline__ float half_hi(uint32_t w) {
+  return float(__builtin_bit_cast(_Float16, uint16_t(w >> 16)));
+}
+
+// The four operands (dims 4n + 0..3 of the 16 rows n) of 8 keys' value codes, and the
+// operand of one key word: nibbles in place.
+__device__ __forceinline__ f16x8_t nib_operand(const u32x4_t& w, int j) {
+  u32x4_t r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = j >= 2 ? w[i] >> 8 : w[i];
+    r[i] = x & (j & 1 ? 0x00F000F0u : 0x000F000Fu);
+  }
+  return __builtin_bit_cast(f16x8_t, r);
+}
+__device__ __forceinline__ f16x8_t key_operand(uint32_t w) {
+  u32x4_t r;
+  const uint32_t x = w >> 8;
+  r[0] = w & 0x000F000Fu;
+  r[1] = w & 0x00F000F0u;
+  r[2] = x & 0x000F000Fu;
+  r[3] = x & 0x00F000F0u;
+  return __builtin_bit_cast(f16x8_t, r);
+}
+
+template <int HD, bool PG32>
+__global__ __launch_bounds__(256, 2) void kv4_decode_kernel(Kv4AttnArgs g, int group, int nsplit_max) {
+  using B = Buf<HD>;
+  constexpr int NG = B::NG, NKL = B::NKL, R = B::R;
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, hg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int split = blockIdx.x, b = blockIdx.z;
+  const int kvh = blockIdx.y % g.c.n_kv, rt = blockIdx.y / g.c.n_kv;
+
+  const AttnSeq sq = attn_seq(g, b);
+  const int row0 = rt * 16, rows = sq.q_len * group - row0;
+  if (rows <= 0) return;
+  const AttnSpan sp = attn_span(g, sq, row0 / group, (row0 + (rows < 16 ? rows : 16) - 1) / group);
+  const AttnSplit pl = attn_split(sp, nsplit_max, split);
+  if (split >= pl.count) return;
+
+  // the lane's column: one (query, head) row
+  const bool col_ok = n < rows;
+  const int cj = (row0 + n) / group, ch = kvh * group + (row0 + n) % group;
+  const int64_t qrow = (int64_t(sq.q0) + cj) * g.n_q + ch;
+  int c_lo = 0, c_hi = sq.kv_len;
+  if (col_ok && g.causal) {
+    const int64_t p = int64_t(sq.first) + cj;
+    c_hi = p < 0 ? 0 : int(p) + 1;
+    c_lo = g.window > 0 && p - g.window + 1 > 0 ? int(p - g.window + 1) : 0;
+  }
+
+  // q as operands: fp16 scaled by a power of two so that the row's largest is in
+  // [2^14, 2^15) (bf16 values stay exact), odd places by 1/16 more
+  f16x8_t qf[NG][2];
+  float qs, xs[NG];
+  {
+    float x[NG][2][8], mx = 0.f;
+#pragma unroll
+    for (int e = 0; e < NG * 2; ++e) {
+      const int p = HD == 64 ? 0 : e / 4, j = HD == 64 ? e : e % 4;
+      const int gi = HD == 64 ? 0 : 2 * p + (j >> 1);
+      const int w = k_word_of<HD>(p, hg, j);
+      u32x4_t v = {0, 0, 0, 0};
+      if (col_ok) v = *reinterpret_cast<const u32x4_t*>(g.q + qrow * HD + 8 * w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[gi][j & 1][2 * i] = bf16_lo(v[i]);
+        x[gi][j & 1][2 * i + 1] = bf16_hi(v[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s += x[i][j >> 3][j & 7], mx = fmaxf(mx, fabsf(x[i][j >> 3][j & 7]));
+      s += __shfl_xor(s, 16);
+      xs[i] = s + __shfl_xor(s, 32);
+    }
+    mx = fmaxf(mx, __shfl_xor(mx, 16));
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    const int ex = mx > 0.f ? int((__float_as_uint(mx) >> 23) & 255) - 127 : 0;
+    const int sh = 14 - ex;  // in [-113, 141]
+    qs = g.scale * kLog2e * ldexpf(1.f, 24 - sh);
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      xs[i] = ldexpf(xs[i], sh - 24);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        // operand order: nibbles (0, 4), (1, 5), (2, 6), (3, 7)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int down = (t & 1) ? sh - 4 : sh;
+          qf[i][j][2 * t] = static_cast<_Float16>(ldexpf(x[i][j][t], down));
+          qf[i][j][2 * t + 1] = static_cast<_Float16>(ldexpf(x[i][j][t + 4], down));
+        }
+      }
+    }
+  }
+
+  // wave-uniform: tiles wholly inside [u_lo, u_hi) need no mask
+  int u_lo = c_lo, u_hi = c_hi;
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) {
+    u_lo = max(u_lo, __shfl_xor(u_lo, o));
+    u_hi = min(u_hi, __shfl_xor(u_hi, o));
+  }
+  u_lo = __builtin_amdgcn_readfirstlane(u_lo);
+  u_hi = __builtin_amdgcn_readfirstlane(u_hi);
+
+  const int psh = g.c.page_shift, pmask = (1 << psh) - 1;
+  const int32_t* __restrict__ table = g.table + int64_t(b) * g.max_pages;
+  const int last_entry = sq.kv_len > 0 ? (sq.kv_len - 1) >> psh : 0;
+
+  // rows (token slots of this head) of the tile's two halves, and whether their page exists
+  struct Where {
+    int64_t r0, r1;
+    bool ok0, ok1;
+  };
+  auto where = [&](int t0) {
+    Where w;
+    const int e0 = t0 >> psh;
+    const int id0 = table[e0 < last_entry ? e0 : last_entry];
+    w.ok0 = uint32_t(id0) < uint32_t(g.c.n_pages);
+    w.r0 = ((int64_t(w.ok0 ? id0 : 0) * g.c.n_kv + kvh) << psh) + (t0 & pmask);
+    if constexpr (PG32) {
+      w.ok1 = w.ok0;
+      w.r1 = w.r0 + 16;
+    } else {
+      const int e1 = (t0 + 16) >> psh;
+      const int id1 = table[e1 < last_entry ? e1 : last_entry];
+      w.ok1 = e1 <= last_entry && uint32_t(id1) < uint32_t(g.c.n_pages);
+      w.r1 = ((int64_t(w.ok1 ? id1 : 0) * g.c.n_kv + kvh) << psh) + ((t0 + 16) & pmask);
+    }
+    return w;
+  };
+  const int krow = 8 * ((n >> 2) & 1) + (n & 3);  // + 4u: the lane's key within its half (n / 8)
+  auto load = [&](const Where& w, B& x) {
+    const int64_t rk = PG32 ? w.r0 + 8 * (n >> 2) + (n & 3) : (n < 8 ? w.r0 : w.r1) + krow;
+    const int64_t rv = PG32 ? w.r0 + 8 * hg : (hg < 2 ? w.r0 : w.r1) + 8 * (hg & 1);
+    const uint32_t* kp = g.c.k_codes + rk * (HD / 8);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int p = 0; p < NKL; ++p) {
+        if constexpr (HD == 64) {
+          const uint2 v = *reinterpret_cast<const uint2*>(kp + 4 * u * (HD / 8) + 2 * hg);
+          x.k[u][p] = u32x4_t{v.x, v.y, 0, 0};
+        } else {
+          x.k[u][p] = *reinterpret_cast<const u32x4_t*>(kp + 4 * u * (HD / 8) + 16 * p + 4 * hg);
+        }
+      }
+    }
+    const int moff = NG == 1 ? (n & 7) : n * R;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      x.km[i] = g.c.k_meta[rv * NG + moff + i];
+      x.vm[i] = g.c.v_meta[rv * NG + moff + i];
+    }
+    const uint16_t* vp = g.c.v_codes + (rv >> 3) * (HD * 2) + n * 8;
+#pragma unroll
+    for (int i = 0; i < NG; ++i) x.v[i] = *reinterpret_cast<const u32x4_t*>(vp + i * 128);
+  };
+
+  f32x4_t acc[NG][4];
+  float bacc[NG], m = kFloor, l = 0.f;
+#pragma unroll
+  for (int i = 0; i < NG; ++i) {
+    bacc[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  }
+
+  auto step = [&](const B& x, int t0, const Where& w) {
+    float sk[R], bk[R], sv[R], bv[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      sk[i] = half_lo(x.km[i]), bk[i] = half_hi(x.km[i]);
+      sv[i] = half_lo(x.vm[i]), bv[i] = half_hi(x.vm[i]);
+    }
+    float sc[8];
+    static_for<2>([&](auto uc) {
+      constexpr int u = decltype(uc)::value;
+      f32x4_t d[NG];
+#pragma unroll
+      for (int i = 0; i < NG; ++i) d[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < NG * 2; ++e) {
+        const int p = HD == 64 ? 0 : e / 4, j = HD == 64 ? e : e % 4;
+        const int gi = HD == 64 ? 0 : 2 * p + (j >> 1);
+        d[gi] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_operand(x.k[u][p][j]), qf[gi][j & 1], d[gi], 0, 0, 0);
+      }
+      static_for<4>([&](auto ic) {
+        constexpr int i = decltype(ic)::value, tk = 4 * u + i;
+        float s = 0.f;
+        static_for<NG>([&](auto gc) {
+          constexpr int gi = decltype(gc)::value, ln = meta_lane<NG>(tk, gi), rg = meta_reg<NG>(tk, gi);
+          s = fmaf(row_bcast<ln>(sk[rg]), d[gi][i], s);
+          s = fmaf(row_bcast<ln>(bk[rg]), xs[gi], s);
+        });
+        sc[tk] = s;
+      });
+    });
+    const bool masked = t0 < u_lo || t0 + kTile > u_hi || !w.ok0 || !w.ok1;
+    uint32_t vis = 0xFF;
+    if (masked) {
+      const int tb = t0 + 8 * hg;
+      const bool ok = hg < 2 ? w.ok0 : w.ok1;
+      vis = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool see = ok && tb + i >= c_lo && tb + i < c_hi;
+        vis |= see ? 1u << i : 0u;
+        sc[i] = see ? sc[i] : -INFINITY;
+      }
+    }
+    float mx = fmaxf(fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])), fmaxf(fmaxf(sc[4], sc[5]), fmaxf(sc[6], sc[7])));
+    if (__any(mx > m)) {
+      mx = fmaxf(mx, __shfl_xor(mx, 16));
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      const float mn = fmaxf(m, mx);
+      const float fac = exp2_hw((m - mn) * qs);
+      m = mn;
+      l *= fac;
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        bacc[i] *= fac;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] *= fac;
+      }
+    }
+    // probabilities times 8 (p <= 1 and scales below 2^13 keep p s within fp16)
+    const float off = fmaf(-m, qs, 3.f);
+    float p[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = exp2_hw(fmaf(sc[i], qs, off));
+    f16x8_t ps[NG];
+    if (!masked) {
+      static_for<8>([&](auto ic) {
+        constexpr int i = decltype(ic)::value;
+        l += p[i];
+        static_for<NG>([&](auto gc) {
+          constexpr int gi = decltype(gc)::value, ln = meta_lane<NG>(i, gi), rg = meta_reg<NG>(i, gi);
+          ps[gi][i] = static_cast<_Float16>(p[i] * row_bcast<ln>(sv[rg]));
+          bacc[gi] = fmaf(row_bcast<ln>(bv[rg]), p[i], bacc[gi]);
+        });
+      });
+    } else {  // hidden keys may hold anything, NaN scales among it
+      static_for<8>([&](auto ic) {
+        constexpr int i = decltype(ic)::value;
+        const bool see = (vis >> i) & 1;
+        const float pi = see ? p[i] : 0.f;
+        l += pi;
+        static_for<NG>([&](auto gc) {
+          constexpr int gi = decltype(gc)::value, ln = meta_lane<NG>(i, gi), rg = meta_reg<NG>(i, gi);
+          const float s1 = row_bcast<ln>(sv[rg]), b1 = row_bcast<ln>(bv[rg]);
+          ps[gi][i] = static_cast<_Float16>(see ? pi * s1 : 0.f);
+          bacc[gi] += see ? pi * b1 : 0.f;
+        });
+      });
+    }
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(nib_operand(x.v[i], j), ps[i], acc[i][j], 0, 0, 0);
+    }
+  };
+
+  // the wave's tiles, the next one's loads under way while one is computed
+  int t = (pl.begin + wave) * kTile;
+  const int t_end = pl.end * kTile;
+  if (t < t_end) {
+    B x0, x1;
+    Where w0 = where(t), w1;
+    load(w0, x0);
+    for (;;) {
+      const int t1 = t + kWaves * kTile;
+      const bool more = t1 < t_end;
+      if (more) {
+        w1 = where(t1);
+        load(w1, x1);
+      }
+      step(x0, t, w0);
+      if (!more) break;
+      const int t2 = t1 + kWaves * kTile;
+      const bool more2 = t2 < t_end;
+      if (more2) {
+        w0 = where(t2);
+        load(w0, x0);
+      }
+      step(x1, t1, w1);
+      if (!more2) break;
+      t = t2;
+    }
+  }
+
+  // join the waves
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+#pragma unroll
+  for (int i = 0; i < NG; ++i) {
+    bacc[i] += __shfl_xor(bacc[i], 16);
+    bacc[i] += __shfl_xor(bacc[i], 32);
+  }
+  __shared__ float s_o[kWaves][16][HD];
+  __shared__ float s_m[kWaves][16], s_l[kWaves][16], s_qs[16];
+  if (hg == 0) {
+    s_m[wave][n] = m;
+    s_l[wave][n] = l;
+    if (wave == 0) s_qs[n] = qs;
+  }
+  __syncthreads();
+  float mm = kFloor;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) mm = fmaxf(mm, s_m[i][n]);
+  if (col_ok) {
+    const float fac = exp2_hw((m - mm) * qs);
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float4 o;
+        o.x = fmaf(acc[i][0][r], 16777216.f, bacc[i]) * fac;
+        o.y = fmaf(acc[i][1][r], 1048576.f, bacc[i]) * fac;
+        o.z = fmaf(acc[i][2][r], 16777216.f, bacc[i]) * fac;
+        o.w = fmaf(acc[i][3][r], 1048576.f, bacc[i]) * fac;
+        *reinterpret_cast<float4*>(&s_o[wave][n][64 * i + 16 * hg + 4 * r]) = o;
+      }
+    }
+  }
+  __syncthreads();
+  const int cols = rows < 16 ? rows : 16;
+  constexpr int Q = HD / 4;  // float4s of a row
+  for (int e = tid; e < cols * Q; e += 256) {
+    const int c = e / Q, d = (e % Q) * 4;
+    float cm = kFloor, cl = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) cm = fmaxf(cm, s_m[i][c]);
+    const float cqs = s_qs[c];
+    float4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+      cl = fmaf(s_l[i][c], exp2_hw((s_m[i][c] - cm) * cqs), cl);
+      const float4 v = *reinterpret_cast<const float4*>(&s_o[i][c][d]);
+      o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+    }
+    const int j = (row0 + c) / group, h = kvh * group + (row0 + c) % group;
+    const int64_t row = (int64_t(sq.q0) + j) * g.n_q + h;
+    if (pl.count == 1) {
+      attn_store4(g, row * HD + d, o, cl);
+    } else {
+      const int64_t R0 = g.T * g.n_q, at = split * R0 + row;
+      float* po = static_cast<float*>(g.ws);
+      *reinterpret_cast<float4*>(po + at * HD + d) = o;
+      if (d == 0) {
+        float* pm = po + nsplit_max * R0 * HD;
+        pm[at * 2] = cm * cqs;  // in powers of two
+        pm[at * 2 + 1] = cl;
+      }
+    }
+  }
+}
+
+// Joins the splits of one (query, head) row: 4 waves over the splits, lanes over the dims.
+template <int HD>
+__global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs g, int group, int nsplit_max) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int b = blockIdx.z, kvh = blockIdx.y % g.c.n_kv, rt = blockIdx.y / g.c.n_kv, c = blockIdx.x;
+  const AttnSeq sq = attn_seq(g, b);
+  const int row0 = rt * 16, rows = sq.q_len * group - row0;
+  if (c >= rows) return;
+  const AttnSpan sp = attn_span(g, sq, row0 / group, (row0 + (rows < 16 ? rows : 16) - 1) / group);
+  const int count = attn_split(sp, nsplit_max, 0).count;
+  if (count == 1) return;
+  const int j = (row0 + c) / group, h = kvh * group + (row0 + c) % group;
+  const int64_t row = (int64_t(sq.q0) + j) * g.n_q + h, R0 = g.T * g.n_q;
+  const float* po = static_cast<const float*>(g.ws);
+  const float* pm = po + nsplit_max * R0 * HD;
+  float mm = -INFINITY;
+  for (int s = lane; s < count; s += 64) mm = fmaxf(mm, pm[(s * R0 + row) * 2]);
+#pragma unroll
+  for (int o = 32; o; o >>= 1) mm = fmaxf(mm, __shfl_xor(mm, o));
+  constexpr int V = HD / 64;
+  float acc[V], l = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+#pragma unroll 4
+  for (int s = wave; s < count; s += 4) {
+    const int64_t at = s * R0 + row;
+    const float f = exp2_hw(pm[at * 2] - mm);
+    l = fmaf(pm[at * 2 + 1], f, l);
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = fmaf(po[at * HD + lane * V + i], f, acc[i]);
+  }
+  __shared__ float s_a[4][HD], s_l[4];
+#pragma unroll
+  for (int i = 0; i < V; ++i) s_a[wave][lane * V + i] = acc[i];
+  if (lane == 0) s_l[wave] = l;
+  __syncthreads();
+  if (tid < HD / 4) {
+    float4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = *reinterpret_cast<const float4*>(&s_a[i][tid * 4]);
+      o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+    }
+    attn_store4(g, row * HD + tid * 4, o, s_l[0] + s_l[1] + s_l[2] + s_l[3]);
+  }
+}
+
+template <int HD>
+int launch_hd(const Kv4AttnArgs& a, hipStream_t s) {
+  const int group = a.n_q / a.c.n_kv;
+  const int64_t rts = (int64_t(a.max_q) * group + 15) / 16;
+  const int ns = attn_nsplit(a.B, a.max_q, a.n_q, a.c.n_kv, int64_t(a.max_pages) << a.c.page_shift);
+  const dim3 grid(uint32_t(ns), uint32_t(a.c.n_kv * rts), uint32_t(a.B));
+  if (a.c.page_shift >= 5) kv4_decode_kernel<HD, true><<<grid, 256, 0, s>>>(a, group, ns);
+  else kv4_decode_kernel<HD, false><<<grid, 256, 0, s>>>(a, group, ns);
+  if (hipGetLastError() != hipSuccess) return 6;
+  if (ns > 1) {
+    kv4_join_kernel<HD><<<dim3(16, uint32_t(a.c.n_kv * rts), uint32_t(a.B)), 256, 0, s>>>(a, group, ns);
+    if (hipGetLastError() != hipSuccess) return 6;
+  }
+  return 0;
+}
+
+}  // namespace
+
+int attn_nsplit(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t max_kv) {
+  const int64_t rts = (max_q * (n_q / n_kv) + 15) / 16;
+  const int64_t blocks = B * n_kv * rts;
+  const int64_t want = int64_t(device_cus()) * 8;  // blocks of a full launch
+  int64_t ns = (want + blocks - 1) / blocks;
+  const int64_t most = (max_kv + kSplitKeys - 1) / kSplitKeys;
+  if (ns > most) ns = most;
+  if (ns > 256) ns = 256;
+  return ns < 1 ? 1 : int(ns);
+}
+
+int launch_kv4_decode(const Kv4AttnArgs& a, hipStream_t s) {
+  if (a.c.hd == 64) return launch_hd<64>(a, s);
+  if (a.c.hd == 128) return launch_hd<128>(a, s);
+  return launch_hd<256>(a, s);
+}
+
+uint64_t kv4_attn_workspace(int64_t T, int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t hd,
+                            int64_t max_kv) {
+  const uint64_t ns = uint64_t(attn_nsplit(B, max_q, n_q, n_kv, max_kv));
+  return ns > 1 ? ns * uint64_t(T) * uint64_t(n_q) * uint64_t(hd + 2) * 4 : 256;
+}
+
+int launch_kv4_attn(const Kv4AttnArgs& a, hipStream_t s) { return launch_kv4_decode(a, s); }
+
+}  // namespace qmm
