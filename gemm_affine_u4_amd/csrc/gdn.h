@@ -11,6 +11,9 @@ namespace qmm {
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr float kGdnEps = 1e-6f;
+constexpr int kGdnStepLen = 16;  // calls of up to this max_len run token by token
+uint64_t gdn_chunk_workspace(int64_t T, int64_t B, int64_t Hk, int64_t Hv, int64_t Dk);
+int launch_gdn_chunk(const GdnArgs& a, hipStream_t s);
 
 struct GdnSeq {
   int t0, len, slot;

@@ -111,10 +111,11 @@ int launch_step(const GdnArgs& a, hipStream_t s) {
 }  // namespace
 
 uint64_t gdn_workspace(int64_t T, int64_t B, int64_t max_len, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv) {
-  return 256;
+  return max_len <= kGdnStepLen ? 256 : gdn_chunk_workspace(T, B, Hk, Hv, Dk);
 }
 
 int launch_gdn(const GdnArgs& a, hipStream_t s) {
+  if (a.max_len > kGdnStepLen) return launch_gdn_chunk(a, s);
   return a.Dk == 64 ? launch_step<64>(a, s) : launch_step<128>(a, s);
 }
 
