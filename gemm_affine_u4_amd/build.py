@@ -27,6 +27,7 @@ SOURCES = ([("qmm_api.cpp", [], "qmm_api.o"), ("qmm_validate.cpp", [], "qmm_vali
             ("qmm_noalloc.hip", [], "qmm_noalloc.o"), ("gemv_step.hip", [], "gemv_step.o"),
             ("moe_gemm.hip", [], "moe_gemm.o"), ("qmm_mix_api.cpp", [], "qmm_mix_api.o"),
             ("kv4_append.hip", [], "kv4_append.o"), ("kv4_decode.hip", [], "kv4_decode.o"),
+            ("kv4_prefill.hip", [], "kv4_prefill.o"),
             ("gdn.hip", [], "gdn.o"),
             ("gdn_chunk.hip", [], "gdn_chunk.o")]
            + [(src, [f"-DQMM_BITS={b}"], f"{src.split('.')[0]}_b{b}.o") for src in ("gemv_u4.hip", "gemm_u4.hip")

@@ -55,40 +55,43 @@ __device__ __forceinline__ AttnSeq attn_seq(const Kv4AttnArgs& g, int b) {
   return s;
 }
 
-struct AttnSpan {
-  int lo, hi;  // in tiles of 32 keys
+// How a call is cut: a function of its sizes alone (host), the same for its workspace.
+struct AttnPlan {
+  int rows;     // (query, head) rows of a block: 16 (kv4_decode.hip), 128 or 256 (kv4_prefill.hip)
+  int shift;    // log2 of the keys of a tile
+  int nsplit;   // at most this many splits of a block's keys ...
+  int keys;     // ... of at least this many keys
 };
-// Keys that queries j0 .. j1 of a sequence can see.
-__device__ __forceinline__ AttnSpan attn_span(const Kv4AttnArgs& g, const AttnSeq& s, int j0, int j1) {
+AttnPlan attn_plan(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t max_kv);
+
+struct AttnSplit {
+  int count, begin, end;  // splits of the block's keys; this split's tiles
+};
+// The tiles of keys that rows row0 .. row0 + rows - 1 of a sequence can see, cut evenly.
+__device__ __forceinline__ AttnSplit attn_split(const Kv4AttnArgs& g, const AttnSeq& s, int row0, int rows, int group,
+                                                const AttnPlan& p, int split) {
   int64_t lo = 0, hi = s.kv_len;
   if (g.causal) {
-    const int64_t p0 = s.first;
-    hi = p0 + j1 + 1;
-    if (g.window > 0 && p0 + j0 - g.window + 1 > 0) lo = p0 + j0 - g.window + 1;
+    hi = int64_t(s.first) + (row0 + rows - 1) / group + 1;
+    const int64_t w = int64_t(s.first) + row0 / group - g.window + 1;
+    if (g.window > 0 && w > 0) lo = w;
   }
   if (hi < 0) hi = 0;
   if (lo > hi) lo = hi;
-  return {int(lo >> 5), int((hi + 31) >> 5)};
-}
-
-constexpr int kSplitKeys = 128;  // a split has at least this many keys
-struct AttnSplit {
-  int count, begin, end;  // splits of the span; this split's tiles
-};
-__device__ __forceinline__ AttnSplit attn_split(const AttnSpan& sp, int nsplit_max, int split) {
-  const int tiles = sp.hi - sp.lo;
-  int c = (tiles * 32 + kSplitKeys - 1) / kSplitKeys;
-  c = c > nsplit_max ? nsplit_max : c < 1 ? 1 : c;
+  const int t0 = int(lo >> p.shift), t1 = int((hi + (1 << p.shift) - 1) >> p.shift), tiles = t1 - t0;
+  const int least = p.keys >> p.shift;
+  int c = (tiles + least - 1) / least;
+  c = c > p.nsplit ? p.nsplit : c < 1 ? 1 : c;
   const int per = (tiles + c - 1) / c;
-  if (per > 0) c = (tiles + per - 1) / per;
   AttnSplit r;
-  r.count = c < 1 ? 1 : c;
-  r.begin = sp.lo + split * per;
-  r.end = r.begin + per < sp.hi ? r.begin + per : sp.hi;
+  r.count = per > 0 ? (tiles + per - 1) / per : 1;
+  r.begin = t0 + split * per;
+  r.end = r.begin + per < t1 ? r.begin + per : t1;
   return r;
 }
-int attn_nsplit(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t max_kv);
-int launch_kv4_decode(const Kv4AttnArgs& a, hipStream_t s);
+int launch_kv4_decode(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t s);
+int launch_kv4_prefill(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t s);
+int launch_kv4_join(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t s);
 
 // Four neighbouring outputs: the weighted sum over its weight, times the gate's sigmoid.
 __device__ __forceinline__ void attn_store4(const Kv4AttnArgs& g, int64_t at, float4 o, float l) {

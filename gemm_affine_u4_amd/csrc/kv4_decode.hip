@@ -37,6 +37,7 @@ constexpr int kTile = 32;    // keys of a wave's step
 constexpr int kWaves = 4;
 constexpr float kFloor = -1e30f;  // maximum of a row that has seen no key yet
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int64_t kDecodeRows = 64;  // calls of up to this many rows per KV head run here
 
 template <int HD>
 struct Buf {
@@ -81,7 +82,7 @@ __device__ __forceinline__ f16x8_t key_operand(uint32_t w) {
 }
 
 template <int HD, bool PG32>
-__global__ __launch_bounds__(256, 2) void kv4_decode_kernel(Kv4AttnArgs g, int group, int nsplit_max) {
+__global__ __launch_bounds__(256, 2) void kv4_decode_kernel(Kv4AttnArgs g, int group, AttnPlan plan) {
   using B = Buf<HD>;
   constexpr int NG = B::NG, NKL = B::NKL, R = B::R;
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, hg = lane >> 4;
@@ -92,8 +93,7 @@ __global__ __launch_bounds__(256, 2) void kv4_decode_kernel(Kv4AttnArgs g, int g
   const AttnSeq sq = attn_seq(g, b);
   const int row0 = rt * 16, rows = sq.q_len * group - row0;
   if (rows <= 0) return;
-  const AttnSpan sp = attn_span(g, sq, row0 / group, (row0 + (rows < 16 ? rows : 16) - 1) / group);
-  const AttnSplit pl = attn_split(sp, nsplit_max, split);
+  const AttnSplit pl = attn_split(g, sq, row0, rows < 16 ? rows : 16, group, plan, split);
   if (split >= pl.count) return;
 
   // the lane's column: one (query, head) row
@@ -411,7 +411,7 @@ __global__ __launch_bounds__(256, 2) void kv4_decode_kernel(Kv4AttnArgs g, int g
       float* po = static_cast<float*>(g.ws);
       *reinterpret_cast<float4*>(po + at * HD + d) = o;
       if (d == 0) {
-        float* pm = po + nsplit_max * R0 * HD;
+        float* pm = po + plan.nsplit * R0 * HD;
         pm[at * 2] = cm * cqs;  // in powers of two
         pm[at * 2 + 1] = cl;
       }
@@ -421,19 +421,17 @@ __global__ __launch_bounds__(256, 2) void kv4_decode_kernel(Kv4AttnArgs g, int g
 
 // Joins the splits of one (query, head) row: 4 waves over the splits, lanes over the dims.
 template <int HD>
-__global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs g, int group, int nsplit_max) {
+__global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs g, int group, AttnPlan plan) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int b = blockIdx.z, kvh = blockIdx.y % g.c.n_kv, rt = blockIdx.y / g.c.n_kv, c = blockIdx.x;
+  const int b = blockIdx.z, kvh = blockIdx.y, rr = blockIdx.x;
   const AttnSeq sq = attn_seq(g, b);
-  const int row0 = rt * 16, rows = sq.q_len * group - row0;
-  if (c >= rows) return;
-  const AttnSpan sp = attn_span(g, sq, row0 / group, (row0 + (rows < 16 ? rows : 16) - 1) / group);
-  const int count = attn_split(sp, nsplit_max, 0).count;
+  if (rr >= sq.q_len * group) return;
+  const int row0 = rr / plan.rows * plan.rows, rows = sq.q_len * group - row0;
+  const int count = attn_split(g, sq, row0, rows < plan.rows ? rows : plan.rows, group, plan, 0).count;
   if (count == 1) return;
-  const int j = (row0 + c) / group, h = kvh * group + (row0 + c) % group;
-  const int64_t row = (int64_t(sq.q0) + j) * g.n_q + h, R0 = g.T * g.n_q;
+  const int64_t row = (int64_t(sq.q0) + rr / group) * g.n_q + kvh * group + rr % group, R0 = g.T * g.n_q;
   const float* po = static_cast<const float*>(g.ws);
-  const float* pm = po + nsplit_max * R0 * HD;
+  const float* pm = po + plan.nsplit * R0 * HD;
   float mm = -INFINITY;
   for (int s = lane; s < count; s += 64) mm = fmaxf(mm, pm[(s * R0 + row) * 2]);
 #pragma unroll
@@ -467,46 +465,68 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs g, int group,
 }
 
 template <int HD>
-int launch_hd(const Kv4AttnArgs& a, hipStream_t s) {
+int launch_hd(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t s) {
   const int group = a.n_q / a.c.n_kv;
   const int64_t rts = (int64_t(a.max_q) * group + 15) / 16;
-  const int ns = attn_nsplit(a.B, a.max_q, a.n_q, a.c.n_kv, int64_t(a.max_pages) << a.c.page_shift);
-  const dim3 grid(uint32_t(ns), uint32_t(a.c.n_kv * rts), uint32_t(a.B));
-  if (a.c.page_shift >= 5) kv4_decode_kernel<HD, true><<<grid, 256, 0, s>>>(a, group, ns);
-  else kv4_decode_kernel<HD, false><<<grid, 256, 0, s>>>(a, group, ns);
-  if (hipGetLastError() != hipSuccess) return 6;
-  if (ns > 1) {
-    kv4_join_kernel<HD><<<dim3(16, uint32_t(a.c.n_kv * rts), uint32_t(a.B)), 256, 0, s>>>(a, group, ns);
-    if (hipGetLastError() != hipSuccess) return 6;
-  }
-  return 0;
+  const dim3 grid(uint32_t(p.nsplit), uint32_t(a.c.n_kv * rts), uint32_t(a.B));
+  if (a.c.page_shift >= 5) kv4_decode_kernel<HD, true><<<grid, 256, 0, s>>>(a, group, p);
+  else kv4_decode_kernel<HD, false><<<grid, 256, 0, s>>>(a, group, p);
+  return hipGetLastError() == hipSuccess ? 0 : 6;
+}
+
+template <int HD>
+int join_hd(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t s) {
+  const int group = a.n_q / a.c.n_kv;
+  kv4_join_kernel<HD><<<dim3(uint32_t(a.max_q * group), uint32_t(a.c.n_kv), uint32_t(a.B)), 256, 0, s>>>(a, group, p);
+  return hipGetLastError() == hipSuccess ? 0 : 6;
 }
 
 }  // namespace
 
-int attn_nsplit(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t max_kv) {
-  const int64_t rts = (max_q * (n_q / n_kv) + 15) / 16;
-  const int64_t blocks = B * n_kv * rts;
-  const int64_t want = int64_t(device_cus()) * 8;  // blocks of a full launch
+AttnPlan attn_plan(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t max_kv) {
+  const int64_t rows = max_q * (n_q / n_kv), cus = device_cus();
+  AttnPlan p;
+  int64_t want;
+  if (rows <= kDecodeRows) {
+    p.rows = 16, p.shift = 5, p.keys = 128;
+    want = 8 * cus;
+  } else {
+    p.rows = B * n_kv * ((rows + 255) / 256) >= 2 * cus ? 256 : 128;
+    p.shift = 6, p.keys = 512;
+    want = 2 * cus;
+  }
+  const int64_t blocks = B * n_kv * ((rows + p.rows - 1) / p.rows);
   int64_t ns = (want + blocks - 1) / blocks;
-  const int64_t most = (max_kv + kSplitKeys - 1) / kSplitKeys;
-  if (ns > most) ns = most;
-  if (ns > 256) ns = 256;
-  return ns < 1 ? 1 : int(ns);
+  if (rows > kDecodeRows && ns < 2 * want / cus) ns = blocks >= want / 2 ? 1 : ns;
+  const int64_t most = (max_kv + p.keys - 1) / p.keys;
+  ns = ns > most ? most : ns;
+  ns = ns > 256 ? 256 : ns < 1 ? 1 : ns;
+  p.nsplit = int(ns);
+  return p;
 }
 
-int launch_kv4_decode(const Kv4AttnArgs& a, hipStream_t s) {
-  if (a.c.hd == 64) return launch_hd<64>(a, s);
-  if (a.c.hd == 128) return launch_hd<128>(a, s);
-  return launch_hd<256>(a, s);
+int launch_kv4_decode(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t s) {
+  if (a.c.hd == 64) return launch_hd<64>(a, p, s);
+  if (a.c.hd == 128) return launch_hd<128>(a, p, s);
+  return launch_hd<256>(a, p, s);
+}
+
+int launch_kv4_join(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t s) {
+  if (a.c.hd == 64) return join_hd<64>(a, p, s);
+  if (a.c.hd == 128) return join_hd<128>(a, p, s);
+  return join_hd<256>(a, p, s);
 }
 
 uint64_t kv4_attn_workspace(int64_t T, int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t hd,
                             int64_t max_kv) {
-  const uint64_t ns = uint64_t(attn_nsplit(B, max_q, n_q, n_kv, max_kv));
+  const uint64_t ns = uint64_t(attn_plan(B, max_q, n_q, n_kv, max_kv).nsplit);
   return ns > 1 ? ns * uint64_t(T) * uint64_t(n_q) * uint64_t(hd + 2) * 4 : 256;
 }
 
-int launch_kv4_attn(const Kv4AttnArgs& a, hipStream_t s) { return launch_kv4_decode(a, s); }
+int launch_kv4_attn(const Kv4AttnArgs& a, hipStream_t s) {
+  const AttnPlan p = attn_plan(a.B, a.max_q, a.n_q, a.c.n_kv, int64_t(a.max_pages) << a.c.page_shift);
+  const int st = p.rows == 16 ? launch_kv4_decode(a, p, s) : launch_kv4_prefill(a, p, s);
+  return st || p.nsplit == 1 ? st : launch_kv4_join(a, p, s);
+}
 
 }  // namespace qmm
