@@ -57,11 +57,12 @@ __device__ __forceinline__ AttnSeq attn_seq(const Kv4AttnArgs& g, int b) {
 
 // How a call is cut: a function of its sizes alone (host), the same for its workspace.
 struct AttnPlan {
-  int rows;     // (query, head) rows of a block: 16 (kv4_decode.hip), 128 or 256 (kv4_prefill.hip)
+  int rows;     // (query, head) rows of a block: 16 (kv4_decode.hip) or kAttnRows (kv4_prefill.hip)
   int shift;    // log2 of the keys of a tile
   int nsplit;   // at most this many splits of a block's keys ...
   int keys;     // ... of at least this many keys
 };
+constexpr int kAttnRows = 128;
 AttnPlan attn_plan(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t max_kv);
 
 struct AttnSplit {

@@ -491,7 +491,7 @@ AttnPlan attn_plan(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t 
     p.rows = 16, p.shift = 5, p.keys = 128;
     want = 8 * cus;
   } else {
-    p.rows = B * n_kv * ((rows + 255) / 256) >= 2 * cus ? 256 : 128;
+    p.rows = kAttnRows;
     p.shift = 6, p.keys = 512;
     want = 2 * cus;
   }
