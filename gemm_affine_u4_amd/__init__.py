@@ -484,9 +484,26 @@ def qmm_moe_gather_fmt(bits: int, group: int, stage, inp, codes, scales, biases,
 
 # ---- token mixers: the paged 4-bit cache, attention over it, the gated delta rule (qmm_mix.h) ----
 
-class _Kv4Struct(ctypes.Structure):
-    _fields_ = [("k_codes", _P), ("k_meta", _P), ("v_codes", _P), ("v_meta", _P), ("n_pages", _I64),
-                ("page_size", _I64), ("n_kv_heads", _I64), ("head_dim", _I64)]
+MIX_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_qmm_mix.so")
+_MIX = None
+
+
+def _mix():
+    """The mixers' marshalling module (csrc/mix_binding.cpp), over the loaded library."""
+    global _MIX
+    if _MIX is None:
+        import importlib.util
+
+        import torch  # noqa: F401  (the module uses its libraries)
+        if not os.path.exists(MIX_PATH):
+            raise RuntimeError(f"{MIX_PATH} is not built; run `python -m gemm_affine_u4_amd.build`")
+        lib = load_library()
+        spec = importlib.util.spec_from_file_location("_qmm_mix", MIX_PATH)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        mod.bind(*(ctypes.cast(getattr(lib, f), _P).value for f in ("qmm_kv4_append", "qmm_kv4_attn", "qmm_gdn")))
+        _MIX = mod
+    return _MIX
 
 
 def kv4_cache_shapes(n_pages: int, n_kv_heads: int, page_size: int, head_dim: int) -> dict:
@@ -499,26 +516,15 @@ def kv4_cache_shapes(n_pages: int, n_kv_heads: int, page_size: int, head_dim: in
 
 class KV4Cache:
     """qmm_kv4_cache over four device tensors of kv4_cache_shapes(...)."""
+    __slots__ = ("tensors", "_c")
 
     def __init__(self, k_codes, k_meta, v_codes, v_meta):
-        _need(k_codes.dim() == 4 and k_codes.element_size() == 4, "k_codes must be [pages, heads, page_size, head_dim/8] "
-                                                                 "32-bit words")
-        pages, heads, page, words = k_codes.shape
-        want = kv4_cache_shapes(pages, heads, page, words * 8)
-        for name, t, size in (("k_meta", k_meta, 4), ("v_codes", v_codes, 2), ("v_meta", v_meta, 4)):
-            _need(tuple(t.shape) == want[name] and t.element_size() == size,
-                  f"{name} must be {want[name]} of {size}-byte elements")
+        self._c = (_MIX or _mix()).cache(k_codes, k_meta, v_codes, v_meta)
         self.tensors = (k_codes, k_meta, v_codes, v_meta)
-        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = pages, heads, page, words * 8
-        self._c = _Kv4Struct(_ptr(k_codes, "k_codes"), _ptr(k_meta, "k_meta"), _ptr(v_codes, "v_codes"),
-                             _ptr(v_meta, "v_meta"), pages, page, heads, words * 8)
-
-    def _ref(self):
-        return ctypes.addressof(self._c)
 
 
-def _i32(t, n: int, what: str):
-    _need(t.numel() == n and t.element_size() == 4 and not t.is_floating_point(), f"{what} must be int32 [{n}]")
+def _handle(stream):
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 def qmm_kv4_append(cache, k, v, slots, positions=None, cos_sin=None, q=None, q_out=None, k_held=None, v_held=None,
@@ -526,32 +532,9 @@ def qmm_kv4_append(cache, k, v, slots, positions=None, cos_sin=None, q=None, q_o
     """Keys and values k, v [T, n_kv, head_dim] (bf16 or fp32) of new tokens into the cache's slots
     int32 [T]; with cos_sin fp32 [max_pos, rot_dim] and positions int32 [T] keys, and q [T, n_q,
     head_dim] -> q_out (bf16), are rotated first.  k_held, v_held: bf16 copies of what is stored."""
-    hd, n_kv = cache.head_dim, cache.n_kv_heads
-    T = k.shape[0]
-    dt = _out_dtype(k)
-    _need(tuple(k.shape) == (T, n_kv, hd) and tuple(v.shape) == (T, n_kv, hd), "k, v must be [T, n_kv, head_dim]")
-    _need(_out_dtype(v) == dt and (q is None or _out_dtype(q) == dt), "q, k, v must share a dtype")
-    _i32(slots, T, "slots")
-    _need((cos_sin is None) == (positions is None), "positions and cos_sin go together")
-    max_pos = rot = n_q = 0
-    if cos_sin is not None:
-        _i32(positions, T, "positions")
-        _need(cos_sin.dim() == 2 and cos_sin.element_size() == 4, "cos_sin must be fp32 [max_pos, rot_dim]")
-        max_pos, rot = cos_sin.shape
-    _need((q is None) == (q_out is None), "q and q_out go together")
-    if q is not None:
-        _need(q.dim() == 3 and q.shape[0] == T and q.shape[2] == hd, "q must be [T, n_q, head_dim]")
-        n_q = q.shape[1]
-        _need(tuple(q_out.shape) == tuple(q.shape) and _out_dtype(q_out) == QMM_OUT_BF16, "q_out must be bf16, as q")
-    for name, t in (("k_held", k_held), ("v_held", v_held)):
-        _need(t is None or (tuple(t.shape) == (T, n_kv, hd) and _out_dtype(t) == QMM_OUT_BF16),
-              f"{name} must be bf16 [T, n_kv, head_dim]")
-    if T == 0:
-        return
-    _check(load_library().qmm_kv4_append(
-        cache._ref(), _ptr(k, "k"), _ptr(v, "v"), T, dt, _ptr(slots, "slots"), _ptr(positions, "positions"),
-        _ptr(cos_sin, "cos_sin"), max_pos, rot, _ptr(q, "q"), n_q, _ptr(q_out, "q_out"), _ptr(k_held, "k_held"),
-        _ptr(v_held, "v_held"), _stream(stream)), "qmm_kv4_append")
+    st = (_MIX or _mix()).append(cache._c, k, v, slots, positions, cos_sin, q, q_out, k_held, v_held, _handle(stream))
+    if st:
+        raise QmmError(st, "qmm_kv4_append")
 
 
 def qmm_kv4_attn_workspace_bytes(T: int, B: int, max_q: int, n_q: int, n_kv: int, head_dim: int, max_kv: int) -> int:
@@ -564,24 +547,10 @@ def qmm_kv4_attn(q, cache, page_table, kv_lens, out, workspace, q_start=None, ma
     """Attention of q [T, n_q, head_dim] (bf16) over the cache of B sequences: page_table int32
     [B, max_pages], kv_lens int32 [B], q_start int32 [B + 1] (None: one query a sequence); out as q.
     scale: head_dim ** -0.5 unless given; gate (as q): out is multiplied by its sigmoid."""
-    _need(q.dim() == 3 and q.shape[2] == cache.head_dim, "q must be [T, n_q, head_dim]")
-    T, n_q, hd = q.shape
-    _need(page_table.dim() == 2 and page_table.element_size() == 4, "page_table must be int32 [B, max_pages]")
-    B, max_pages = page_table.shape
-    _i32(kv_lens, B, "kv_lens")
-    if q_start is not None:
-        _i32(q_start, B + 1, "q_start")
-    _need(_out_dtype(q) == QMM_OUT_BF16 and _out_dtype(out) == QMM_OUT_BF16 and tuple(out.shape) == tuple(q.shape),
-          "q and out must be bf16 [T, n_q, head_dim]")
-    _need(gate is None or (tuple(gate.shape) == tuple(q.shape) and _out_dtype(gate) == QMM_OUT_BF16),
-          "gate must be bf16, as q")
-    if T == 0:
-        return
-    _check(load_library().qmm_kv4_attn(
-        _ptr(q, "q"), T, _ptr(q_start, "q_start"), _ptr(kv_lens, "kv_lens"), _ptr(page_table, "page_table"), B,
-        max_pages, int(max_q), cache._ref(), n_q, float(hd ** -0.5 if scale is None else scale), int(bool(causal)),
-        int(window), _ptr(gate, "gate"), _ptr(workspace, "workspace"), _bytes(workspace), _ptr(out, "out"),
-        _stream(stream)), "qmm_kv4_attn")
+    st = (_MIX or _mix()).attn(q, cache._c, page_table, kv_lens, out, workspace, q_start, max_q, scale,
+                               1 if causal else 0, window, gate, _handle(stream))
+    if st:
+        raise QmmError(st, "qmm_kv4_attn")
 
 
 def qmm_gdn_workspace_bytes(T: int, B: int, max_len: int, Hk: int, Hv: int, Dk: int, Dv: int) -> int:
@@ -595,29 +564,7 @@ def qmm_gdn(q, k, v, g, beta, state, y, workspace, state_out=None, seq_start=Non
     [T, Hv], state fp32 [slots, Hv, Dv, Dk] (updated in place unless state_out is given), y
     [T, Hv, Dv] bf16 or fp32; seq_start int32 [B + 1] (None: one token a sequence), state_slots
     int32 [B].  scale: Dk ** -0.5 unless given."""
-    import torch
-    _need(q.dim() == 3 and v.dim() == 3, "q, k must be [T, Hk, Dk], v [T, Hv, Dv]")
-    T, Hk, Dk = q.shape
-    Hv, Dv = v.shape[1], v.shape[2]
-    _need(tuple(k.shape) == (T, Hk, Dk) and v.shape[0] == T and tuple(y.shape) == (T, Hv, Dv),
-          "q, k must be [T, Hk, Dk], v and y [T, Hv, Dv]")
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _need(_out_dtype(t) == QMM_OUT_BF16, f"{name} must be bf16")
-    for name, t in (("g", g), ("beta", beta)):
-        _need(tuple(t.shape) == (T, Hv) and t.dtype == torch.float32, f"{name} must be fp32 [T, Hv]")
-    state_out = state if state_out is None else state_out
-    for name, t in (("state", state), ("state_out", state_out)):
-        _need(t.dim() == 4 and tuple(t.shape) == (state.shape[0], Hv, Dv, Dk) and t.dtype == torch.float32,
-              f"{name} must be fp32 [slots, Hv, Dv, Dk]")
-    B = T if seq_start is None else seq_start.numel() - 1
-    if seq_start is not None:
-        _i32(seq_start, B + 1, "seq_start")
-    if state_slots is not None:
-        _i32(state_slots, B, "state_slots")
-    if B == 0 or (T == 0 and state_out is state):
-        return
-    _check(load_library().qmm_gdn(
-        _ptr(q, "q"), _ptr(k, "k"), _ptr(v, "v"), _ptr(g, "g"), _ptr(beta, "beta"), T, _ptr(seq_start, "seq_start"), B,
-        int(max_len), Hk, Hv, Dk, Dv, float(Dk ** -0.5 if scale is None else scale), int(bool(l2norm)),
-        _ptr(state, "state"), _ptr(state_out, "state_out"), _ptr(state_slots, "state_slots"), state.shape[0],
-        _ptr(workspace, "workspace"), _bytes(workspace), _ptr(y, "y"), _out_dtype(y), _stream(stream)), "qmm_gdn")
+    st = (_MIX or _mix()).gdn(q, k, v, g, beta, state, y, workspace, state_out, seq_start, state_slots, max_len, scale,
+                              1 if l2norm else 0, _handle(stream))
+    if st:
+        raise QmmError(st, "qmm_gdn")

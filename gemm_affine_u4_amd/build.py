@@ -18,6 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libqmm.so")
 CEILING_OUT = os.path.join(PKG, "libqmm_ceiling.so")
+BINDING_OUT = os.path.join(PKG, "_qmm_mix.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 # (source, extra flags, object): the GEMV and GEMM sources are built once per code width.
@@ -69,12 +70,45 @@ def _link(objs, out):
     os.replace(tmp, out)
 
 
+def _compile_binding() -> str:
+    """The token mixers' Python side (mix_binding.cpp): host code against torch's headers."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    obj = os.path.join(BUILD_DIR, "mix_binding.o")
+    inc = [INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths("cuda")]
+    cmd = [HIPCC, "-O2", "-std=c++17", "-fPIC", "-x", "c++", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *sum((["-isystem", i] for i in inc), []),
+           "-c", os.path.join(CSRC, "mix_binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compilation failed for mix_binding.cpp:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING_OUT + ".tmp"
+    cmd = [HIPCC, "-shared", "-fPIC", obj, f"-L{lib}", "-lc10", "-lc10_hip", "-ltorch_cpu",
+           "-ltorch_python", "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_OUT)
+
+
 def build(jobs: int = 8) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     with ThreadPoolExecutor(max_workers=jobs) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, SOURCES + [CEILING]))
     _link(objs[:-1], OUT)
     _link(objs[-1:], CEILING_OUT)
+    _link_binding(binding.result())
     return OUT
 
 

@@ -27,11 +27,17 @@ def test_header_functions_are_exported():
     assert set(names) <= set(re.findall(r" T (qmm_\w+)$", out, re.M))
 
 
+class Kv4Struct(ctypes.Structure):
+    """qmm_kv4_cache of the C ABI."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "k_meta", "v_codes", "v_meta")] + [
+        (n, ctypes.c_int64) for n in ("n_pages", "page_size", "n_kv_heads", "head_dim")]
+
+
 def cache(**kw):
     f = dict(k_codes=A, k_meta=A + 64 * MB, v_codes=A + 128 * MB, v_meta=A + 192 * MB, n_pages=8, page_size=32,
              n_kv_heads=2, head_dim=128)
     f.update(kw)
-    return qmm._Kv4Struct(*[f[n] for n, _ in qmm._Kv4Struct._fields_])
+    return Kv4Struct(*[f[n] for n, _ in Kv4Struct._fields_])
 
 
 B0 = A + 256 * MB
