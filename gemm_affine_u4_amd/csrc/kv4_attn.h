@@ -58,6 +58,7 @@ __device__ __forceinline__ AttnSeq attn_seq(const Kv4AttnArgs& g, int b) {
 // How a call is cut: a function of its sizes alone (host), the same for its workspace.
 struct AttnPlan {
   int rows;     // (query, head) rows of a block: 16 (kv4_decode.hip) or kAttnRows (kv4_prefill.hip)
+  int waves;    // of a block
   int shift;    // log2 of the keys of a tile
   int nsplit;   // at most this many splits of a block's keys ...
   int keys;     // ... of at least this many keys

@@ -5,22 +5,26 @@
 // so the codes enter the matrix product exactly and each group's scale and bias are two
 // fp32 multiply-adds on the product.  The output is
 //   sum_t p_t v_t = sum_t (p_t s_t) c_t + sum_t p_t b_t,
-// with p_t s_t rounded to fp16 (relative 2^-12, an eighth of the output's own rounding) and
-// everything else in fp32.  A nibble c masked in place is the fp16 number c 2^-24 (or, in
-// the next four bits, 16 c 2^-24): a subnormal that the matrix cores take exactly, so a code
-// costs half a mask instruction and no conversion; the powers of two go into q (1/16 for the
-// odd places) and into the final factor.
+// with p_t s_t rounded to fp16 (relative 2^-11, an eighth of the output's own rounding) and
+// the weights p in the sums' products likewise; the rest is fp32.  A nibble c masked in place
+// is the fp16 number c 2^-24 (or, in the next four bits, 16 c 2^-24): a subnormal that the
+// matrix cores take exactly, so a code costs half a mask instruction and no conversion; the
+// powers of two go into q (1/16 for the odd places) and into the final factor.
+//
+// Measured: 64 sequences of 100 to 16000 keys, 24/8 heads x 128: 136 us, 5.1 TB/s of cache;
+// one of 131071 keys, 40/4 heads x 256: 34 us, 4.4 TB/s; one of 517 keys: 8.0 us.
 //
 // Bound: the cache's bytes (HBM) for long contexts, launch and latency for short ones.
 //
-// Split.  A block of 4 waves takes one KV head's up to 16 (query, head) rows and a range of
+// Split.  A block of 4 or 8 waves takes one KV head's up to 16 (query, head) rows and a range of
 // keys; its waves take 32 keys at a time and keep an online softmax of their own (maximum,
 // sum and output in registers, no barrier), joined once at the end.  Keys are the rows of
 // the first product (S^T = K Q^T) and dims the rows of the second (O^T = V^T P^T), so a lane
 // that gets the scores of keys 8h .. 8h+7 of its column holds exactly the probabilities
 // that the second product wants from it: nothing crosses lanes between the two.  A lane's
-// share of the scales is one word per group pair, read once and broadcast along the row by
-// the multiply-add itself (DPP row_newbcast).
+// share of the scales is one word per group pair, read once and broadcast along the row
+// (DPP row_newbcast).  Sums of weights and of weights times biases, and of biases times query
+// sums, are products of their own with the matrix cores.
 #include <hip/hip_runtime.h>
 
 #include <utility>
@@ -33,8 +37,7 @@
 namespace qmm {
 namespace {
 
-constexpr int kTile = 32;    // keys of a wave's step
-constexpr int kWaves = 4;
+constexpr int kTile = 32;  // keys of a wave's step
 constexpr float kFloor = -1e30f;  // maximum of a row that has seen no key yet
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int64_t kDecodeRows = 64;  // calls of up to this many rows per KV head run here
@@ -44,20 +47,25 @@ struct Buf {
   static constexpr int NG = HD / 64, NKL = HD == 256 ? 2 : 1, R = NG > 1 ? NG / 2 : 1;
   u32x4_t k[2][NKL];  // key codes of the two 16-key tiles
   u32x4_t v[NG];      // value codes: 8 keys x 4 dims of each group
+  uint32_t kb[2][NG];  // the scales of the lane's two rows of the first product (their biases)
   uint32_t km[R], vm[R];
 };
 
 // Lane (of its row of 16) and register that hold the meta word of key tk (0..7), group g.
 template <int NG>
-constexpr int meta_lane(int tk, int g) { return NG == 1 ? tk : (tk * NG + g) / (NG / 2); }
+constexpr int meta_lane(int tk, int g) { return (tk * NG + g) / (NG > 1 ? NG / 2 : 1); }
 template <int NG>
-constexpr int meta_reg(int tk, int g) { return NG == 1 ? 0 : (tk * NG + g) % (NG / 2); }
+constexpr int meta_reg(int tk, int g) { return (tk * NG + g) % (NG > 1 ? NG / 2 : 1); }
 
 __device__ __forceinline__ float half_lo(uint32_t w) {
   return float(__builtin_bit_cast(_Float16, uint16_t(w)));
 }
-__device__ __forceinline__ float half_hi(uint32_t w) {
-  return float(__builtin_bit_cast(_Float16, uint16_t(w >> 16)));
+
+// x of the lane N places on in the row of 16 (DPP row_shl; zero past its end).
+template <int N>
+__device__ __forceinline__ uint32_t row_next(uint32_t x) {
+  if constexpr (N == 0) return x;
+  else return uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x100 + N, 0xf, 0xf, true));
 }
 
 // The four operands (dims 4n + 0..3 of the 16 rows n) of 8 keys' value codes, and the
@@ -80,9 +88,12 @@ __device__ __forceinline__ f16x8_t key_operand(uint32_t w) {
   r[3] = x & 0x00F000F0u;
   return __builtin_bit_cast(f16x8_t, r);
 }
+__device__ __forceinline__ f32x4_t mma16(f16x8_t a, f16x8_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
 
-template <int HD, bool PG32>
-__global__ __launch_bounds__(256, 2) void kv4_decode_kernel(Kv4AttnArgs g, int group, AttnPlan plan) {
+template <int HD, bool PG32, int NW>
+__global__ __launch_bounds__(NW * 64, 2) void kv4_decode_kernel(Kv4AttnArgs g, int group, AttnPlan plan) {
   using B = Buf<HD>;
   constexpr int NG = B::NG, NKL = B::NKL, R = B::R;
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, hg = lane >> 4;
@@ -96,6 +107,94 @@ __global__ __launch_bounds__(256, 2) void kv4_decode_kernel(Kv4AttnArgs g, int g
   const AttnSplit pl = attn_split(g, sq, row0, rows < 16 ? rows : 16, group, plan, split);
   if (split >= pl.count) return;
 
+  // Pages, a window of 64 of the wave's tiles at a time: lane i holds the page of its i-th
+  // tile from the window's first on (and of its second half, where pages are of 16).
+  const int psh = g.c.page_shift, pmask = (1 << psh) - 1;
+  const int32_t* __restrict__ table = g.table + int64_t(b) * g.max_pages;
+  const int last_key = sq.kv_len > 0 ? sq.kv_len - 1 : 0;
+  constexpr int kStride = NW * kTile;
+  const int t_end = pl.end * kTile;
+  int t = (pl.begin + wave) * kTile, window = t;
+  int pages0 = 0, pages1 = 0;          // 0 where there is no page,
+  uint64_t there0 = 0, there1 = 0;     // its bit clear then
+  auto enter = [&](int t0) {
+    window = t0;
+    const int k = t0 + lane * kStride;
+    // checked here, so that the wait for the entries stays in this rare branch
+    const int id0 = table[(k < last_key ? k : last_key) >> psh];
+    there0 = __ballot(uint32_t(id0) < uint32_t(g.c.n_pages));
+    pages0 = uint32_t(id0) < uint32_t(g.c.n_pages) ? id0 : 0;
+    if constexpr (!PG32) {
+      const int id1 = table[(k + 16 < last_key ? k + 16 : last_key) >> psh];
+      there1 = __ballot(uint32_t(id1) < uint32_t(g.c.n_pages));
+      pages1 = uint32_t(id1) < uint32_t(g.c.n_pages) ? id1 : 0;
+    }
+  };
+  enter(t);
+
+  // rows (token slots of this head) of the tile's two halves, and whether their page exists
+  struct Where {
+    int64_t r0, r1;
+    bool ok0, ok1;
+  };
+  auto where = [&](int t0) {
+    Where w;
+    const int i = (t0 - window) / kStride;
+    w.ok0 = (there0 >> i) & 1;
+    w.r0 = ((int64_t(__builtin_amdgcn_readlane(pages0, i)) * g.c.n_kv + kvh) << psh) + (t0 & pmask);
+    if constexpr (PG32) {
+      w.ok1 = w.ok0;
+      w.r1 = w.r0 + 16;
+    } else {
+      w.ok1 = (there1 >> i) & 1;
+      w.r1 = ((int64_t(__builtin_amdgcn_readlane(pages1, i)) * g.c.n_kv + kvh) << psh) + ((t0 + 16) & pmask);
+    }
+    return w;
+  };
+  const int krow = 8 * ((n >> 2) & 1) + (n & 3);  // + 4u: the lane's key within its half (n / 8)
+  auto load = [&](const Where& w, B& x) {
+    const int64_t rk = PG32 ? w.r0 + 8 * (n >> 2) + (n & 3) : (n < 8 ? w.r0 : w.r1) + krow;
+    const int64_t rv = PG32 ? w.r0 + 8 * hg : (hg < 2 ? w.r0 : w.r1) + 8 * (hg & 1);
+    const uint32_t* kp = g.c.k_codes + rk * (HD / 8);
+    const uint32_t* kb = g.c.k_meta + rk * NG;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int p = 0; p < NKL; ++p) {
+        if constexpr (HD == 64) {
+          const uint2 v = *reinterpret_cast<const uint2*>(kp + 4 * u * (HD / 8) + 2 * hg);
+          x.k[u][p] = u32x4_t{v.x, v.y, 0, 0};
+        } else {
+          x.k[u][p] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(kp + 4 * u * (HD / 8) + 16 * p + 4 * hg));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NG; ++i) x.kb[u][i] = kb[4 * u * NG + i];
+    }
+    const int moff = NG == 1 ? (n & 7) : n * R;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      x.km[i] = g.c.k_meta[rv * NG + moff + i];
+      x.vm[i] = g.c.v_meta[rv * NG + moff + i];
+    }
+    const uint16_t* vp = g.c.v_codes + (rv >> 3) * (HD * 2) + n * 8;
+#pragma unroll
+    for (int i = 0; i < NG; ++i) x.v[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(vp + i * 128));
+  };
+
+  // Behind its last tile a wave loads that one again: were the loads conditional, the wait for
+  // a tile's own would have to wait for the next one's too.
+  const int t_last = t + (t < t_end ? (t_end - 1 - t) / kStride * kStride : 0);
+  auto ahead = [&](int t0, Where& w, B& x) {
+    const int tc = t0 < t_last ? t0 : t_last;
+    if (tc - window >= 64 * kStride) enter(tc);
+    w = where(tc);
+    load(w, x);
+  };
+  B x0, x1;
+  Where w0, w1;
+  ahead(t, w0, x0);  // under way while the queries are laid out
+
   // the lane's column: one (query, head) row
   const bool col_ok = n < rows;
   const int cj = (row0 + n) / group, ch = kvh * group + (row0 + n) % group;
@@ -108,11 +207,12 @@ __global__ __launch_bounds__(256, 2) void kv4_decode_kernel(Kv4AttnArgs g, int g
   }
 
   // q as operands: fp16 scaled by a power of two so that the row's largest is in
-  // [2^14, 2^15) (bf16 values stay exact), odd places by 1/16 more
-  f16x8_t qf[NG][2];
-  float qs, xs[NG];
+  // [2^14, 2^15) (bf16 values stay exact), odd places by 1/16 more; and the groups' sums, in
+  // two fp16 pieces, against the biases
+  f16x8_t qf[NG][2], xf;
+  float qs;
   {
-    float x[NG][2][8], mx = 0.f;
+    float x[NG][2][8], xs[NG], mx = 0.f;
 #pragma unroll
     for (int e = 0; e < NG * 2; ++e) {
       const int p = HD == 64 ? 0 : e / 4, j = HD == 64 ? e : e % 4;
@@ -140,16 +240,21 @@ __global__ __launch_bounds__(256, 2) void kv4_decode_kernel(Kv4AttnArgs g, int g
     const int sh = 14 - ex;  // in [-113, 141]
     qs = g.scale * kLog2e * ldexpf(1.f, 24 - sh);
 #pragma unroll
+    for (int i = 0; i < 8; ++i) xf[i] = static_cast<_Float16>(0.f);
+#pragma unroll
     for (int i = 0; i < NG; ++i) {
-      xs[i] = ldexpf(xs[i], sh - 24);
+      // the products' k places i and NG + i of the first lane group
+      const float y = hg == 0 ? ldexpf(xs[i], sh - 24) : 0.f;
+      xf[i] = static_cast<_Float16>(y);
+      xf[NG + i] = static_cast<_Float16>(y - static_cast<float>(xf[i]));
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         // operand order: nibbles (0, 4), (1, 5), (2, 6), (3, 7)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int down = (t & 1) ? sh - 4 : sh;
-          qf[i][j][2 * t] = static_cast<_Float16>(ldexpf(x[i][j][t], down));
-          qf[i][j][2 * t + 1] = static_cast<_Float16>(ldexpf(x[i][j][t + 4], down));
+        for (int e = 0; e < 4; ++e) {
+          const int down = (e & 1) ? sh - 4 : sh;
+          qf[i][j][2 * e] = static_cast<_Float16>(ldexpf(x[i][j][e], down));
+          qf[i][j][2 * e + 1] = static_cast<_Float16>(ldexpf(x[i][j][e + 4], down));
         }
       }
     }
@@ -165,100 +270,70 @@ __global__ __launch_bounds__(256, 2) void kv4_decode_kernel(Kv4AttnArgs g, int g
   u_lo = __builtin_amdgcn_readfirstlane(u_lo);
   u_hi = __builtin_amdgcn_readfirstlane(u_hi);
 
-  const int psh = g.c.page_shift, pmask = (1 << psh) - 1;
-  const int32_t* __restrict__ table = g.table + int64_t(b) * g.max_pages;
-  const int last_entry = sq.kv_len > 0 ? (sq.kv_len - 1) >> psh : 0;
-
-  // rows (token slots of this head) of the tile's two halves, and whether their page exists
-  struct Where {
-    int64_t r0, r1;
-    bool ok0, ok1;
-  };
-  auto where = [&](int t0) {
-    Where w;
-    const int e0 = t0 >> psh;
-    const int id0 = table[e0 < last_entry ? e0 : last_entry];
-    w.ok0 = uint32_t(id0) < uint32_t(g.c.n_pages);
-    w.r0 = ((int64_t(w.ok0 ? id0 : 0) * g.c.n_kv + kvh) << psh) + (t0 & pmask);
-    if constexpr (PG32) {
-      w.ok1 = w.ok0;
-      w.r1 = w.r0 + 16;
-    } else {
-      const int e1 = (t0 + 16) >> psh;
-      const int id1 = table[e1 < last_entry ? e1 : last_entry];
-      w.ok1 = e1 <= last_entry && uint32_t(id1) < uint32_t(g.c.n_pages);
-      w.r1 = ((int64_t(w.ok1 ? id1 : 0) * g.c.n_kv + kvh) << psh) + ((t0 + 16) & pmask);
-    }
-    return w;
-  };
-  const int krow = 8 * ((n >> 2) & 1) + (n & 3);  // + 4u: the lane's key within its half (n / 8)
-  auto load = [&](const Where& w, B& x) {
-    const int64_t rk = PG32 ? w.r0 + 8 * (n >> 2) + (n & 3) : (n < 8 ? w.r0 : w.r1) + krow;
-    const int64_t rv = PG32 ? w.r0 + 8 * hg : (hg < 2 ? w.r0 : w.r1) + 8 * (hg & 1);
-    const uint32_t* kp = g.c.k_codes + rk * (HD / 8);
+  // output, and in a lane's rows of two more products: the weights' sum, and (rows 0, 1 of
+  // bacc[i], lane group 0) sums of weight times bias of group i, R + i
+  f32x4_t acc[NG][4], bacc[R], lacc = {0.f, 0.f, 0.f, 0.f};
+  float m = kFloor;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-#pragma unroll
-      for (int p = 0; p < NKL; ++p) {
-        if constexpr (HD == 64) {
-          const uint2 v = *reinterpret_cast<const uint2*>(kp + 4 * u * (HD / 8) + 2 * hg);
-          x.k[u][p] = u32x4_t{v.x, v.y, 0, 0};
-        } else {
-          x.k[u][p] = *reinterpret_cast<const u32x4_t*>(kp + 4 * u * (HD / 8) + 16 * p + 4 * hg);
-        }
-      }
-    }
-    const int moff = NG == 1 ? (n & 7) : n * R;
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      x.km[i] = g.c.k_meta[rv * NG + moff + i];
-      x.vm[i] = g.c.v_meta[rv * NG + moff + i];
-    }
-    const uint16_t* vp = g.c.v_codes + (rv >> 3) * (HD * 2) + n * 8;
-#pragma unroll
-    for (int i = 0; i < NG; ++i) x.v[i] = *reinterpret_cast<const u32x4_t*>(vp + i * 128);
-  };
-
-  f32x4_t acc[NG][4];
-  float bacc[NG], m = kFloor, l = 0.f;
+  for (int i = 0; i < R; ++i) bacc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < NG; ++i) {
-    bacc[i] = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
+  f16x8_t ones;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) ones[i] = static_cast<_Float16>(1.f);
 
   auto step = [&](const B& x, int t0, const Where& w) {
-    float sk[R], bk[R], sv[R], bv[R];
+    const bool masked = t0 < u_lo || t0 + kTile > u_hi || !w.ok0 || !w.ok1;
+    float sk[R], sv[R];
+    uint32_t vm[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      sk[i] = half_lo(x.km[i]), bk[i] = half_hi(x.km[i]);
-      sv[i] = half_lo(x.vm[i]), bv[i] = half_hi(x.vm[i]);
+      sk[i] = half_lo(x.km[i]);
+      vm[i] = x.vm[i];
+      // keys that are not there may have any scale, NaN among them
+      if (masked) {
+        const int tk = t0 + 8 * hg + (NG == 1 ? (n & 7) : n * R / NG);
+        vm[i] = (hg < 2 ? w.ok0 : w.ok1) && tk < sq.kv_len ? vm[i] : 0u;
+      }
+      sv[i] = half_lo(vm[i]);
     }
     float sc[8];
     static_for<2>([&](auto uc) {
       constexpr int u = decltype(uc)::value;
+      // sum_g b_g sum(q_g): biases in k places g and NG + g
+      u32x4_t bw = {0, 0, 0, 0};
+      if constexpr (NG == 1) {
+        bw[0] = __builtin_amdgcn_perm(x.kb[u][0], x.kb[u][0], 0x07060706u);
+      } else if constexpr (NG == 2) {
+        bw[0] = bw[1] = __builtin_amdgcn_perm(x.kb[u][1], x.kb[u][0], 0x07060302u);
+      } else {
+        bw[0] = bw[2] = __builtin_amdgcn_perm(x.kb[u][1], x.kb[u][0], 0x07060302u);
+        bw[1] = bw[3] = __builtin_amdgcn_perm(x.kb[u][NG - 1], x.kb[u][NG - 2], 0x07060302u);
+      }
+      const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+      const f32x4_t bias = mma16(__builtin_bit_cast(f16x8_t, bw), xf, zero);
       f32x4_t d[NG];
 #pragma unroll
-      for (int i = 0; i < NG; ++i) d[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < NG; ++i) d[i] = zero;
 #pragma unroll
       for (int e = 0; e < NG * 2; ++e) {
         const int p = HD == 64 ? 0 : e / 4, j = HD == 64 ? e : e % 4;
         const int gi = HD == 64 ? 0 : 2 * p + (j >> 1);
-        d[gi] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_operand(x.k[u][p][j]), qf[gi][j & 1], d[gi], 0, 0, 0);
+        d[gi] = mma16(key_operand(x.k[u][p][j]), qf[gi][j & 1], d[gi]);
       }
       static_for<4>([&](auto ic) {
         constexpr int i = decltype(ic)::value, tk = 4 * u + i;
-        float s = 0.f;
+        float s = bias[i];
         static_for<NG>([&](auto gc) {
-          constexpr int gi = decltype(gc)::value, ln = meta_lane<NG>(tk, gi), rg = meta_reg<NG>(tk, gi);
-          s = fmaf(row_bcast<ln>(sk[rg]), d[gi][i], s);
-          s = fmaf(row_bcast<ln>(bk[rg]), xs[gi], s);
+          constexpr int gi = decltype(gc)::value;
+          s = fmaf(row_bcast<meta_lane<NG>(tk, gi)>(sk[meta_reg<NG>(tk, gi)]), d[gi][i], s);
         });
         sc[tk] = s;
       });
     });
-    const bool masked = t0 < u_lo || t0 + kTile > u_hi || !w.ok0 || !w.ok1;
     uint32_t vis = 0xFF;
     if (masked) {
       const int tb = t0 + 8 * hg;
@@ -278,10 +353,11 @@ __global__ __launch_bounds__(256, 2) void kv4_decode_kernel(Kv4AttnArgs g, int g
       const float mn = fmaxf(m, mx);
       const float fac = exp2_hw((m - mn) * qs);
       m = mn;
-      l *= fac;
+      lacc *= fac;
+#pragma unroll
+      for (int i = 0; i < R; ++i) bacc[i] *= fac;
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
-        bacc[i] *= fac;
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] *= fac;
       }
@@ -291,77 +367,60 @@ __global__ __launch_bounds__(256, 2) void kv4_decode_kernel(Kv4AttnArgs g, int g
     float p[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) p[i] = exp2_hw(fmaf(sc[i], qs, off));
-    f16x8_t ps[NG];
-    if (!masked) {
-      static_for<8>([&](auto ic) {
-        constexpr int i = decltype(ic)::value;
-        l += p[i];
-        static_for<NG>([&](auto gc) {
-          constexpr int gi = decltype(gc)::value, ln = meta_lane<NG>(i, gi), rg = meta_reg<NG>(i, gi);
-          ps[gi][i] = static_cast<_Float16>(p[i] * row_bcast<ln>(sv[rg]));
-          bacc[gi] = fmaf(row_bcast<ln>(bv[rg]), p[i], bacc[gi]);
-        });
-      });
-    } else {  // hidden keys may hold anything, NaN scales among it
-      static_for<8>([&](auto ic) {
-        constexpr int i = decltype(ic)::value;
-        const bool see = (vis >> i) & 1;
-        const float pi = see ? p[i] : 0.f;
-        l += pi;
-        static_for<NG>([&](auto gc) {
-          constexpr int gi = decltype(gc)::value, ln = meta_lane<NG>(i, gi), rg = meta_reg<NG>(i, gi);
-          const float s1 = row_bcast<ln>(sv[rg]), b1 = row_bcast<ln>(bv[rg]);
-          ps[gi][i] = static_cast<_Float16>(see ? pi * s1 : 0.f);
-          bacc[gi] += see ? pi * b1 : 0.f;
-        });
-      });
+    if (masked) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] = (vis >> i) & 1 ? p[i] : 0.f;
     }
+    f16x8_t ps[NG], pf;
+    static_for<8>([&](auto ic) {
+      constexpr int i = decltype(ic)::value;
+      pf[i] = static_cast<_Float16>(p[i]);
+      static_for<NG>([&](auto gc) {
+        constexpr int gi = decltype(gc)::value;
+        ps[gi][i] = static_cast<_Float16>(p[i] * row_bcast<meta_lane<NG>(i, gi)>(sv[meta_reg<NG>(i, gi)]));
+      });
+    });
+    lacc = mma16(ones, pf, lacc);
+    // biases: row n of the operand from the lanes n, n + 16 / 8, .. that hold its group's keys
+    constexpr int kHop = NG == 1 ? 1 : 2;
+    static_for<R>([&](auto rc) {
+      constexpr int r = decltype(rc)::value;
+      u32x4_t bw;
+      static_for<4>([&](auto ic) {
+        constexpr int i = decltype(ic)::value;
+        bw[i] = __builtin_amdgcn_perm(row_next<(2 * i + 1) * kHop>(vm[r]), row_next<2 * i * kHop>(vm[r]), 0x07060302u);
+      });
+      bacc[r] = mma16(__builtin_bit_cast(f16x8_t, bw), pf, bacc[r]);
+    });
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(nib_operand(x.v[i], j), ps[i], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < 4; ++j) acc[i][j] = mma16(nib_operand(x.v[i], j), ps[i], acc[i][j]);
     }
   };
 
   // the wave's tiles, the next one's loads under way while one is computed
-  int t = (pl.begin + wave) * kTile;
-  const int t_end = pl.end * kTile;
   if (t < t_end) {
-    B x0, x1;
-    Where w0 = where(t), w1;
-    load(w0, x0);
     for (;;) {
-      const int t1 = t + kWaves * kTile;
-      const bool more = t1 < t_end;
-      if (more) {
-        w1 = where(t1);
-        load(w1, x1);
-      }
+      ahead(t + kStride, w1, x1);
       step(x0, t, w0);
-      if (!more) break;
-      const int t2 = t1 + kWaves * kTile;
-      const bool more2 = t2 < t_end;
-      if (more2) {
-        w0 = where(t2);
-        load(w0, x0);
-      }
-      step(x1, t1, w1);
-      if (!more2) break;
-      t = t2;
+      if ((t += kStride) > t_last) break;
+      ahead(t + kStride, w0, x0);
+      step(x1, t, w1);
+      if ((t += kStride) > t_last) break;
     }
   }
 
-  // join the waves
-  l += __shfl_xor(l, 16);
-  l += __shfl_xor(l, 32);
+  // join the waves.  Rows 0 and 1 of bacc are in lane group 0: group i's sum for the column
+  const float l = lacc[0];
+  float bias[NG];
 #pragma unroll
   for (int i = 0; i < NG; ++i) {
-    bacc[i] += __shfl_xor(bacc[i], 16);
-    bacc[i] += __shfl_xor(bacc[i], 32);
+    // group i: register i % R, row i / R of the operand
+    bias[i] = __shfl(bacc[i % R][NG == 1 ? 0 : i / R], n);
   }
-  __shared__ float s_o[kWaves][16][HD];
-  __shared__ float s_m[kWaves][16], s_l[kWaves][16], s_qs[16];
+  __shared__ float s_o[NW][16][HD];
+  __shared__ float s_m[NW][16], s_l[NW][16], s_qs[16];
   if (hg == 0) {
     s_m[wave][n] = m;
     s_l[wave][n] = l;
@@ -370,7 +429,7 @@ __global__ __launch_bounds__(256, 2) void kv4_decode_kernel(Kv4AttnArgs g, int g
   __syncthreads();
   float mm = kFloor;
 #pragma unroll
-  for (int i = 0; i < kWaves; ++i) mm = fmaxf(mm, s_m[i][n]);
+  for (int i = 0; i < NW; ++i) mm = fmaxf(mm, s_m[i][n]);
   if (col_ok) {
     const float fac = exp2_hw((m - mm) * qs);
 #pragma unroll
@@ -378,10 +437,10 @@ __global__ __launch_bounds__(256, 2) void kv4_decode_kernel(Kv4AttnArgs g, int g
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         float4 o;
-        o.x = fmaf(acc[i][0][r], 16777216.f, bacc[i]) * fac;
-        o.y = fmaf(acc[i][1][r], 1048576.f, bacc[i]) * fac;
-        o.z = fmaf(acc[i][2][r], 16777216.f, bacc[i]) * fac;
-        o.w = fmaf(acc[i][3][r], 1048576.f, bacc[i]) * fac;
+        o.x = fmaf(acc[i][0][r], 16777216.f, bias[i]) * fac;
+        o.y = fmaf(acc[i][1][r], 1048576.f, bias[i]) * fac;
+        o.z = fmaf(acc[i][2][r], 16777216.f, bias[i]) * fac;
+        o.w = fmaf(acc[i][3][r], 1048576.f, bias[i]) * fac;
         *reinterpret_cast<float4*>(&s_o[wave][n][64 * i + 16 * hg + 4 * r]) = o;
       }
     }
@@ -389,15 +448,15 @@ __global__ __launch_bounds__(256, 2) void kv4_decode_kernel(Kv4AttnArgs g, int g
   __syncthreads();
   const int cols = rows < 16 ? rows : 16;
   constexpr int Q = HD / 4;  // float4s of a row
-  for (int e = tid; e < cols * Q; e += 256) {
+  for (int e = tid; e < cols * Q; e += NW * 64) {
     const int c = e / Q, d = (e % Q) * 4;
     float cm = kFloor, cl = 0.f;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) cm = fmaxf(cm, s_m[i][c]);
+    for (int i = 0; i < NW; ++i) cm = fmaxf(cm, s_m[i][c]);
     const float cqs = s_qs[c];
     float4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
+    for (int i = 0; i < NW; ++i) {
       cl = fmaf(s_l[i][c], exp2_hw((s_m[i][c] - cm) * cqs), cl);
       const float4 v = *reinterpret_cast<const float4*>(&s_o[i][c][d]);
       o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
@@ -469,8 +528,13 @@ int launch_hd(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t s) {
   const int group = a.n_q / a.c.n_kv;
   const int64_t rts = (int64_t(a.max_q) * group + 15) / 16;
   const dim3 grid(uint32_t(p.nsplit), uint32_t(a.c.n_kv * rts), uint32_t(a.B));
-  if (a.c.page_shift >= 5) kv4_decode_kernel<HD, true><<<grid, 256, 0, s>>>(a, group, p);
-  else kv4_decode_kernel<HD, false><<<grid, 256, 0, s>>>(a, group, p);
+  if (p.waves == 8) {
+    if (a.c.page_shift >= 5) kv4_decode_kernel<HD, true, 8><<<grid, 512, 0, s>>>(a, group, p);
+    else kv4_decode_kernel<HD, false, 8><<<grid, 512, 0, s>>>(a, group, p);
+  } else {
+    if (a.c.page_shift >= 5) kv4_decode_kernel<HD, true, 4><<<grid, 256, 0, s>>>(a, group, p);
+    else kv4_decode_kernel<HD, false, 4><<<grid, 256, 0, s>>>(a, group, p);
+  }
   return hipGetLastError() == hipSuccess ? 0 : 6;
 }
 
@@ -483,25 +547,31 @@ int join_hd(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t s) {
 
 }  // namespace
 
+// Few queries: splits of at least 1024 keys (none up to 2048), one block per compute unit for few
+// long sequences (131071 keys x 4 heads: 64 splits 36 us, 128 splits 40 us: a block's fixed
+// part is ~6 us), and up to 4 for many, whose lengths may differ (64 sequences of 100 to
+// 16000 keys x 8 heads: 141 us in 4, 156 us in 2).  8 waves a block where that leaves half of
+// the units idle (517 keys x 8 heads: 8.3 against 8.8 us).
+// Prompts: splits only where the blocks would not fill half of the GPU.
 AttnPlan attn_plan(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t max_kv) {
   const int64_t rows = max_q * (n_q / n_kv), cus = device_cus();
   AttnPlan p;
-  int64_t want;
-  if (rows <= kDecodeRows) {
-    p.rows = 16, p.shift = 5, p.keys = 128;
-    want = 8 * cus;
-  } else {
-    p.rows = kAttnRows;
-    p.shift = 6, p.keys = 512;
-    want = 2 * cus;
-  }
+  p.rows = rows <= kDecodeRows ? 16 : kAttnRows;
   const int64_t blocks = B * n_kv * ((rows + p.rows - 1) / p.rows);
-  int64_t ns = (want + blocks - 1) / blocks;
-  if (rows > kDecodeRows && ns < 2 * want / cus) ns = blocks >= want / 2 ? 1 : ns;
+  int64_t ns;
+  if (p.rows == 16) {
+    p.shift = 5, p.keys = 1024;
+    ns = 8 * cus / blocks < 4 ? 8 * cus / blocks : 4;
+    if (ns < cus / blocks) ns = cus / blocks;
+    if (max_kv <= 2 * p.keys) ns = 1;
+  } else {
+    p.shift = 6, p.keys = 512;
+    ns = blocks >= cus ? 1 : (2 * cus + blocks - 1) / blocks;
+  }
   const int64_t most = (max_kv + p.keys - 1) / p.keys;
   ns = ns > most ? most : ns;
-  ns = ns > 256 ? 256 : ns < 1 ? 1 : ns;
-  p.nsplit = int(ns);
+  p.nsplit = int(ns > 256 ? 256 : ns < 1 ? 1 : ns);
+  p.waves = p.rows == 16 && blocks * p.nsplit <= cus / 2 ? 8 : 4;
   return p;
 }
 
