@@ -38,8 +38,11 @@ constexpr int kTri = 6;                        // (w, s) pairs
 __host__ __device__ constexpr int tri_at(int w, int s) { return w < 2 ? w : 2 * w - 2 + s; }
 constexpr int64_t kFragM = 0, kFragA = kTri * 3 * 1024, kFactors = 2 * kTri * 3 * 1024;
 constexpr int64_t kHeadBytes = kFactors + C * 16;
-// Workspace of one (chunk, key head): K^T, dim tiles x 2 token halves.
-constexpr int64_t key_bytes(int64_t dk) { return dk / 16 * 2 * 1024; }
+// Workspace of one (chunk, key head): K^T (dim tiles x 2 token halves), K and Q (quarters of
+// the dims x row tiles), each as a wave of the walk loads it: read by rows, the 16 lanes of a
+// load's quarter would touch 16 cache lines.
+__host__ __device__ constexpr int64_t part_bytes(int64_t dk) { return dk * C * 2; }
+__host__ __device__ constexpr int64_t key_bytes(int64_t dk) { return 3 * part_bytes(dk); }
 
 __device__ __forceinline__ bf16x8_t frag8(const u32x4_t& v) { return __builtin_bit_cast(bf16x8_t, v); }
 __device__ __forceinline__ f32x4_t mma(const u32x4_t& a, const u32x4_t& b, f32x4_t c) {
@@ -63,6 +66,7 @@ template <int DK>
 __global__ __launch_bounds__(256) void gdn_prep_kernel(GdnArgs g, int64_t n_slots_ws) {
   constexpr int KS = DK + 8;   // LDS row of keys, in bf16: 16-byte reads of 16 rows meet no bank twice
   constexpr int FS = C + 4;    // LDS row of a 64 x 64 fp32 matrix
+  constexpr int DT = DK / 64;  // dim tiles of a wave of the walk
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, hg = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = blockIdx.x, hv = blockIdx.y, b = blockIdx.z, rep = g.Hv / g.Hk, hk = hv / rep;
@@ -129,14 +133,27 @@ __global__ __launch_bounds__(256) void gdn_prep_kernel(GdnArgs g, int64_t n_slot
     unsigned char* kt = ws + n_slots_ws * g.Hv * kHeadBytes + (slot * g.Hk + hk) * key_bytes(DK);
 #pragma unroll
     for (int f = 0; f < DK / 16 * 2 / 4; ++f) {
-      const int fr = f * 4 + w, dt = fr >> 1, s = fr & 1;
+      const int fr = f * 4 + w, s = fr & 1;
+      const int dim = (fr >> 1) / DT * (DK / 4) + 4 * DT * (n >> 2) + 4 * ((fr >> 1) % DT) + (n & 3);
       u32x4_t v;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint16_t* p = s_k + (32 * s + 8 * hg + 2 * i) * KS + 16 * dt + n;
+        const uint16_t* p = s_k + (32 * s + 8 * hg + 2 * i) * KS + dim;
         v[i] = uint32_t(p[0]) | (uint32_t(p[KS]) << 16);
       }
       *reinterpret_cast<u32x4_t*>(kt + fr * 1024 + lane * 16) = v;
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int from = (16 * t + n) * KS + w * (DK / 4) + 4 * DT * hg;
+      unsigned char* to = kt + part_bytes(DK) + ((w * 4 + t) * 64 + lane) * (8 * DT);
+      if constexpr (DT == 2) {
+        *reinterpret_cast<u32x4_t*>(to) = *reinterpret_cast<const u32x4_t*>(s_k + from);
+        *reinterpret_cast<u32x4_t*>(to + part_bytes(DK)) = *reinterpret_cast<const u32x4_t*>(s_q + from);
+      } else {
+        *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(s_k + from);
+        *reinterpret_cast<uint2*>(to + part_bytes(DK)) = *reinterpret_cast<const uint2*>(s_q + from);
+      }
     }
   }
   // row tile w of K K^T and Q K^T
@@ -229,25 +246,27 @@ __global__ __launch_bounds__(256) void gdn_prep_kernel(GdnArgs g, int64_t n_slot
     const float top = s_hi[C - 1], tol = s_lo[C - 1];
     const float e = exp2_hw(s_hi[tid] + s_lo[tid]);
     const bool in = tid < left;
-    float4 f;
-    f.x = in ? e * s_rk[tid] : 0.f;
-    f.y = in ? e * s_rq[tid] : 0.f;
-    f.z = in ? exp2_hw((top - s_hi[tid]) + (tol - s_lo[tid])) * s_rk[tid] : 0.f;
-    f.w = exp2_hw(top + tol);
-    *reinterpret_cast<float4*>(mine + kFactors + tid * 16) = f;
+    float* f = reinterpret_cast<float*>(mine + kFactors);
+    f[tid] = in ? e * s_rk[tid] : 0.f;
+    f[C + tid] = in ? e * s_rq[tid] : 0.f;
+    f[2 * C + tid] = in ? exp2_hw((top - s_hi[tid]) + (tol - s_lo[tid])) * s_rk[tid] : 0.f;
+    f[3 * C + tid] = exp2_hw(top + tol);
   }
 }
 
 // ---- walk: one value head's 16 NT columns through a sequence -------------------------------
 
+// Eight waves.  Four carry the state: wave w holds dims w DK/4 .. of it in registers, in an
+// order that makes them the operand of K S and Q S as they stand, so only sums of partial
+// products, X, D and U = D e^{c_64 - c} cross waves (LDS, three barriers a chunk).  The other four
+// make the outputs of the chunk whose D they were given while the first four go on.
 template <int DK, int NT>
-__global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void gdn_walk_kernel(GdnArgs g, int64_t n_slots_ws, int slices,
-                                                                        int heads) {
-  constexpr int SS = DK + 8, XS = C + 8;  // LDS rows in bf16
-  constexpr int DT = DK / 64;             // dim tiles of a wave
-  constexpr int KSTEP = DK / 32;
+__global__ __launch_bounds__(512, 2) void gdn_walk_kernel(GdnArgs g, int64_t n_slots_ws, int slices, int heads) {
+  constexpr int XS = C + 8;    // LDS row of a column's tokens in bf16 ...
+  constexpr int DS = C + 4;    // ... and in fp32
+  constexpr int DT = DK / 64;  // dim tiles of a wave
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, hg = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave & 3;
   // block L runs on XCD L % 8: the slices of a (sequence, head) share one
   const int xi = int(blockIdx.x) >> 3, unit = (int(blockIdx.x) & 7) + 8 * (xi / slices), slice = xi % slices;
   if (unit >= heads) return;
@@ -256,18 +275,110 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void gdn_walk_kernel(GdnArgs 
   const bool kept = uint32_t(sq.slot) < uint32_t(g.n_slots);
   if (sq.len == 0 && (!kept || g.state_in == g.state_out)) return;
 
-  __shared__ __attribute__((aligned(16))) uint16_t s_s[3][16 * NT * SS];
-  __shared__ __attribute__((aligned(16))) uint16_t s_x[3][16 * NT * XS], s_d[3][16 * NT * XS], s_u[3][16 * NT * XS];
+  __shared__ f32x4_t s_ks[4][NT][4][64], s_qs[4][NT][4][64];  // partial sums: of wave, for row tile
+  __shared__ __attribute__((aligned(16))) uint16_t s_x[3][16 * NT * XS], s_u[3][16 * NT * XS];
+  __shared__ __attribute__((aligned(16))) float s_d[16 * NT * DS];
 
-  // state: rows = dims 16 (w DT + dt) + 4 hg + i, column v0 + 16 nt + n
   const int v0 = slice * 16 * NT;
-  const int64_t sbase = ((int64_t(kept ? sq.slot : 0) * g.Hv + hv) * g.Dv + v0 + n) * DK + 16 * w * DT + 4 * hg;
+  const int chunks = (sq.len + C - 1) / C;
+  const unsigned char* ws = static_cast<const unsigned char*>(g.ws);
+  const unsigned char* head0 = ws + (chunk_slot(sq, b, 0) * g.Hv + hv) * kHeadBytes;
+  const int64_t head_step = g.Hv * kHeadBytes;
+  auto head_at = [&](int c) { return head0 + c * head_step; };
+  // A column's tokens of V and y: 32 bits from the chunk's first one (64 rows of Hv Dv).
+  const uint32_t row_bytes = uint32_t(g.Hv) * uint32_t(g.Dv) * 2u;
+  auto load_tri = [&](int c, int64_t part, u32x4_t (&f)[2][3]) {
+    const unsigned char* at = head_at(c) + part;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+        f[s][p] = *reinterpret_cast<const u32x4_t*>(at + (tri_at(w, s <= (w >> 1) ? s : 0) * 3 + p) * 1024 + uint32_t(lane * 16));
+    }
+  };
+  // six partial products
+  auto mma6 = [&](const u32x4_t (&f)[3], const u32x4_t (&x)[3], f32x4_t (&a)[3]) {
+    a[0] = mma(f[0], x[0], a[0]);
+    a[1] = mma(f[0], x[1], a[1]);
+    a[2] = mma(f[0], x[2], a[2]);
+    a[1] = mma(f[1], x[0], a[1]);
+    a[2] = mma(f[1], x[1], a[2]);
+    a[2] = mma(f[2], x[0], a[2]);
+  };
+
+  if (wave >= 4) {  // outputs
+    u32x4_t fa[2][3];
+    f32x4_t fy;
+    auto load = [&](int c) {
+      load_tri(c, kFragA, fa);
+      fy = *reinterpret_cast<const f32x4_t*>(head_at(c) + kFactors + (C + 16 * w) * 4 + uint32_t(hg * 16));
+    };
+    if (chunks) load(0);
+    for (int c = 0; c < chunks; ++c) {
+      __syncthreads();
+      __syncthreads();
+      __syncthreads();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        f32x4_t a[3] = {};
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (s > (w >> 1)) continue;
+          const float* at = &s_d[(16 * nt + n) * DS + 32 * s + 8 * hg];
+          const f32x4_t d0 = *reinterpret_cast<const f32x4_t*>(at), d1 = *reinterpret_cast<const f32x4_t*>(at + 4);
+          u32x4_t x[3];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t h, m, l;
+            if (i < 2) split2(d0[2 * i], d0[2 * i + 1], h, m, l);
+            else split2(d1[2 * i - 4], d1[2 * i - 3], h, m, l);
+            x[0][i] = h, x[1][i] = m, x[2][i] = l;
+          }
+          mma6(fa[s], x, a);
+        }
+        const f32x4_t q = (s_qs[0][nt][w][lane] + s_qs[1][nt][w][lane]) + (s_qs[2][nt][w][lane] + s_qs[3][nt][w][lane]);
+        const f32x4_t y = a[0] + (a[1] + a[2]);
+        f32x4_t v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = fmaf(fy[i], q[i], y[i]);
+        asm volatile("" : "+v"(v));  // whole before the branches, which else wait for each other's stores
+        const int left = sq.len - c * C - 16 * w;  // tokens from the row tile's first on
+        const int64_t y0 = ((int64_t(sq.t0) + c * C + 16 * w) * g.Hv + hv) * g.Dv + v0 + 16 * nt;
+        const uint32_t at = uint32_t(4 * hg) * row_bytes + uint32_t(2 * n);
+        if (g.f32_out) {
+          unsigned char* to = static_cast<unsigned char*>(g.y) + y0 * 4;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (4 * hg + i < left) *reinterpret_cast<float*>(to + uint64_t(at + uint32_t(i) * row_bytes) * 2) = v[i];
+        } else {
+          unsigned char* to = static_cast<unsigned char*>(g.y) + y0 * 2;
+          uint16_t r[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) r[i] = f32_to_bf16_bits(v[i]);
+          if (left >= 16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<uint16_t*>(to + (at + uint32_t(i) * row_bytes)) = r[i];
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (4 * hg + i < left) *reinterpret_cast<uint16_t*>(to + (at + uint32_t(i) * row_bytes)) = r[i];
+          }
+        }
+      }
+      load(c + 1 < chunks ? c + 1 : c);
+    }
+    return;
+  }
+
+  __builtin_amdgcn_s_setprio(2);  // the chain that the sequence waits for
+  // state: row 4 hg + i of tile dt is dim w DK/4 + 4 DT hg + 4 dt + i, column v0 + 16 nt + n
+  const int64_t sbase = ((int64_t(kept ? sq.slot : 0) * g.Hv + hv) * g.Dv + v0 + n) * DK + w * (DK / 4) + 4 * DT * hg;
   f32x4_t st[DT][NT];
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
-      st[dt][nt] = kept ? *reinterpret_cast<const f32x4_t*>(g.state_in + sbase + int64_t(16 * nt) * DK + 16 * dt)
+      st[dt][nt] = kept ? *reinterpret_cast<const f32x4_t*>(g.state_in + sbase + int64_t(16 * nt) * DK + 4 * dt)
                         : f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
   auto put4 = [&](uint16_t (*pl)[16 * NT * XS], int nt, f32x4_t x) {  // rows 16 w + 4 hg .. +3 of column 16 nt + n
@@ -279,185 +390,181 @@ __global__ __launch_bounds__(256, NT == 1 ? 2 : 1) void gdn_walk_kernel(GdnArgs 
     *reinterpret_cast<uint2*>(&pl[1][at]) = uint2{m0, m1};
     *reinterpret_cast<uint2*>(&pl[2][at]) = uint2{l0, l1};
   };
-  auto put_state = [&]() {
+  auto get = [&](const uint16_t (*pl)[16 * NT * XS], int nt, int s, u32x4_t (&x)[3]) {
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt) {
+    for (int p = 0; p < 3; ++p)
+      x[p] = *reinterpret_cast<const u32x4_t*>(&pl[p][(16 * nt + n) * XS + 32 * s + 8 * hg]);
+  };
+
+  const unsigned char* key0 = ws + n_slots_ws * g.Hv * kHeadBytes + (chunk_slot(sq, b, 0) * g.Hk + hk) * key_bytes(DK);
+  const int64_t key_step = g.Hk * key_bytes(DK);
+  auto key_at = [&](int c) { return key0 + c * key_step; };
+  u32x4_t fk[4], fq[4], fm[2][3], ft[DT][2];
+  f32x4_t fx, fz;
+  float decay;
+  uint16_t fv[NT][4];
+  auto load_rows = [&](int part, int c, u32x4_t (&f)[4]) {  // this wave's dims of all 64 tokens: K (1), Q (2)
+    const unsigned char* at = key_at(c) + part * part_bytes(DK) + w * (512 * 4 * DT);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const f32x4_t x = st[dt][nt];
-        uint32_t h0, m0, l0, h1, m1, l1;
-        split2(x[0], x[1], h0, m0, l0);
-        split2(x[2], x[3], h1, m1, l1);
-        const int at = (16 * nt + n) * SS + 16 * (w * DT + dt) + 4 * hg;
-        *reinterpret_cast<uint2*>(&s_s[0][at]) = uint2{h0, h1};
-        *reinterpret_cast<uint2*>(&s_s[1][at]) = uint2{m0, m1};
-        *reinterpret_cast<uint2*>(&s_s[2][at]) = uint2{l0, l1};
+    for (int t = 0; t < 4; ++t) {
+      if constexpr (DT == 2) {
+        f[t] = *reinterpret_cast<const u32x4_t*>(at + t * 1024 + uint32_t(lane * 16));
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(at + t * 512 + uint32_t(lane * 8));
+        f[t] = u32x4_t{v.x, v.y, 0u, 0u};
       }
     }
   };
-
-  const int chunks = (sq.len + C - 1) / C;
-  const unsigned char* ws = static_cast<const unsigned char*>(g.ws);
-  const unsigned char* ktb = ws + n_slots_ws * g.Hv * kHeadBytes;
-  u32x4_t fk[KSTEP], fq[KSTEP], fm[2][3], fa[2][3], ft[DT][2];
-  float4 fac[4];
-  float fv[NT][4];
-  auto head_at = [&](int c) { return ws + (chunk_slot(sq, b, c) * g.Hv + hv) * kHeadBytes; };
-  auto row_at = [&](int c, int r) {  // token of row r of chunk c, the last one behind the sequence
-    const int t = c * C + r;
-    return int64_t(sq.t0) + (t < sq.len ? t : sq.len - 1);
-  };
-  auto load_kq = [&](int c) {
-    const int64_t at = (row_at(c, 16 * w + n) * g.Hk + hk) * DK + 8 * hg;
+  uint32_t voff[4];
 #pragma unroll
-    for (int s = 0; s < KSTEP; ++s) {
-      fk[s] = *reinterpret_cast<const u32x4_t*>(g.k + at + 32 * s);
-      fq[s] = *reinterpret_cast<const u32x4_t*>(g.q + at + 32 * s);
-    }
-  };
+  for (int i = 0; i < 4; ++i) voff[i] = uint32_t(16 * w + 4 * hg + i) * row_bytes;
   auto load_v = [&](int c) {
+    const int left = sq.len - c * C;
+    const uint32_t last = uint32_t(left < C ? left - 1 : C - 1) * row_bytes;
+    const unsigned char* from = reinterpret_cast<const unsigned char*>(g.v) +
+                                2 * (((int64_t(sq.t0) + c * C) * g.Hv + hv) * g.Dv + v0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t at = (row_at(c, 16 * w + 4 * hg + i) * g.Hv + hv) * g.Dv + v0 + n;
+    for (int i = 0; i < 4; ++i) {  // the sequence's last token stands for those behind it
+      const uint32_t at = voff[i] < last ? voff[i] : last;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) fv[nt][i] = bf16_bits_to_f32(g.v[at + 16 * nt]);
+      for (int nt = 0; nt < NT; ++nt)
+        fv[nt][i] = *reinterpret_cast<const uint16_t*>(from + 32 * nt + (at + uint32_t(2 * n)));
     }
   };
-  auto load_fac = [&](int c) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      fac[i] = *reinterpret_cast<const float4*>(head_at(c) + kFactors + (16 * w + 4 * hg + i) * 16);
+  auto load_fac = [&](int c, int which) {
+    return *reinterpret_cast<const f32x4_t*>(head_at(c) + kFactors + (which * C + 16 * w) * 4 + uint32_t(hg * 16));
   };
-  auto load_tri = [&](int c, int64_t part, u32x4_t (&f)[2][3]) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      if (s > (w >> 1)) continue;
-#pragma unroll
-      for (int p = 0; p < 3; ++p)
-        f[s][p] = *reinterpret_cast<const u32x4_t*>(head_at(c) + part + (tri_at(w, s) * 3 + p) * 1024 + lane * 16);
-    }
-  };
+  auto load_decay = [&](int c) { return *reinterpret_cast<const float*>(head_at(c) + kFactors + 3 * C * 4 + uint32_t(lane * 4)); };
   auto load_kt = [&](int c) {
-    const unsigned char* kt = ktb + (chunk_slot(sq, b, c) * g.Hk + hk) * key_bytes(DK);
+    const unsigned char* kt = key_at(c) + w * (2048 * DT);
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) {
 #pragma unroll
       for (int s = 0; s < 2; ++s)
-        ft[dt][s] = *reinterpret_cast<const u32x4_t*>(kt + ((w * DT + dt) * 2 + s) * 1024 + lane * 16);
+        ft[dt][s] = *reinterpret_cast<const u32x4_t*>(kt + (dt * 2 + s) * 1024 + uint32_t(lane * 16));
     }
   };
-  // lower-triangular product of row tile w with the columns in `pl`, six partial products
-  auto tri_mul = [&](const u32x4_t (&f)[2][3], const uint16_t (*pl)[16 * NT * XS], int nt) {
-    f32x4_t a0 = {0.f, 0.f, 0.f, 0.f}, a1 = a0, a2 = a0;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      if (s > (w >> 1)) continue;
-      u32x4_t x[3];
-#pragma unroll
-      for (int p = 0; p < 3; ++p)
-        x[p] = *reinterpret_cast<const u32x4_t*>(&pl[p][(16 * nt + n) * XS + 32 * s + 8 * hg]);
-      a0 = mma(f[s][0], x[0], a0);
-      a1 = mma(f[s][0], x[1], a1);
-      a2 = mma(f[s][0], x[2], a2);
-      a1 = mma(f[s][1], x[0], a1);
-      a2 = mma(f[s][1], x[1], a2);
-      a2 = mma(f[s][2], x[0], a2);
-    }
-    return a0 + (a1 + a2);
-  };
-
   if (chunks) {
-    load_kq(0);
+    load_rows(1, 0, fk);
+    fx = load_fac(0, 0);
     load_v(0);
-    load_fac(0);
+    load_rows(2, 0, fq);
     load_tri(0, kFragM, fm);
-    load_tri(0, kFragA, fa);
+    fz = load_fac(0, 2);
+    decay = load_decay(0);
     load_kt(0);
-    put_state();
+  }
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt) {  // arrived before the loop, which then counts its own loads
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) asm volatile("" : "+v"(st[dt][nt]));
   }
   for (int c = 0; c < chunks; ++c) {
     const int cn = c + 1 < chunks ? c + 1 : c;
-    __syncthreads();
-    // K S and Q S
-    f32x4_t ks[NT][3], qs[NT][3];
+    u32x4_t sp[NT][3];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int p = 0; p < 3; ++p) ks[nt][p] = qs[nt][p] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < 4; ++i) {
+        uint32_t h = 0, m = 0, l = 0;
+        if (i / 2 < DT) split2(st[i / 2 < DT ? i / 2 : 0][nt][2 * (i & 1)], st[i / 2 < DT ? i / 2 : 0][nt][2 * (i & 1) + 1], h, m, l);
+        sp[nt][0][i] = h, sp[nt][1][i] = m, sp[nt][2][i] = l;
+      }
     }
+    // K S: this wave's dims, smallest parts first
+    f32x4_t ks[NT][4], qs[NT][4];
 #pragma unroll
-    for (int s = 0; s < KSTEP; ++s) {
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int p = 2; p >= 0; --p) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) ks[nt][t] = mma(fk[t], sp[nt][p], p == 2 ? f32x4_t{0.f, 0.f, 0.f, 0.f} : ks[nt][t]);
+      }
+    }
+    load_rows(1, cn, fk);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) s_ks[w][nt][t][lane] = ks[nt][t];
+    }
+    __syncthreads();
+    f32x4_t x[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[nt][i] = s_ks[i][nt][w][lane];
+    }
+    auto qs_mul = [&](int t0) {  // Q S of two row tiles, while LDS answers
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int p = 0; p < 3; ++p) {
-          const u32x4_t x = *reinterpret_cast<const u32x4_t*>(&s_s[p][(16 * nt + n) * SS + 32 * s + 8 * hg]);
-          ks[nt][p] = mma(fk[s], x, ks[nt][p]);
-          qs[nt][p] = mma(fq[s], x, qs[nt][p]);
+        for (int p = 2; p >= 0; --p) {
+#pragma unroll
+          for (int t = t0; t < t0 + 2; ++t)
+            qs[nt][t] = mma(fq[t], sp[nt][p], p == 2 ? f32x4_t{0.f, 0.f, 0.f, 0.f} : qs[nt][t]);
         }
       }
-    }
-    load_kq(cn);
+    };
+    qs_mul(0);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      f32x4_t x;
-      const f32x4_t k3 = ks[nt][0] + (ks[nt][1] + ks[nt][2]);
+      const f32x4_t sum = (x[nt][0] + x[nt][1]) + (x[nt][2] + x[nt][3]);
+      f32x4_t r;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = fmaf(-fac[i].x, k3[i], fv[nt][i]);
-      put4(s_x, nt, x);
+      for (int i = 0; i < 4; ++i) r[i] = fmaf(-fx[i], sum[i], bf16_bits_to_f32(fv[nt][i]));
+      put4(s_x, nt, r);
     }
+    fx = load_fac(cn, 0);
     load_v(cn);
     __syncthreads();
+    qs_mul(2);
+    load_rows(2, cn, fq);
     // D, as it is (for the outputs) and faded to the chunk's end (for the state)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const f32x4_t d = tri_mul(fm, s_x, nt);
-      put4(s_d, nt, d);
-      f32x4_t u;
+      f32x4_t a[3] = {};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] = d[i] * fac[i].z;
-      put4(s_u, nt, u);
+      for (int s = 0; s < 2; ++s) {
+        if (s > (w >> 1)) continue;
+        u32x4_t xp[3];
+        get(s_x, nt, s, xp);
+        mma6(fm[s], xp, a);
+      }
+      const f32x4_t d = a[0] + (a[1] + a[2]);
+      *reinterpret_cast<f32x4_t*>(&s_d[(16 * nt + n) * DS + 16 * w + 4 * hg]) = d;
+      put4(s_u, nt, d * fz);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) s_qs[w][nt][t][lane] = qs[nt][t];
     }
     load_tri(cn, kFragM, fm);
+    fz = load_fac(cn, 2);
     __syncthreads();
-    const float decay = fac[0].w;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      f32x4_t a[DT][2];
+      u32x4_t up[2][3];
+      get(s_u, nt, 0, up[0]);
+      get(s_u, nt, 1, up[1]);
 #pragma unroll
-      for (int dt = 0; dt < DT; ++dt) {
-        f32x4_t a0 = {0.f, 0.f, 0.f, 0.f}, a1 = a0, a2 = a0;
+      for (int p = 2; p >= 0; --p) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const int at = (16 * nt + n) * XS + 32 * s + 8 * hg;
-          a0 = mma(ft[dt][s], *reinterpret_cast<const u32x4_t*>(&s_u[0][at]), a0);
-          a1 = mma(ft[dt][s], *reinterpret_cast<const u32x4_t*>(&s_u[1][at]), a1);
-          a2 = mma(ft[dt][s], *reinterpret_cast<const u32x4_t*>(&s_u[2][at]), a2);
+        for (int dt = 0; dt < DT; ++dt) {
+#pragma unroll
+          for (int s = 0; s < 2; ++s) a[dt][s] = mma(ft[dt][s], up[s][p], p == 2 ? f32x4_t{0.f, 0.f, 0.f, 0.f} : a[dt][s]);
         }
-        st[dt][nt] = st[dt][nt] * decay + (a0 + (a1 + a2));
       }
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) st[dt][nt] = st[dt][nt] * decay + (a[dt][0] + a[dt][1]);
     }
     load_kt(cn);
-    put_state();  // every wave has read the old planes: two barriers ago
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      f32x4_t y = tri_mul(fa, s_d, nt);
-      const f32x4_t q3 = qs[nt][0] + (qs[nt][1] + qs[nt][2]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = c * C + 16 * w + 4 * hg + i;
-        if (t < sq.len)
-          gdn_store(g, ((int64_t(sq.t0) + t) * g.Hv + hv) * g.Dv + v0 + 16 * nt + n, fmaf(fac[i].y, q3[i], y[i]));
-      }
-    }
-    load_tri(cn, kFragA, fa);
-    load_fac(cn);
+    decay = load_decay(cn);
   }
   if (kept) {
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
-        *reinterpret_cast<f32x4_t*>(g.state_out + sbase + int64_t(16 * nt) * DK + 16 * dt) = st[dt][nt];
+        *reinterpret_cast<f32x4_t*>(g.state_out + sbase + int64_t(16 * nt) * DK + 4 * dt) = st[dt][nt];
     }
   }
 }
@@ -468,7 +575,7 @@ template <int DK, int NT>
 void walk(const GdnArgs& a, int64_t n, hipStream_t s) {
   const int slices = a.Dv / (16 * NT), heads = a.B * a.Hv;
   const uint32_t grid = uint32_t((heads + 7) / 8 * 8) * uint32_t(slices);
-  gdn_walk_kernel<DK, NT><<<dim3(grid), 256, 0, s>>>(a, n, slices, heads);
+  gdn_walk_kernel<DK, NT><<<dim3(grid), 512, 0, s>>>(a, n, slices, heads);
 }
 
 template <int DK>
@@ -478,7 +585,7 @@ int launch(const GdnArgs& a, hipStream_t s) {
   gdn_prep_kernel<DK><<<dim3(chunks ? chunks : 1, uint32_t(a.Hv), uint32_t(a.B)), 256, 0, s>>>(a, n);
   if (hipGetLastError() != hipSuccess) return 6;
   // 32 columns a block share its operands' loads where 16 would more than fill the GPU
-  if (int64_t(a.B) * a.Hv * (a.Dv / 16) > 2 * int64_t(device_cus())) walk<DK, 2>(a, n, s);
+  if (int64_t(a.B) * a.Hv * (a.Dv / 16) > int64_t(device_cus())) walk<DK, 2>(a, n, s);
   else walk<DK, 1>(a, n, s);
   return hipGetLastError() == hipSuccess ? 0 : 6;
 }
