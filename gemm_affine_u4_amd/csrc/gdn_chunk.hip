@@ -11,7 +11,9 @@
 //
 // Precision.  Keys, queries and values are bf16 and enter exactly (their norms are factors
 // of rows).  An fp32 factor x enters as h + m + l, three bf16 values that hold its 24 bits; a
-// product of two such factors takes the six partial products down to 2^-24.  T comes from
+// product of two such factors takes the six partial products down to 2^-24.  What only a
+// bf16 output reads (scores, D as their factor, S as Q's) enters as h + m: 2^-16 relative, 1/128 of
+// that output's own rounding; an fp32 output takes l too (PO planes).  T comes from
 // forward substitution and fp32 matrix products; sums are fp32, the running sum of g fp64.
 //
 // Bound: latency of the chunk's dependent products for few sequences (three barriers a
@@ -62,11 +64,13 @@ __device__ __forceinline__ int64_t chunk_slot(const GdnSeq& s, int b, int c) { r
 
 // ---- prep: one (chunk, value head) ---------------------------------------------------------
 
-template <int DK>
-__global__ __launch_bounds__(256) void gdn_prep_kernel(GdnArgs g, int64_t n_slots_ws) {
-  constexpr int KS = DK + 8;   // LDS row of keys, in bf16: 16-byte reads of 16 rows meet no bank twice
-  constexpr int FS = C + 4;    // LDS row of a 64 x 64 fp32 matrix
-  constexpr int DT = DK / 64;  // dim tiles of a wave of the walk
+// Wave w makes row tile w (16 tokens) of L, T and the scores, as transposed products: lane
+// (n, hg) then holds columns 4 hg .. +3 of every 16 of row n, which is the fragment order that the
+// walk loads, with the tokens of a 32-wide step taken as 16 (j / 4) + 4 hg + j % 4.
+template <int DK, int PO>
+__global__ __launch_bounds__(256, 4) void gdn_prep_kernel(GdnArgs g, int64_t n_slots_ws) {
+  constexpr int KSTEP = DK / 32;
+  constexpr int LS = 20;  // LDS row of a 16 x 16 fp32 tile
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, hg = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = blockIdx.x, hv = blockIdx.y, b = blockIdx.z, rep = g.Hv / g.Hk, hk = hv / rep;
@@ -75,39 +79,29 @@ __global__ __launch_bounds__(256) void gdn_prep_kernel(GdnArgs g, int64_t n_slot
   const int left = sq.len - c * C;  // tokens from the chunk's start on
   const int64_t tok0 = int64_t(sq.t0) + c * C;
 
-  constexpr int kKQ = 2 * C * KS * 2, kLA = 2 * C * FS * 4;
-  __shared__ __attribute__((aligned(16))) unsigned char s_pool[(kKQ > kLA ? kKQ : kLA)];
-  uint16_t* s_k = reinterpret_cast<uint16_t*>(s_pool);
-  uint16_t* s_q = s_k + C * KS;
-  float* s_l = reinterpret_cast<float*>(s_pool);  // over the keys, once they are used
-  float* s_a = s_l + C * FS;
-  __shared__ __attribute__((aligned(16))) float s_t[C * FS];
-  __shared__ float s_rk[C], s_rq[C], s_beta[C], s_hi[C], s_lo[C];
+  __shared__ u32x4_t s_k[4][KSTEP][64];
+  __shared__ __attribute__((aligned(16))) float s_l[10][16 * LS], s_t[4][16 * LS];
+  __shared__ __attribute__((aligned(16))) float s_rk[C], s_rq[C], s_beta[C], s_hi[C], s_lo[C];
+  auto tile = [](int i, int j) { return i * (i + 1) / 2 + j; };
 
-  // keys and queries; tokens behind the sequence repeat its last one (their beta is 0)
-  constexpr int LPR = DK / 8;
+  // keys and queries of the wave's rows; tokens behind the sequence repeat its last one (their beta is 0)
+  const int row = 16 * w + n;
+  u32x4_t ak[KSTEP], aq[KSTEP];
+  {
+    const int64_t at = ((tok0 + (row < left ? row : left - 1)) * g.Hk + hk) * DK;
 #pragma unroll
-  for (int it = 0; it < C * LPR / 256; ++it) {
-    const int e = it * 256 + tid, r = e / LPR, d = (e % LPR) * 8;
-    const int64_t tok = tok0 + (r < left ? r : left - 1);
-    const int64_t at = (tok * g.Hk + hk) * DK + d;
-    const u32x4_t kv = *reinterpret_cast<const u32x4_t*>(g.k + at), qv = *reinterpret_cast<const u32x4_t*>(g.q + at);
-    *reinterpret_cast<u32x4_t*>(s_k + r * KS + d) = kv;
-    *reinterpret_cast<u32x4_t*>(s_q + r * KS + d) = qv;
-    float kk = 0.f, qq = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      kk = fmaf(bf16_lo(kv[i]), bf16_lo(kv[i]), fmaf(bf16_hi(kv[i]), bf16_hi(kv[i]), kk));
-      qq = fmaf(bf16_lo(qv[i]), bf16_lo(qv[i]), fmaf(bf16_hi(qv[i]), bf16_hi(qv[i]), qq));
+    for (int s = 0; s < KSTEP; ++s) {
+      if constexpr (DK == 128) {
+        ak[s] = *reinterpret_cast<const u32x4_t*>(g.k + at + 32 * s + 8 * hg);
+        aq[s] = *reinterpret_cast<const u32x4_t*>(g.q + at + 32 * s + 8 * hg);
+      } else {
+        const uint16_t *kp = g.k + at + 32 * s + 4 * hg, *qp = g.q + at + 32 * s + 4 * hg;
+        const uint2 k0 = *reinterpret_cast<const uint2*>(kp), k1 = *reinterpret_cast<const uint2*>(kp + 16);
+        const uint2 q0 = *reinterpret_cast<const uint2*>(qp), q1 = *reinterpret_cast<const uint2*>(qp + 16);
+        ak[s] = u32x4_t{k0.x, k0.y, k1.x, k1.y};
+        aq[s] = u32x4_t{q0.x, q0.y, q1.x, q1.y};
+      }
     }
-    if (g.l2norm) {
-#pragma unroll
-      for (int o = 1; o < LPR; o <<= 1) kk += __shfl_xor(kk, o), qq += __shfl_xor(qq, o);
-      kk = 1.f / sqrtf(kk + kGdnEps), qq = 1.f / sqrtf(qq + kGdnEps);
-    } else {
-      kk = qq = 1.f;
-    }
-    if (d == 0) s_rk[r] = kk, s_rq[r] = qq * g.scale;
   }
   if (w == 0) {
     const bool in = lane < left;
@@ -124,124 +118,143 @@ __global__ __launch_bounds__(256) void gdn_prep_kernel(GdnArgs g, int64_t n_slot
     s_hi[lane] = hi;
     s_lo[lane] = float(x - double(hi));
   }
+  float rk = 1.f, rq = 1.f;
+#pragma unroll
+  for (int s = 0; s < KSTEP; ++s) s_k[w][s][lane] = ak[s];
+  if (g.l2norm) {
+    rk = rq = 0.f;
+#pragma unroll
+    for (int s = 0; s < KSTEP; ++s) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        rk = fmaf(bf16_lo(ak[s][i]), bf16_lo(ak[s][i]), fmaf(bf16_hi(ak[s][i]), bf16_hi(ak[s][i]), rk));
+        rq = fmaf(bf16_lo(aq[s][i]), bf16_lo(aq[s][i]), fmaf(bf16_hi(aq[s][i]), bf16_hi(aq[s][i]), rq));
+      }
+    }
+    rk += __shfl_xor(rk, 16), rq += __shfl_xor(rq, 16);
+    rk += __shfl_xor(rk, 32), rq += __shfl_xor(rq, 32);
+    rk = 1.f / sqrtf(rk + kGdnEps), rq = 1.f / sqrtf(rq + kGdnEps);
+  }
+  rq *= g.scale;
+  if (hg == 0) s_rk[row] = rk, s_rq[row] = rq;
   __syncthreads();
 
   const int64_t slot = chunk_slot(sq, b, c);
   unsigned char* ws = static_cast<unsigned char*>(g.ws);
   unsigned char* mine = ws + (slot * g.Hv + hv) * kHeadBytes;
-  if (hv % rep == 0) {  // K^T fragments, once per key head
+  if (hv % rep == 0) {  // fragments of K^T, K and Q, once per key head
     unsigned char* kt = ws + n_slots_ws * g.Hv * kHeadBytes + (slot * g.Hk + hk) * key_bytes(DK);
+    unsigned char *kf = kt + part_bytes(DK), *qf = kf + part_bytes(DK);
+#pragma unroll
+    for (int s = 0; s < KSTEP; ++s) {
+      if constexpr (DK == 128) {
+        const int at = s * 4096 + w * 1024 + lane * 16;
+        *reinterpret_cast<u32x4_t*>(kf + at) = ak[s];
+        *reinterpret_cast<u32x4_t*>(qf + at) = aq[s];
+      } else {
+        const int at = s * 4096 + w * 512 + lane * 8;
+        *reinterpret_cast<uint2*>(kf + at) = uint2{ak[s][0], ak[s][1]};
+        *reinterpret_cast<uint2*>(kf + at + 2048) = uint2{ak[s][2], ak[s][3]};
+        *reinterpret_cast<uint2*>(qf + at) = uint2{aq[s][0], aq[s][1]};
+        *reinterpret_cast<uint2*>(qf + at + 2048) = uint2{aq[s][2], aq[s][3]};
+      }
+    }
 #pragma unroll
     for (int f = 0; f < DK / 16 * 2 / 4; ++f) {
-      const int fr = f * 4 + w, s = fr & 1;
-      const int dim = (fr >> 1) / DT * (DK / 4) + 4 * DT * (n >> 2) + 4 * ((fr >> 1) % DT) + (n & 3);
+      const int fr = f * 4 + w, dt = fr >> 1, s = fr & 1;  // dim tile, token half
       u32x4_t v;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint16_t* p = s_k + (32 * s + 8 * hg + 2 * i) * KS + dim;
-        v[i] = uint32_t(p[0]) | (uint32_t(p[KS]) << 16);
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(
+                                &s_k[2 * s + (i >> 1)][dt >> 1][(n >> 2) * 16 + 4 * hg + 2 * (i & 1)]) +
+                            4 * (dt & 1) + (n & 3);
+        v[i] = uint32_t(p[0]) | (uint32_t(p[8]) << 16);
       }
       *reinterpret_cast<u32x4_t*>(kt + fr * 1024 + lane * 16) = v;
     }
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int from = (16 * t + n) * KS + w * (DK / 4) + 4 * DT * hg;
-      unsigned char* to = kt + part_bytes(DK) + ((w * 4 + t) * 64 + lane) * (8 * DT);
-      if constexpr (DT == 2) {
-        *reinterpret_cast<u32x4_t*>(to) = *reinterpret_cast<const u32x4_t*>(s_k + from);
-        *reinterpret_cast<u32x4_t*>(to + part_bytes(DK)) = *reinterpret_cast<const u32x4_t*>(s_q + from);
-      } else {
-        *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(s_k + from);
-        *reinterpret_cast<uint2*>(to + part_bytes(DK)) = *reinterpret_cast<const uint2*>(s_q + from);
-      }
-    }
   }
-  // row tile w of K K^T and Q K^T
-  f32x4_t kk[4], qk[4];
+  // row tile w of K K^T and Q K^T, transposed
+  const float beta = s_beta[row], hi = s_hi[row], lo = s_lo[row];
+  f32x4_t sc[4] = {};  // the scores
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    kk[j] = qk[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     if (j > w) continue;
+    f32x4_t kk = {0.f, 0.f, 0.f, 0.f}, qk = kk;
 #pragma unroll
-    for (int s = 0; s < DK / 32; ++s) {
-      const u32x4_t bk = *reinterpret_cast<const u32x4_t*>(s_k + (16 * j + n) * KS + 32 * s + 8 * hg);
-      const u32x4_t ak = *reinterpret_cast<const u32x4_t*>(s_k + (16 * w + n) * KS + 32 * s + 8 * hg);
-      const u32x4_t aq = *reinterpret_cast<const u32x4_t*>(s_q + (16 * w + n) * KS + 32 * s + 8 * hg);
-      kk[j] = mma(ak, bk, kk[j]);
-      qk[j] = mma(aq, bk, qk[j]);
+    for (int s = 0; s < KSTEP; ++s) {
+      const u32x4_t bk = s_k[j][s][lane];
+      kk = mma(bk, ak[s], kk);
+      qk = mma(bk, aq[s], qk);
     }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int col = 16 * j + n;
-    const float rkj = s_rk[col], hj = s_hi[col], lj = s_lo[col];
+    const int col = 16 * j + 4 * hg;
+    const f32x4_t rkc = *reinterpret_cast<const f32x4_t*>(&s_rk[col]), hic = *reinterpret_cast<const f32x4_t*>(&s_hi[col]),
+                  loc = *reinterpret_cast<const f32x4_t*>(&s_lo[col]);
+    f32x4_t l;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int row = 16 * w + 4 * hg + i;
-      const float fall = row >= col ? exp2_hw((s_hi[row] - hj) + (s_lo[row] - lj)) : 0.f;
-      s_l[row * FS + col] = row > col ? s_beta[row] * s_rk[row] * rkj * fall * kk[j][i] : 0.f;
-      s_a[row * FS + col] = row >= col ? s_rq[row] * rkj * fall * qk[j][i] : 0.f;
-      s_t[row * FS + col] = 0.f;
+      const float fall = row >= col + i ? exp2_hw((hi - hic[i]) + (lo - loc[i])) : 0.f;
+      l[i] = row > col + i ? beta * rk * rkc[i] * fall * kk[i] : 0.f;
+      sc[j][i] = row >= col + i ? rq * rkc[i] * fall * qk[i] : 0.f;
     }
+    *reinterpret_cast<f32x4_t*>(&s_l[tile(w, j)][n * LS + 4 * hg]) = l;
   }
-  __syncthreads();
-  // T: the four diagonal blocks by forward substitution (lane: block hg, column n) ...
-  if (w == 0) {
+  auto put = [&](int64_t part, int planes, int s, const f32x4_t& x0, const f32x4_t& x1) {
+    u32x4_t f[3];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4_t& x = i < 2 ? x0 : x1;
+      uint32_t h, m, l;
+      split2(x[2 * (i & 1)], x[2 * (i & 1) + 1], h, m, l);
+      f[0][i] = h, f[1][i] = m, f[2][i] = l;
+    }
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      if (p < planes) *reinterpret_cast<u32x4_t*>(mine + part + (tri_at(w, s) * 3 + p) * 1024 + uint32_t(lane * 16)) = f[p];
+    }
+  };
+  put(kFragA, PO, 0, sc[0], sc[1]);
+  if (w >= 2) put(kFragA, PO, 1, sc[2], sc[3]);
+  // T_ww by forward substitution, column n in each lane of it ...
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  {
     float x[16];
-    const float* lb = s_l + (16 * hg) * FS + 16 * hg;
+    const float* lb = s_l[tile(w, w)];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float a = i == n ? 1.f : 0.f;
 #pragma unroll
-      for (int j = 0; j < i; ++j) a = fmaf(-lb[i * FS + j], x[j], a);
+      for (int j = 0; j < i; ++j) a = fmaf(-lb[i * LS + j], x[j], a);
       x[i] = a;
-      s_t[(16 * hg + i) * FS + 16 * hg + n] = a;
+      if ((i >> 2) == hg) s_t[w][i * LS + n] = a;
     }
   }
   __syncthreads();
-  // ... and below them T_ij = -T_ii sum_k L_ik T_kj, one block diagonal after the other
+  // ... and left of it, T (I + L) = I: T_wj = -(sum_{k > j} T_wk L_kj) T_jj, all in this wave
+  f32x4_t tt[4] = {};
 #pragma unroll
-  for (int d = 1; d < 4; ++d) {
-    const int i = w + d, j = w;
-    if (i < 4) {
-      f32x4_t p = {0.f, 0.f, 0.f, 0.f};
-      for (int k = j; k < i; ++k) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-          p = __builtin_amdgcn_mfma_f32_16x16x4f32(s_l[(16 * i + n) * FS + 16 * k + 4 * s + hg],
-                                                   s_t[(16 * k + 4 * s + hg) * FS + 16 * j + n], p, 0, 0, 0);
-      }
-      f32x4_t t = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int s = 0; s < 4; ++s)  // the product's rows 4 hg + s are in this lane already
-        t = __builtin_amdgcn_mfma_f32_16x16x4f32(-s_t[(16 * i + n) * FS + 16 * i + 4 * hg + s], p[s], t, 0, 0, 0);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) s_t[(16 * i + 4 * hg + r) * FS + 16 * j + n] = t[r];
+  for (int j = 3; j >= 0; --j) {
+    if (j > w) continue;
+    if (j == w) {
+      tt[j] = *reinterpret_cast<const f32x4_t*>(&s_t[w][n * LS + 4 * hg]);
+      continue;
     }
-    __syncthreads();
+    f32x4_t x = {0.f, 0.f, 0.f, 0.f}, t = x;
+#pragma unroll
+    for (int k = j + 1; k < 4; ++k) {
+      if (k > w) continue;
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        x = __builtin_amdgcn_mfma_f32_16x16x4f32(s_l[tile(k, j)][(4 * hg + s) * LS + n], tt[k][s], x, 0, 0, 0);
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      t = __builtin_amdgcn_mfma_f32_16x16x4f32(-s_t[j][(4 * hg + s) * LS + n], x[s], t, 0, 0, 0);
+    tt[j] = t;
   }
-  // fragments of T diag(beta) and of the scores
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    if (s > (w >> 1)) continue;
-    const int col = 32 * s + 8 * hg, at = (16 * w + n) * FS + col;
-    u32x4_t pm[3], pa[3];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t h, m, l;
-      split2(s_t[at + 2 * i] * s_beta[col + 2 * i], s_t[at + 2 * i + 1] * s_beta[col + 2 * i + 1], h, m, l);
-      pm[0][i] = h, pm[1][i] = m, pm[2][i] = l;
-      split2(s_a[at + 2 * i], s_a[at + 2 * i + 1], h, m, l);
-      pa[0][i] = h, pa[1][i] = m, pa[2][i] = l;
-    }
-#pragma unroll
-    for (int p = 0; p < 3; ++p) {
-      const int64_t o = (tri_at(w, s) * 3 + p) * 1024 + lane * 16;
-      *reinterpret_cast<u32x4_t*>(mine + kFragM + o) = pm[p];
-      *reinterpret_cast<u32x4_t*>(mine + kFragA + o) = pa[p];
-    }
-  }
+  for (int j = 0; j < 4; ++j) tt[j] *= *reinterpret_cast<const f32x4_t*>(&s_beta[16 * j + 4 * hg]);
+  put(kFragM, 3, 0, tt[0], tt[1]);
+  if (w >= 2) put(kFragM, 3, 1, tt[2], tt[3]);
   if (tid < C) {  // factors of the rows: of K S, of Q S, of K in the state's update; the state's decay
     const float top = s_hi[C - 1], tol = s_lo[C - 1];
     const float e = exp2_hw(s_hi[tid] + s_lo[tid]);
@@ -260,7 +273,7 @@ __global__ __launch_bounds__(256) void gdn_prep_kernel(GdnArgs g, int64_t n_slot
 // order that makes them the operand of K S and Q S as they stand, so only sums of partial
 // products, X, D and U = D e^{c_64 - c} cross waves (LDS, three barriers a chunk).  The other four
 // make the outputs of the chunk whose D they were given while the first four go on.
-template <int DK, int NT>
+template <int DK, int NT, int PO>
 __global__ __launch_bounds__(512, 2) void gdn_walk_kernel(GdnArgs g, int64_t n_slots_ws, int slices, int heads) {
   constexpr int XS = C + 8;    // LDS row of a column's tokens in bf16 ...
   constexpr int DS = C + 4;    // ... and in fp32
@@ -287,30 +300,32 @@ __global__ __launch_bounds__(512, 2) void gdn_walk_kernel(GdnArgs g, int64_t n_s
   auto head_at = [&](int c) { return head0 + c * head_step; };
   // A column's tokens of V and y: 32 bits from the chunk's first one (64 rows of Hv Dv).
   const uint32_t row_bytes = uint32_t(g.Hv) * uint32_t(g.Dv) * 2u;
-  auto load_tri = [&](int c, int64_t part, u32x4_t (&f)[2][3]) {
+  auto load_tri = [&](int c, int64_t part, int planes, u32x4_t (&f)[2][3]) {
     const unsigned char* at = head_at(c) + part;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
 #pragma unroll
-      for (int p = 0; p < 3; ++p)
-        f[s][p] = *reinterpret_cast<const u32x4_t*>(at + (tri_at(w, s <= (w >> 1) ? s : 0) * 3 + p) * 1024 + uint32_t(lane * 16));
+      for (int p = 0; p < 3; ++p) {
+        if (p < planes)
+          f[s][p] = *reinterpret_cast<const u32x4_t*>(at + (tri_at(w, s <= (w >> 1) ? s : 0) * 3 + p) * 1024 + uint32_t(lane * 16));
+      }
     }
   };
-  // six partial products
-  auto mma6 = [&](const u32x4_t (&f)[3], const u32x4_t (&x)[3], f32x4_t (&a)[3]) {
+  // the partial products that `planes` planes can hold
+  auto mma_planes = [&](int planes, const u32x4_t (&f)[3], const u32x4_t (&x)[3], f32x4_t (&a)[3]) {
     a[0] = mma(f[0], x[0], a[0]);
     a[1] = mma(f[0], x[1], a[1]);
-    a[2] = mma(f[0], x[2], a[2]);
+    if (planes == 3) a[2] = mma(f[0], x[2], a[2]);
     a[1] = mma(f[1], x[0], a[1]);
-    a[2] = mma(f[1], x[1], a[2]);
-    a[2] = mma(f[2], x[0], a[2]);
+    if (planes == 3) a[2] = mma(f[1], x[1], a[2]);
+    if (planes == 3) a[2] = mma(f[2], x[0], a[2]);
   };
 
   if (wave >= 4) {  // outputs
     u32x4_t fa[2][3];
     f32x4_t fy;
     auto load = [&](int c) {
-      load_tri(c, kFragA, fa);
+      load_tri(c, kFragA, PO, fa);
       fy = *reinterpret_cast<const f32x4_t*>(head_at(c) + kFactors + (C + 16 * w) * 4 + uint32_t(hg * 16));
     };
     if (chunks) load(0);
@@ -334,7 +349,7 @@ __global__ __launch_bounds__(512, 2) void gdn_walk_kernel(GdnArgs g, int64_t n_s
             else split2(d1[2 * i - 4], d1[2 * i - 3], h, m, l);
             x[0][i] = h, x[1][i] = m, x[2][i] = l;
           }
-          mma6(fa[s], x, a);
+          mma_planes(PO, fa[s], x, a);
         }
         const f32x4_t q = (s_qs[0][nt][w][lane] + s_qs[1][nt][w][lane]) + (s_qs[2][nt][w][lane] + s_qs[3][nt][w][lane]);
         const f32x4_t y = a[0] + (a[1] + a[2]);
@@ -381,11 +396,13 @@ __global__ __launch_bounds__(512, 2) void gdn_walk_kernel(GdnArgs g, int64_t n_s
       st[dt][nt] = kept ? *reinterpret_cast<const f32x4_t*>(g.state_in + sbase + int64_t(16 * nt) * DK + 4 * dt)
                         : f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
-  auto put4 = [&](uint16_t (*pl)[16 * NT * XS], int nt, f32x4_t x) {  // rows 16 w + 4 hg .. +3 of column 16 nt + n
+  // rows 16 w + 4 hg .. +3 of a column stand where a fragment's lane finds its eight in one piece
+  const int pos = 32 * (w >> 1) + 8 * hg + 4 * (w & 1);
+  auto put4 = [&](uint16_t (*pl)[16 * NT * XS], int nt, f32x4_t x) {  // of column 16 nt + n
     uint32_t h0, m0, l0, h1, m1, l1;
     split2(x[0], x[1], h0, m0, l0);
     split2(x[2], x[3], h1, m1, l1);
-    const int at = (16 * nt + n) * XS + 16 * w + 4 * hg;
+    const int at = (16 * nt + n) * XS + pos;
     *reinterpret_cast<uint2*>(&pl[0][at]) = uint2{h0, h1};
     *reinterpret_cast<uint2*>(&pl[1][at]) = uint2{m0, m1};
     *reinterpret_cast<uint2*>(&pl[2][at]) = uint2{l0, l1};
@@ -449,7 +466,7 @@ __global__ __launch_bounds__(512, 2) void gdn_walk_kernel(GdnArgs g, int64_t n_s
     fx = load_fac(0, 0);
     load_v(0);
     load_rows(2, 0, fq);
-    load_tri(0, kFragM, fm);
+    load_tri(0, kFragM, 3, fm);
     fz = load_fac(0, 2);
     decay = load_decay(0);
     load_kt(0);
@@ -498,10 +515,10 @@ __global__ __launch_bounds__(512, 2) void gdn_walk_kernel(GdnArgs g, int64_t n_s
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int p = 2; p >= 0; --p) {
+        for (int p = PO - 1; p >= 0; --p) {
 #pragma unroll
           for (int t = t0; t < t0 + 2; ++t)
-            qs[nt][t] = mma(fq[t], sp[nt][p], p == 2 ? f32x4_t{0.f, 0.f, 0.f, 0.f} : qs[nt][t]);
+            qs[nt][t] = mma(fq[t], sp[nt][p], p == PO - 1 ? f32x4_t{0.f, 0.f, 0.f, 0.f} : qs[nt][t]);
         }
       }
     };
@@ -528,15 +545,15 @@ __global__ __launch_bounds__(512, 2) void gdn_walk_kernel(GdnArgs g, int64_t n_s
         if (s > (w >> 1)) continue;
         u32x4_t xp[3];
         get(s_x, nt, s, xp);
-        mma6(fm[s], xp, a);
+        mma_planes(3, fm[s], xp, a);
       }
       const f32x4_t d = a[0] + (a[1] + a[2]);
-      *reinterpret_cast<f32x4_t*>(&s_d[(16 * nt + n) * DS + 16 * w + 4 * hg]) = d;
+      *reinterpret_cast<f32x4_t*>(&s_d[(16 * nt + n) * DS + pos]) = d;
       put4(s_u, nt, d * fz);
 #pragma unroll
       for (int t = 0; t < 4; ++t) s_qs[w][nt][t][lane] = qs[nt][t];
     }
-    load_tri(cn, kFragM, fm);
+    load_tri(cn, kFragM, 3, fm);
     fz = load_fac(cn, 2);
     __syncthreads();
 #pragma unroll
@@ -571,22 +588,22 @@ __global__ __launch_bounds__(512, 2) void gdn_walk_kernel(GdnArgs g, int64_t n_s
 
 int64_t ws_slots(int64_t T, int64_t B) { return T / C + B + 1; }
 
-template <int DK, int NT>
+template <int DK, int NT, int PO>
 void walk(const GdnArgs& a, int64_t n, hipStream_t s) {
   const int slices = a.Dv / (16 * NT), heads = a.B * a.Hv;
   const uint32_t grid = uint32_t((heads + 7) / 8 * 8) * uint32_t(slices);
-  gdn_walk_kernel<DK, NT><<<dim3(grid), 512, 0, s>>>(a, n, slices, heads);
+  gdn_walk_kernel<DK, NT, PO><<<dim3(grid), 512, 0, s>>>(a, n, slices, heads);
 }
 
-template <int DK>
+template <int DK, int PO>
 int launch(const GdnArgs& a, hipStream_t s) {
   const int64_t n = ws_slots(a.T, a.B);
   const uint32_t chunks = uint32_t((int64_t(a.max_len < a.T ? a.max_len : a.T) + C - 1) / C);
-  gdn_prep_kernel<DK><<<dim3(chunks ? chunks : 1, uint32_t(a.Hv), uint32_t(a.B)), 256, 0, s>>>(a, n);
+  gdn_prep_kernel<DK, PO><<<dim3(chunks ? chunks : 1, uint32_t(a.Hv), uint32_t(a.B)), 256, 0, s>>>(a, n);
   if (hipGetLastError() != hipSuccess) return 6;
   // 32 columns a block share its operands' loads where 16 would more than fill the GPU
-  if (int64_t(a.B) * a.Hv * (a.Dv / 16) > int64_t(device_cus())) walk<DK, 2>(a, n, s);
-  else walk<DK, 1>(a, n, s);
+  if (int64_t(a.B) * a.Hv * (a.Dv / 16) > int64_t(device_cus())) walk<DK, 2, PO>(a, n, s);
+  else walk<DK, 1, PO>(a, n, s);
   return hipGetLastError() == hipSuccess ? 0 : 6;
 }
 
@@ -596,6 +613,9 @@ uint64_t gdn_chunk_workspace(int64_t T, int64_t B, int64_t Hk, int64_t Hv, int64
   return uint64_t(ws_slots(T, B)) * uint64_t(Hv * kHeadBytes + Hk * key_bytes(Dk));
 }
 
-int launch_gdn_chunk(const GdnArgs& a, hipStream_t s) { return a.Dk == 64 ? launch<64>(a, s) : launch<128>(a, s); }
+int launch_gdn_chunk(const GdnArgs& a, hipStream_t s) {
+  if (a.f32_out) return a.Dk == 64 ? launch<64, 3>(a, s) : launch<128, 3>(a, s);
+  return a.Dk == 64 ? launch<64, 2>(a, s) : launch<128, 2>(a, s);
+}
 
 }  // namespace qmm
