@@ -284,6 +284,49 @@ def test_a_long_context_is_split_and_joined_the_same_every_time():
         assert_within(bf16_bits_to_f64(outs[0])[0, a], ref, 1.01 * tol[0, a], f"head {a}")
 
 
+def check_long(rng, q_lens, kv_lens, n_q, n_kv, hd, page, causal=True, window=0):
+    """Long contexts whose tables name a few whole pages again and again."""
+    c = mix.Cache(5, n_kv, page, hd)
+    for slot in range(5 * page):
+        for h in range(n_kv):
+            c.put(slot, h, rng.standard_normal(hd).astype(np.float32), rng.standard_normal(hd).astype(np.float32))
+    table = rng.integers(0, 5, (len(kv_lens), -(-max(kv_lens) // page))).astype(np.int32)
+    starts = np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32)
+    T, max_q = int(starts[-1]), max(q_lens)
+    qb, qv = bf16(rng.standard_normal((T, n_q, hd)))
+    out = Guarded((T, n_q, hd), False)
+    need = qmm.qmm_kv4_attn_workspace_bytes(T, len(kv_lens), max_q, n_q, n_kv, hd, table.shape[1] * page)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    qmm.qmm_kv4_attn(dev(qb), gpu_cache(c), dev(table), dev(np.array(kv_lens, np.int32)), out.t, ws, q_start=dev(starts),
+                     max_q=max_q, causal=causal, window=window)
+    torch.cuda.synchronize()
+    got = bf16_bits_to_f64(out.values())
+    for b, (n, kv) in enumerate(zip(q_lens, kv_lens)):
+        if kv == max(kv_lens) or b % 16 == 0:
+            sl = slice(starts[b], starts[b + 1])
+            ref, tol = mix.attention(qv[sl], c, table[b], kv, n, hd ** -0.5, causal, window, None)
+            assert_within(got[sl], ref, tol, f"sequence {b} q {n} kv {kv}")
+
+
+@pytest.mark.parametrize("hd,page", [(128, 16), (64, 32), (256, 16)])
+def test_long_contexts_of_single_tokens(hd, page):
+    """More sequences than the GPU has room for, one of them with hundreds of steps for each wave."""
+    rng = np.random.default_rng([41, hd])
+    lens = rng.integers(0, 70, 300).tolist()
+    lens[123] = 13003
+    check_long(rng, [1] * 300, lens, 16, 8, hd, page)
+
+
+@pytest.mark.parametrize("hd,page", [(128, 16), (64, 64), (256, 16)])
+def test_long_contexts_of_prompts(hd, page):
+    rng = np.random.default_rng([42, hd])
+    check_long(rng, [70], [4900], 3, 1, hd, page)                    # split over the keys and joined
+    check_long(rng, [90, 3], [3300, 2700], 2, 1, hd, page, window=1500)
+    lens = rng.integers(33, 90, 34).tolist()
+    lens[30] = 3471
+    check_long(rng, [33] * 34, lens, 16, 8, hd, page)                # one block walks all of them
+
+
 def test_append_then_attend_step_by_step():
     """A sequence's prompt and three single tokens after it through append and attention."""
     rng = np.random.default_rng(17)
@@ -402,6 +445,13 @@ def test_gdn_prompts(dk, dv, lens):
     rng = np.random.default_rng([dk, dv, len(lens), lens[0]])
     check_gdn(rng, lens, 2, 4, dk, dv, f32=True)
     check_gdn(rng, lens, 1, 3, dk, dv, in_place=True, no_slot=0 if len(lens) > 1 else None)
+
+
+@pytest.mark.parametrize("dk,dv,f32", [(128, 128, False), (128, 128, True), (64, 128, False), (128, 64, True)])
+def test_gdn_prompts_of_many_heads(dk, dv, f32):
+    """More heads than the GPU takes at 16 columns a block."""
+    rng = np.random.default_rng([dk, dv, 43])
+    check_gdn(rng, [70, 0, 129, 33], 8, 24, dk, dv, f32=f32, no_slot=3)
 
 
 def test_gdn_prompt_corners():
