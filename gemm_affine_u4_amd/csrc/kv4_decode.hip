@@ -547,11 +547,14 @@ int join_hd(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t s) {
 
 }  // namespace
 
-// Few queries: splits of at least 1024 keys (none up to 2048), one block per compute unit for few
-// long sequences (131071 keys x 4 heads: 64 splits 36 us, 128 splits 40 us: a block's fixed
-// part is ~6 us), and up to 4 for many, whose lengths may differ (64 sequences of 100 to
-// 16000 keys x 8 heads: 141 us in 4, 156 us in 2).  8 waves a block where that leaves half of
-// the units idle (517 keys x 8 heads: 8.3 against 8.8 us).
+// Few queries: one block per compute unit for few long sequences (131071 keys x 4 heads: 64
+// splits 36 us, 128 splits 40 us: a block's fixed part is ~6 us), and up to 4 for many, whose
+// lengths may differ (64 sequences of 100 to 16000 keys x 8 heads: 141 us in 4, 156 us in 2).
+// Splits of at least 1024 keys, and down to 128 while half of the units would idle (one
+// sequence of 4096 keys x 8 heads: 10.3 against 14.1 us; four of 2000: 10.9 against 15.4).  None up to
+// 768 keys or two splits, where the second launch costs more (517 keys: 8.3 against 10.0 us;
+// 16 sequences of 2000 keys, 12 queries each: 29 against 50).  8 waves a block
+// where that leaves half of the units idle (517 keys x 8 heads: 8.3 against 8.8 us).
 // Prompts: splits only where the blocks would not fill half of the GPU.
 AttnPlan attn_plan(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t max_kv) {
   const int64_t rows = max_q * (n_q / n_kv), cus = device_cus();
@@ -561,9 +564,10 @@ AttnPlan attn_plan(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t 
   int64_t ns;
   if (p.rows == 16) {
     p.shift = 5, p.keys = 1024;
+    while (p.keys > 128 && blocks * ((max_kv + p.keys - 1) / p.keys) <= cus / 2) p.keys /= 2;
     ns = 8 * cus / blocks < 4 ? 8 * cus / blocks : 4;
     if (ns < cus / blocks) ns = cus / blocks;
-    if (max_kv <= 2 * p.keys) ns = 1;
+    if (max_kv <= 768 || max_kv <= 2 * p.keys) ns = 1;
   } else {
     p.shift = 6, p.keys = 512;
     ns = blocks >= cus ? 1 : (2 * cus + blocks - 1) / blocks;
