@@ -64,7 +64,7 @@ struct AttnPlan {
   int keys;     // ... of at least this many keys
 };
 constexpr int kAttnRows = 128;
-AttnPlan attn_plan(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t max_kv);
+AttnPlan attn_plan(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t hd, int64_t max_kv);
 
 struct AttnSplit {
   int count, begin, end;  // splits of the block's keys; this split's tiles

@@ -40,7 +40,10 @@ namespace {
 constexpr int kTile = 32;  // keys of a wave's step
 constexpr float kFloor = -1e30f;  // maximum of a row that has seen no key yet
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int64_t kDecodeRows = 64;  // calls of up to this many rows per KV head run here
+// Calls of up to this many rows per KV head run here.  Against the prompts' kernel: 16 sequences of
+// 2000 keys x 8 heads x 128: 120 rows 49 against 67 us, 160 rows 60 against 54; four of 8000
+// keys x 4 heads x 256: 48 rows 34 against 41, 78 rows 52 against 42.
+constexpr int64_t decode_rows(int64_t hd) { return hd == 256 ? 64 : 128; }
 
 template <int HD>
 struct Buf {
@@ -555,11 +558,12 @@ int join_hd(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t s) {
 // 768 keys or two splits, where the second launch costs more (517 keys: 8.3 against 10.0 us;
 // 16 sequences of 2000 keys, 12 queries each: 29 against 50).  8 waves a block
 // where that leaves half of the units idle (517 keys x 8 heads: 8.3 against 8.8 us).
-// Prompts: splits only where the blocks would not fill half of the GPU.
-AttnPlan attn_plan(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t max_kv) {
+// Prompts: as many splits of 512 keys as leave one block to a unit (512 queries on 2048 keys,
+// 40/8 heads x 128: 50 us; on 8000 keys, 24/4 heads x 256: 182 us, unsplit 289, twice as many 204).
+AttnPlan attn_plan(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t hd, int64_t max_kv) {
   const int64_t rows = max_q * (n_q / n_kv), cus = device_cus();
   AttnPlan p;
-  p.rows = rows <= kDecodeRows ? 16 : kAttnRows;
+  p.rows = rows <= decode_rows(hd) ? 16 : kAttnRows;
   const int64_t blocks = B * n_kv * ((rows + p.rows - 1) / p.rows);
   int64_t ns;
   if (p.rows == 16) {
@@ -570,7 +574,7 @@ AttnPlan attn_plan(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t 
     if (max_kv <= 768 || max_kv <= 2 * p.keys) ns = 1;
   } else {
     p.shift = 6, p.keys = 512;
-    ns = blocks >= cus ? 1 : (2 * cus + blocks - 1) / blocks;
+    ns = cus / blocks;
   }
   const int64_t most = (max_kv + p.keys - 1) / p.keys;
   ns = ns > most ? most : ns;
@@ -593,12 +597,12 @@ int launch_kv4_join(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t s) {
 
 uint64_t kv4_attn_workspace(int64_t T, int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t hd,
                             int64_t max_kv) {
-  const uint64_t ns = uint64_t(attn_plan(B, max_q, n_q, n_kv, max_kv).nsplit);
+  const uint64_t ns = uint64_t(attn_plan(B, max_q, n_q, n_kv, hd, max_kv).nsplit);
   return ns > 1 ? ns * uint64_t(T) * uint64_t(n_q) * uint64_t(hd + 2) * 4 : 256;
 }
 
 int launch_kv4_attn(const Kv4AttnArgs& a, hipStream_t s) {
-  const AttnPlan p = attn_plan(a.B, a.max_q, a.n_q, a.c.n_kv, int64_t(a.max_pages) << a.c.page_shift);
+  const AttnPlan p = attn_plan(a.B, a.max_q, a.n_q, a.c.n_kv, a.c.hd, int64_t(a.max_pages) << a.c.page_shift);
   const int st = p.rows == 16 ? launch_kv4_decode(a, p, s) : launch_kv4_prefill(a, p, s);
   return st || p.nsplit == 1 ? st : launch_kv4_join(a, p, s);
 }

@@ -325,6 +325,15 @@ def test_long_contexts_of_prompts(hd, page):
     lens = rng.integers(33, 90, 34).tolist()
     lens[30] = 3471
     check_long(rng, [33] * 34, lens, 16, 8, hd, page)                # one block walks all of them
+    check_long(rng, [66] * 34, [n + 33 for n in lens], 16, 8, hd, page)
+
+
+@pytest.mark.parametrize("hd,rows", [(64, 128), (64, 129), (128, 128), (128, 129), (256, 64), (256, 65)])
+def test_attention_where_the_kernels_meet(hd, rows):
+    """The most rows per KV head that the few-query kernel takes, and one more."""
+    rng = np.random.default_rng([44, hd, rows])
+    check_attention(rng, [rows, 5], [rows + 140, 70], 1, 1, hd, 16, gated=True)
+    check_attention(rng, [rows], [rows - 9], 2, 2, hd, 32, window=50)
 
 
 def test_append_then_attend_step_by_step():
