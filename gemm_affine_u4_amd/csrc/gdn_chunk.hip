@@ -12,8 +12,9 @@
 // Precision.  Keys, queries and values are bf16 and enter exactly (their norms are factors
 // of rows).  An fp32 factor x enters as h + m + l, three bf16 values that hold its 24 bits; a
 // product of two such factors takes the six partial products down to 2^-24.  What only a
-// bf16 output reads (scores, D as their factor, S as Q's) enters as h + m: 2^-16 relative, 1/128 of
-// that output's own rounding; an fp32 output takes l too (PO planes).  T comes from
+// bf16 output reads (scores, D as their factor, S as Q's) enters as h + m: each part left out is at
+// most 2^-16 of its product, 1/256 of that output's own rounding; an fp32 output takes l too (PO
+// planes; the state always does).  T comes from
 // forward substitution and fp32 matrix products; sums are fp32, the running sum of g fp64.
 //
 // Bound: latency of the chunk's dependent products (three barriers a chunk, ~1.7 us for 16

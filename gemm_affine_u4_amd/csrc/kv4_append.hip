@@ -10,6 +10,10 @@
 // group of 64 exactly 8 lanes (its extremes meet by DPP), a key word one lane.  A wave
 // keeps one token: its lanes' cos and sin (the same dims for every head) are read once and
 // stay in registers over the token's heads; small calls take one step of heads per wave.
+//
+// Measured, 40/8 heads x 128: 16 tokens 4.4 us; 8192 tokens 64 us (3.9 TB/s; 45 us where inputs are
+// in the last-level cache; writing q past the caches took 61 us but the attention that reads it
+// next would miss).  1021 fp32 tokens of 24/4 heads x 256: 11.7 us, 4.4 TB/s.
 #include <hip/hip_runtime.h>
 
 #include "kv4_device.h"

@@ -16,6 +16,10 @@
 // A step is ordered by hand (step() below): a wave issues in order, so vector work placed
 // behind a run of matrix instructions waits for all of them, while one placed between two
 // runs beside them.
+//
+// Measured: a prompt of 2048, 40/8 heads x 128, causal: 63 us, 0.68 PFLOP/s (before the hand order
+// 77, with tiles dequantized by each wave for itself 129); five prompts on up to 9000 keys,
+// 24/4 heads x 256: 456 us, 0.61 PFLOP/s.  8 waves, 16-column tiles and 32-key tiles were slower.
 #include <hip/hip_runtime.h>
 
 #include "kv4_attn.h"

@@ -89,13 +89,14 @@ int qmm_kv4_append(const qmm_kv4_cache* cache, const void* k, const void* v, int
  *   causal = 1: query j of n (0-based) of a sequence stands at p = kv_len - n + j and sees
  *     keys t <= p, with window > 0 only t > p - window.  causal = 0 (window must be 0):
  *     every query sees all keys.
- *   A query that sees no key gives zeros.  scale > 0 and finite; |q| below 2^100.
+ *   A query that sees no key gives zeros.  scale > 0 and finite; |q| below 2^100, and for
+ *   prompts scale * |q| * log2(e) below 65504 (larger ones are taken as that).
  *   gate (nullable) [T][n_q_heads][head_dim] bf16: out is multiplied by
  *     1 / (1 + exp(-gate)) (the output gate that qmm_fused_qkv_rope writes).
  * Sums, maxima and the softmax are fp32; codes enter the products exactly, probabilities
  * times scale (few queries) or dequantized keys, values and probabilities (prompts) are
  * rounded to fp16 (values of a magnitude above 65504 do not occur in a cache that
- * qmm_kv4_append wrote).  The same call gives the same bits every time.
+ * qmm_kv4_append wrote), for prompts the scaled queries too.  The same call gives the same bits every time.
  * workspace: 256-byte aligned, at least qmm_kv4_attn_workspace_bytes of the same T, B, max_q,
  * heads and max_kv = max_pages * page_size (0 for sizes out of range; always > 0 otherwise).
  */
@@ -125,7 +126,9 @@ int qmm_kv4_attn(const uint16_t* q, int64_t T, const int32_t* q_start, const int
  *   Dk and Dv 64 or 128.
  * The state and all sums are fp32.  Sequences of up to 16 tokens (max_len) run token by
  * token; longer ones in chunks of 64 tokens on the matrix cores with each fp32 factor as
- * a sum of three bf16 values.  The same call gives the same bits every time.
+ * a sum of three bf16 values (two where only a bf16 y reads it).  Inputs are finite: in a
+ * chunk an infinite v or q would reach the outputs of earlier tokens of the chunk too.
+ * The same call gives the same bits every time.
  * workspace: 256-byte aligned, at least qmm_gdn_workspace_bytes of the same sizes (0 for sizes
  * out of range; always > 0 otherwise).
  */

@@ -485,6 +485,30 @@ def test_gdn_prompt_corners():
     assert_within(y.cpu().numpy(), ry, ty, "y")
 
 
+def test_gdn_prompt_then_tokens_through_one_state():
+    """A sequence cut into calls of both kernels, its state in place, against one pass over all of it."""
+    rng = np.random.default_rng(45)
+    hk, hv, d, cuts = 2, 4, 128, [100, 1, 1, 7, 70, 1]
+    T = sum(cuts)
+    (qb, qv), (kb, kv), (vb, vv) = (bf16(rng.standard_normal((T, h, d))) for h in (hk, hk, hv))
+    g = (-0.1 * rng.exponential(size=(T, hv))).astype(np.float32)
+    beta = rng.uniform(0, 1, (T, hv)).astype(np.float32)
+    s0 = rng.standard_normal((1, hv, d, d)).astype(np.float32)
+    state, y = dev(s0), torch.zeros(T, hv, d, device="cuda")
+    at = 0
+    for n in cuts:
+        sl = slice(at, at + n)
+        ws = torch.empty(qmm.qmm_gdn_workspace_bytes(n, 1, n, hk, hv, d, d), dtype=torch.uint8, device="cuda")
+        qmm.qmm_gdn(dev(qb[sl]), dev(kb[sl]), dev(vb[sl]), dev(g[sl]), dev(beta[sl]), state, y[sl], ws,
+                    seq_start=dev(np.array([0, n], np.int32)), max_len=n, l2norm=True)
+        at += n
+    torch.cuda.synchronize()
+    ry, rs = mix.gdn(qv, kv, vv, g, beta, s0[0], d ** -0.5, True)
+    ts, ty = gdn_tol(T, d, s0[0], vv, rs, 1.0, d ** -0.5)
+    assert_within(y.cpu().numpy(), ry, ty + np.abs(ry) * 2.0 ** -24, "y")
+    assert_within(state[0].cpu().numpy(), rs, ts, "state")
+
+
 @pytest.mark.parametrize("lens", [[1, 1, 1], [100, 30]])
 def test_gdn_in_a_graph_and_on_another_stream(lens):
     rng = np.random.default_rng(24)
