@@ -111,7 +111,8 @@ __global__ __launch_bounds__(256, 4) void gdn_prep_kernel(GdnArgs g, int64_t n_s
     const bool in = lane < left;
     const int64_t at = (tok0 + (in ? lane : left - 1)) * g.Hv + hv;
     s_beta[lane] = in ? g.beta[at] : 0.f;
-    double x = in ? double(g.g[at]) : 0.0;
+    // e^-200 is 0 in fp32 as all below it are: held there, the chunk's sums stay exact and finite
+    double x = in ? double(fmaxf(g.g[at], -200.f)) : 0.0;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
       const double y = __shfl_up(x, o);

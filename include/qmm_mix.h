@@ -112,7 +112,7 @@ int qmm_kv4_attn(const uint16_t* q, int64_t T, const int32_t* q_start, const int
  * sequence and value head, with a state S of Dk x Dv and, per token,
  *   S <- exp(g) S;   S <- S + k (beta (v - S^T k))^T;   y = S^T (scale q).
  *   q, k [T][Hk][Dk] bf16, v [T][Hv][Dv] bf16, g and beta fp32 [T][Hv] (g the natural
- *     logarithm of the decay, <= 0), y [T][Hv][Dv] bf16 or fp32 per out_dtype; Hv a multiple of Hk,
+ *     logarithm of the decay, <= 0; -infinity forgets all before the token), y [T][Hv][Dv] bf16 or fp32 per out_dtype; Hv a multiple of Hk,
  *     value head a reading key head a / (Hv / Hk).
  *   l2norm = 1: q and k are divided by sqrt(sum of squares + 1e-6) first.
  *   seq_start int32 [B+1] as q_start above (rows behind the last sequence are left as they

@@ -336,6 +336,35 @@ def test_attention_where_the_kernels_meet(hd, rows):
     check_attention(rng, [rows], [rows - 9], 2, 2, hd, 32, window=50)
 
 
+def test_a_cache_past_32_bit_offsets():
+    """The last pages of a pool whose code arrays are larger than 4 GiB each."""
+    rng = np.random.default_rng(47)
+    n_q, n_kv, hd, page, n = 16, 8, 256, 64, 100
+    pages = (1 << 32) // (n_kv * page * hd // 2) + 3
+    shapes = qmm.kv4_cache_shapes(pages, n_kv, page, hd)
+    g = qmm.KV4Cache(*[torch.zeros(s, dtype=t, device="cuda")
+                       for s, t in zip(shapes.values(), (torch.int32, torch.int32, torch.int16, torch.int32))])
+    c = mix.Cache(2, n_kv, page, hd)
+    q, k, v = (rng.standard_normal((n, h, hd)).astype(np.float32) for h in (n_q, n_kv, n_kv))
+    small = np.array([[1, 0]], np.int32)
+    table = np.array([[pages - 1, pages - 2]], np.int32)
+    pos = np.arange(n)
+    qmm.qmm_kv4_append(g, dev(k), dev(v), dev((table[0, pos // page] * page + pos % page).astype(np.int32)))
+    for t in range(n):
+        for h in range(n_kv):
+            c.put(int(small[0, t // page]) * page + t % page, h, k[t, h], v[t, h])
+    qb, qv = bf16(q)
+    for first in (n - 1, 0):  # one token, then the whole prompt
+        m = n - first
+        out = Guarded((m, n_q, hd), False)
+        ws = torch.empty(qmm.qmm_kv4_attn_workspace_bytes(m, 1, m, n_q, n_kv, hd, 2 * page), dtype=torch.uint8, device="cuda")
+        qmm.qmm_kv4_attn(dev(qb[first:]), g, dev(table), dev(np.array([n], np.int32)), out.t, ws,
+                         q_start=dev(np.array([0, m], np.int32)), max_q=m)
+        torch.cuda.synchronize()
+        ref, tol = mix.attention(qv[first:], c, small[0], n, m, hd ** -0.5)
+        assert_within(bf16_bits_to_f64(out.values()), ref, tol, f"{m} queries")
+
+
 def test_append_then_attend_step_by_step():
     """A sequence's prompt and three single tokens after it through append and attention."""
     rng = np.random.default_rng(17)
@@ -483,6 +512,31 @@ def test_gdn_prompt_corners():
     ts, ty = gdn_tol(T, 128, np.zeros((1, 128, 128)), vv, rs, 1.0, 128 ** -0.5)
     assert_within(state.cpu().numpy()[0], rs, ts, "state")
     assert_within(y.cpu().numpy(), ry, ty, "y")
+
+
+@pytest.mark.parametrize("n", [12, 150])
+@pytest.mark.parametrize("low", [-1e4, -1e9, float(np.finfo(np.float32).min), -np.inf])
+def test_gdn_forgets_at_the_lowest_decays(n, low):
+    """A log decay of any size below fp32's range ends what came before and nothing else."""
+    rng = np.random.default_rng(46)
+    hk, hv, d = 1, 2, 128
+    (qb, qv), (kb, kv), (vb, vv) = (bf16(rng.standard_normal((n, h, d))) for h in (hk, hk, hv))
+    g = (-0.1 * rng.exponential(size=(n, hv))).astype(np.float32)
+    cut = n - 5
+    g[cut], g[3] = low, low
+    beta = rng.uniform(0, 1, (n, hv)).astype(np.float32)
+    s0 = rng.standard_normal((1, hv, d, d)).astype(np.float32)
+    state, y = dev(s0), torch.zeros(n, hv, d, device="cuda")
+    ws = torch.empty(qmm.qmm_gdn_workspace_bytes(n, 1, n, hk, hv, d, d), dtype=torch.uint8, device="cuda")
+    qmm.qmm_gdn(dev(qb), dev(kb), dev(vb), dev(g), dev(beta), state, y, ws, seq_start=dev(np.array([0, n], np.int32)),
+                max_len=n, l2norm=True)
+    torch.cuda.synchronize()
+    ry, rs = mix.gdn(qv, kv, vv, np.maximum(g, -1e3), beta, s0[0], d ** -0.5, True)
+    ts, ty = gdn_tol(n, d, s0[0], vv, rs, 1.0, d ** -0.5)
+    assert_within(y.cpu().numpy(), ry, ty + np.abs(ry) * 2.0 ** -24, "y")
+    assert_within(state[0].cpu().numpy(), rs, ts, "state")
+    _, alone = mix.gdn(qv[cut:], kv[cut:], vv[cut:], np.maximum(g[cut:], -1e3), beta[cut:], np.zeros_like(s0[0]), d ** -0.5, True)
+    assert_within(state[0].cpu().numpy(), alone, ts, "state of the last tokens alone")
 
 
 def test_gdn_prompt_then_tokens_through_one_state():
