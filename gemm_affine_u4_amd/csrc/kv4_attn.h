@@ -55,6 +55,20 @@ __device__ __forceinline__ AttnSeq attn_seq(const Kv4AttnArgs& g, int b) {
   return s;
 }
 
+// The sequence of rank `rank` by falling number of keys (up to 64 of them; more even out by
+// themselves).  Blocks start in that order, so that the last ones to end are short.
+__device__ __forceinline__ int attn_longest_first(const Kv4AttnArgs& g, int rank, int lane) {
+  const int n = int(gridDim.z);
+  if (n == 1 || n > 64) return rank;
+  const int len = lane < n ? attn_seq(g, lane).kv_len : -1;
+  int before = 0;
+  for (int j = 0; j < n; ++j) {
+    const int other = __builtin_amdgcn_readlane(len, j);
+    before += other > len || (other == len && j < lane);
+  }
+  return __ffsll(static_cast<unsigned long long>(__ballot(lane < n && before == rank))) - 1;
+}
+
 // How a call is cut: a function of its sizes alone (host), the same for its workspace.
 struct AttnPlan {
   int rows;     // (query, head) rows of a block: 16 (kv4_decode.hip) or kAttnRows (kv4_prefill.hip)

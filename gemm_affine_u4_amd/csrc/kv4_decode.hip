@@ -11,8 +11,9 @@
 // matrix cores take exactly, so a code costs half a mask instruction and no conversion; the
 // powers of two go into q (1/16 for the odd places) and into the final factor.
 //
-// Measured: 64 sequences of 100 to 16000 keys, 24/8 heads x 128: 136 us, 5.1 TB/s of cache;
-// one of 131071 keys, 40/4 heads x 256: 34 us, 4.4 TB/s; one of 517 keys: 8.0 us.
+// Measured: 64 sequences of 100 to 16000 keys, 40/8 heads x 128: 126 us, 5.5 TB/s of cache (in the
+// order given, not longest first: 135); one of 131071 keys, 24/4 heads x 256: 34 us, 4.4 TB/s; one of
+// 517 keys: 8.0 us.
 //
 // Bound: the cache's bytes (HBM) for long contexts, launch and latency for short ones.
 //
@@ -101,7 +102,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kv4_decode_kernel(Kv4AttnArgs g, i
   constexpr int NG = B::NG, NKL = B::NKL, R = B::R;
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, hg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int split = blockIdx.x, b = blockIdx.z;
+  const int split = blockIdx.x, b = attn_longest_first(g, int(blockIdx.z), tid & 63);
   const int kvh = blockIdx.y % g.c.n_kv, rt = blockIdx.y / g.c.n_kv;
 
   const AttnSeq sq = attn_seq(g, b);

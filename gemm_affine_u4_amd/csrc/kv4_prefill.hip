@@ -19,7 +19,7 @@
 //
 // Measured: a prompt of 2048, 40/8 heads x 128, causal: 63 us, 0.68 PFLOP/s (before the hand order
 // 77, with tiles dequantized by each wave for itself 129); five prompts on up to 9000 keys,
-// 24/4 heads x 256: 456 us, 0.61 PFLOP/s.  8 waves, 16-column tiles and 32-key tiles were slower.
+// 24/4 heads x 256: 395 us, 0.71 PFLOP/s (sequences in the order given: 456).  8 waves, 16-column tiles and 32-key tiles were slower.
 #include <hip/hip_runtime.h>
 
 #include "kv4_attn.h"
@@ -90,7 +90,7 @@ __global__ __launch_bounds__(NW * 64, HD == 256 ? 1 : 2) void kv4_prefill_kernel
   constexpr int NG = HD / 64, WPL = U::WPL, PER = U::PER, UK = U::UK, ROWS = kAttnRows, OT = HD / 32;
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, hh = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int split = blockIdx.x, b = blockIdx.z;
+  const int split = blockIdx.x, b = attn_longest_first(g, int(blockIdx.z), tid & 63);
   const int kvh = blockIdx.y % g.c.n_kv, rt = tiles - 1 - int(blockIdx.y) / g.c.n_kv;  // longest rows first
 
   const AttnSeq sq = attn_seq(g, b);
