@@ -527,6 +527,35 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs g, int group,
   }
 }
 
+// The same for prompts, whose rows are many and whose splits are few: HD / 4 lanes a row.
+template <int HD>
+__global__ __launch_bounds__(256) void kv4_join_rows_kernel(Kv4AttnArgs g, int group, AttnPlan plan) {
+  constexpr int LPR = HD / 4, RPB = 256 / LPR;  // lanes of a row, rows of a block (all of one row block)
+  const int b = blockIdx.z, kvh = blockIdx.y, rr = int(blockIdx.x) * RPB + int(threadIdx.x) / LPR;
+  const int d = (threadIdx.x % LPR) * 4;
+  const AttnSeq sq = attn_seq(g, b);
+  if (rr >= sq.q_len * group) return;
+  const int row0 = rr / plan.rows * plan.rows, rows = sq.q_len * group - row0;
+  const int count = attn_split(g, sq, row0, rows < plan.rows ? rows : plan.rows, group, plan, 0).count;
+  if (count == 1) return;
+  const int64_t row = (int64_t(sq.q0) + rr / group) * g.n_q + kvh * group + rr % group, R0 = g.T * g.n_q;
+  const float* po = static_cast<const float*>(g.ws);
+  const float* pm = po + plan.nsplit * R0 * HD;
+  float mm = -INFINITY, l = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < count; ++s) mm = fmaxf(mm, pm[(s * R0 + row) * 2]);
+  float4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < count; ++s) {
+    const int64_t at = s * R0 + row;
+    const float f = exp2_hw(pm[at * 2] - mm);
+    const float4 v = *reinterpret_cast<const float4*>(po + at * HD + d);
+    l = fmaf(pm[at * 2 + 1], f, l);
+    o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+  }
+  attn_store4(g, row * HD + d, o, l);
+}
+
 template <int HD>
 int launch_hd(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t s) {
   const int group = a.n_q / a.c.n_kv;
@@ -545,7 +574,11 @@ int launch_hd(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t s) {
 template <int HD>
 int join_hd(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t s) {
   const int group = a.n_q / a.c.n_kv;
-  kv4_join_kernel<HD><<<dim3(uint32_t(a.max_q * group), uint32_t(a.c.n_kv), uint32_t(a.B)), 256, 0, s>>>(a, group, p);
+  const uint32_t rows = uint32_t(a.max_q * group), rpb = 1024 / HD;
+  if (p.rows == 16)
+    kv4_join_kernel<HD><<<dim3(rows, uint32_t(a.c.n_kv), uint32_t(a.B)), 256, 0, s>>>(a, group, p);
+  else
+    kv4_join_rows_kernel<HD><<<dim3((rows + rpb - 1) / rpb, uint32_t(a.c.n_kv), uint32_t(a.B)), 256, 0, s>>>(a, group, p);
   return hipGetLastError() == hipSuccess ? 0 : 6;
 }
 
@@ -559,8 +592,10 @@ int join_hd(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t s) {
 // 768 keys or two splits, where the second launch costs more (517 keys: 8.3 against 10.0 us;
 // 16 sequences of 2000 keys, 12 queries each: 29 against 50).  8 waves a block
 // where that leaves half of the units idle (517 keys x 8 heads: 8.3 against 8.8 us).
-// Prompts: as many splits of 512 keys as leave one block to a unit (512 queries on 2048 keys,
-// 40/8 heads x 128: 50 us; on 8000 keys, 24/4 heads x 256: 182 us, unsplit 289, twice as many 204).
+// Prompts: as many splits of 512 keys as leave one block to a unit (512 queries on 8000 keys,
+// 24/4 heads x 256: 165 us, unsplit 289), or up to 128 dims, where a unit holds two, as many of
+// 2048 keys as leave two (40/8 heads x 128: 115 us, one 160; with shorter splits of many blocks
+// the join costs more: 4 x 200 queries on 2000 keys 62 against 54 us).
 AttnPlan attn_plan(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t hd, int64_t max_kv) {
   const int64_t rows = max_q * (n_q / n_kv), cus = device_cus();
   AttnPlan p;
@@ -576,6 +611,10 @@ AttnPlan attn_plan(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t 
   } else {
     p.shift = 6, p.keys = 512;
     ns = cus / blocks;
+    if (hd < 256) {
+      const int64_t two = 2 * cus / blocks, longs = (max_kv + 2047) / 2048;
+      if ((two < longs ? two : longs) > ns) ns = two, p.keys = 2048;
+    }
   }
   const int64_t most = (max_kv + p.keys - 1) / p.keys;
   ns = ns > most ? most : ns;
