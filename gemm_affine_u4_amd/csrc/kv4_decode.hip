@@ -11,8 +11,8 @@
 // matrix cores take exactly, so a code costs half a mask instruction and no conversion; the
 // powers of two go into q (1/16 for the odd places) and into the final factor.
 //
-// Measured: 64 sequences of 100 to 16000 keys, 40/8 heads x 128: 126 us, 5.5 TB/s of cache (in the
-// order given, not longest first: 135); one of 131071 keys, 24/4 heads x 256: 34 us, 4.4 TB/s; one of
+// Measured: 64 sequences of 100 to 16000 keys, 40/8 heads x 128: 124 us, 5.6 TB/s of cache (in the
+// order given, not longest first: 133); one of 131071 keys, 24/4 heads x 256: 34 us, 4.4 TB/s; one of
 // 517 keys: 8.0 us.
 //
 // Bound: the cache's bytes (HBM) for long contexts, launch and latency for short ones.
@@ -527,7 +527,7 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs g, int group,
   }
 }
 
-// The same for prompts, whose rows are many and whose splits are few: HD / 4 lanes a row.
+// The same for many rows or few splits: HD / 4 lanes a row.
 template <int HD>
 __global__ __launch_bounds__(256) void kv4_join_rows_kernel(Kv4AttnArgs g, int group, AttnPlan plan) {
   constexpr int LPR = HD / 4, RPB = 256 / LPR;  // lanes of a row, rows of a block (all of one row block)
@@ -575,7 +575,9 @@ template <int HD>
 int join_hd(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t s) {
   const int group = a.n_q / a.c.n_kv;
   const uint32_t rows = uint32_t(a.max_q * group), rpb = 1024 / HD;
-  if (p.rows == 16)
+  // few splits: HD / 4 lanes a row go through them one by one (16 sequences of 4096 keys: 22.7
+  // against 23.9 us); at 16 splits the waves of a row are faster (2000 keys: 10.0 against 12.0)
+  if (p.rows == 16 && p.nsplit > 8)
     kv4_join_kernel<HD><<<dim3(rows, uint32_t(a.c.n_kv), uint32_t(a.B)), 256, 0, s>>>(a, group, p);
   else
     kv4_join_rows_kernel<HD><<<dim3((rows + rpb - 1) / rpb, uint32_t(a.c.n_kv), uint32_t(a.B)), 256, 0, s>>>(a, group, p);
