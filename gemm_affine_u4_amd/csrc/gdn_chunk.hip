@@ -390,7 +390,6 @@ __global__ __launch_bounds__(512, 2) void gdn_walk_kernel(GdnArgs g, int64_t n_s
     return;
   }
 
-  __builtin_amdgcn_s_setprio(2);  // the chain that the sequence waits for
   // state: row 4 hg + i of tile dt is dim w DK/4 + 4 DT hg + 4 dt + i, column v0 + 16 nt + n
   const int64_t sbase = ((int64_t(kept ? sq.slot : 0) * g.Hv + hv) * g.Dv + v0 + n) * DK + w * (DK / 4) + 4 * DT * hg;
   f32x4_t st[DT][NT];

@@ -539,6 +539,43 @@ def test_gdn_forgets_at_the_lowest_decays(n, low):
     assert_within(state[0].cpu().numpy(), alone, ts, "state of the last tokens alone")
 
 
+@pytest.mark.parametrize("hk,hv", [(1, 2), (16, 48)])
+def test_gdn_gives_the_same_bits_every_time(hk, hv):
+    rng = np.random.default_rng([48, hv])
+    lens, d = [500, 1, 333, 90], 128
+    T, B = sum(lens), len(lens)
+    q, k, v = (dev(bf16(rng.standard_normal((T, h, d)))[0]) for h in (hk, hk, hv))
+    g = dev(-0.1 * rng.exponential(size=(T, hv)).astype(np.float32))
+    beta = dev(rng.uniform(0, 1, (T, hv)).astype(np.float32))
+    s_in = dev(rng.standard_normal((B, hv, d, d)).astype(np.float32))
+    starts = dev(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32))
+    ws = torch.empty(qmm.qmm_gdn_workspace_bytes(T, B, max(lens), hk, hv, d, d), dtype=torch.uint8, device="cuda")
+    first = None
+    for i in range(8):
+        s_out, y = torch.empty_like(s_in), torch.empty(T, hv, d, device="cuda")
+        ws.fill_(255 - i)
+        qmm.qmm_gdn(q, k, v, g, beta, s_in, y, ws, state_out=s_out, seq_start=starts, max_len=max(lens), l2norm=True)
+        torch.cuda.synchronize()
+        if first is None:
+            first = s_out, y
+        assert torch.equal(s_out, first[0]) and torch.equal(y, first[1]), i
+
+
+def test_attention_gives_the_same_bits_every_time():
+    rng = np.random.default_rng(49)
+    for q_lens, kv_lens, hd in (([1] * 9, [700, 3, 64, 65, 300, 31, 1, 128, 257], 128), ([200, 77], [260, 700], 128),
+                                ([90, 130], [300, 131], 256)):
+        q, (c, table, lens), starts, ws = attn_setup(rng, q_lens, kv_lens, 8, 2, hd, 16)
+        first = None
+        for i in range(6):
+            out = torch.empty_like(q)
+            ws.fill_(255 - i)
+            qmm.qmm_kv4_attn(q, c, table, lens, out, ws, q_start=starts, max_q=max(q_lens))
+            torch.cuda.synchronize()
+            first = out if first is None else first
+            assert torch.equal(out, first), (q_lens, i)
+
+
 def test_gdn_prompt_then_tokens_through_one_state():
     """A sequence cut into calls of both kernels, its state in place, against one pass over all of it."""
     rng = np.random.default_rng(45)
