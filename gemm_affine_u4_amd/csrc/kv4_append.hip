@@ -11,9 +11,9 @@
 // keeps one token: its lanes' cos and sin (the same dims for every head) are read once and
 // stay in registers over the token's heads; small calls take one step of heads per wave.
 //
-// Measured, 40/8 heads x 128: 16 tokens 4.4 us; 8192 tokens 64 us (3.9 TB/s; 45 us where inputs are
-// in the last-level cache; writing q past the caches took 61 us but the attention that reads it
-// next would miss).  1021 fp32 tokens of 24/4 heads x 256: 11.7 us, 4.4 TB/s.
+// Measured, 40/8 heads x 128: 16 tokens 3.7 us; 8192 tokens 56 us (4.4 TB/s; 40 us where inputs are
+// in the last-level cache).  1021 fp32 tokens of 24/4 heads x 256: 10.9 us, 4.7 TB/s.  q is
+// written through the caches: the attention that follows reads it.
 #include <hip/hip_runtime.h>
 
 #include "kv4_device.h"
@@ -217,11 +217,12 @@ int launch_hd(const Kv4AppendArgs& a, hipStream_t s) {
   constexpr int HPW = 512 / HD;
   const int q_units = a.q ? (a.n_q + HPW - 1) / HPW : 0;
   const int units = q_units + (2 * a.c.n_kv + HPW - 1) / HPW;
-  // One step per wave until the GPU's waves are filled a few times over, then more: the
-  // lane's 16 angles are then read once for several heads.
-  int per = 1;
-  while (per < units && a.T * ((units + per) / (per + 1)) >= int64_t(device_cus()) * 64) ++per;
-  const int wpt = (units + per - 1) / per;
+  // One step of heads per wave up to 16 waves for each compute unit, then several: the lane's 16
+  // angles are then read once for them (8192 tokens, 14 steps: one wave 56 us, a wave a step 74; 1024
+  // tokens: 4 waves a token 9.4 us, 1 wave 13.3).
+  const int64_t fill = a.T ? int64_t(device_cus()) * 16 / a.T : 1;
+  const int want = int(fill < 1 ? 1 : fill < units ? fill : units);
+  const int per = (units + want - 1) / want, wpt = (units + per - 1) / per;
   const int64_t blocks = (a.T * wpt + 3) / 4;
   if (a.rot % 16 == 0)
     kv4_append_kernel<HD, F32, true><<<dim3(uint32_t(blocks)), 256, 0, s>>>(a, units, q_units, per, wpt);
