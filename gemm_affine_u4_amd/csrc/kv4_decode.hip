@@ -11,7 +11,7 @@
 // matrix cores take exactly, so a code costs half a mask instruction and no conversion; the
 // powers of two go into q (1/16 for the odd places) and into the final factor.
 //
-// Measured: 64 sequences of 100 to 16000 keys, 40/8 heads x 128: 124 us, 5.6 TB/s of cache (in the
+// Measured: 64 sequences of 100 to 16000 keys, 40/8 heads x 128: 120 us, 5.8 TB/s of cache (in the
 // order given, not longest first: 133); one of 131071 keys, 24/4 heads x 256: 34 us, 4.4 TB/s; one of
 // 517 keys: 8.0 us.
 //
@@ -102,10 +102,11 @@ __global__ __launch_bounds__(NW * 64, 2) void kv4_decode_kernel(Kv4AttnArgs g, i
   constexpr int NG = B::NG, NKL = B::NKL, R = B::R;
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, hg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int split = blockIdx.x, b = attn_longest_first(g, int(blockIdx.z), tid & 63);
+  const int split = blockIdx.x;
+  int b = blockIdx.z;
   const int kvh = blockIdx.y % g.c.n_kv, rt = blockIdx.y / g.c.n_kv;
 
-  const AttnSeq sq = attn_seq(g, b);
+  const AttnSeq sq = attn_longest_first(g, b, lane);
   const int row0 = rt * 16, rows = sq.q_len * group - row0;
   if (rows <= 0) return;
   const AttnSplit pl = attn_split(g, sq, row0, rows < 16 ? rows : 16, group, plan, split);

@@ -90,10 +90,11 @@ __global__ __launch_bounds__(NW * 64, HD == 256 ? 1 : 2) void kv4_prefill_kernel
   constexpr int NG = HD / 64, WPL = U::WPL, PER = U::PER, UK = U::UK, ROWS = kAttnRows, OT = HD / 32;
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, hh = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int split = blockIdx.x, b = attn_longest_first(g, int(blockIdx.z), tid & 63);
+  const int split = blockIdx.x;
+  int b = blockIdx.z;
   const int kvh = blockIdx.y % g.c.n_kv, rt = tiles - 1 - int(blockIdx.y) / g.c.n_kv;  // longest rows first
 
-  const AttnSeq sq = attn_seq(g, b);
+  const AttnSeq sq = attn_longest_first(g, b, lane);
   const int row0 = rt * ROWS, rows = sq.q_len * group - row0;
   if (rows <= 0) return;
   const AttnSplit pl = attn_split(g, sq, row0, rows < ROWS ? rows : ROWS, group, plan, split);

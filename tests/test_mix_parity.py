@@ -284,7 +284,7 @@ def test_a_long_context_is_split_and_joined_the_same_every_time():
         assert_within(bf16_bits_to_f64(outs[0])[0, a], ref, 1.01 * tol[0, a], f"head {a}")
 
 
-def check_long(rng, q_lens, kv_lens, n_q, n_kv, hd, page, causal=True, window=0):
+def check_long(rng, q_lens, kv_lens, n_q, n_kv, hd, page, causal=True, window=0, check=()):
     """Long contexts whose tables name a few whole pages again and again."""
     c = mix.Cache(5, n_kv, page, hd)
     for slot in range(5 * page):
@@ -302,7 +302,7 @@ def check_long(rng, q_lens, kv_lens, n_q, n_kv, hd, page, causal=True, window=0)
     torch.cuda.synchronize()
     got = bf16_bits_to_f64(out.values())
     for b, (n, kv) in enumerate(zip(q_lens, kv_lens)):
-        if kv == max(kv_lens) or b % 16 == 0:
+        if kv == max(kv_lens) or b % 16 == 0 or b in check:
             sl = slice(starts[b], starts[b + 1])
             ref, tol = mix.attention(qv[sl], c, table[b], kv, n, hd ** -0.5, causal, window, None)
             assert_within(got[sl], ref, tol, f"sequence {b} q {n} kv {kv}")
@@ -315,6 +315,17 @@ def test_long_contexts_of_single_tokens(hd, page):
     lens = rng.integers(0, 70, 300).tolist()
     lens[123] = 13003
     check_long(rng, [1] * 300, lens, 16, 8, hd, page)
+
+
+@pytest.mark.parametrize("B", [2, 9, 63, 64, 65])
+def test_long_contexts_in_any_order(B):
+    """Ragged lengths, equal and empty ones among them, in batches that are put in order or not."""
+    rng = np.random.default_rng([50, B])
+    lens = rng.integers(1, 2600, B).tolist()
+    lens[B // 2], lens[-1], lens[0] = 0, lens[0], 2700
+    check_long(rng, [1] * B, lens, 4, 2, 128, 32, check=range(B))
+    if B < 10:
+        check_long(rng, [67 + b % 3 for b in range(B)], [n + 70 for n in lens], 4, 2, 128, 32, check=range(B))
 
 
 @pytest.mark.parametrize("hd,page", [(128, 16), (64, 64), (256, 16)])
