@@ -12,8 +12,8 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr float kGdnEps = 1e-6f;
 // Calls of up to this max_len run token by token, longer ones in chunks.  Measured at 16 tokens
-// against 17, 32 heads x 128: one sequence 11.8 against 13.1 us, 16 of them 43 against 61, 64 of
-// them 132 against 222; at 24 one sequence would take 16 us by tokens.
+// against 17, 32 heads x 128: one sequence 11.8 against 12.7 us, 16 of them 43 against 58, 64 of
+// them 132 against 210; at 24 one sequence would take 16 us by tokens.
 constexpr int kGdnStepLen = 16;
 uint64_t gdn_chunk_workspace(int64_t T, int64_t B, int64_t Hk, int64_t Hv, int64_t Dk);
 int launch_gdn_chunk(const GdnArgs& a, hipStream_t s);

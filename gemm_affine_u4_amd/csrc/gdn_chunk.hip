@@ -26,6 +26,8 @@
 // sequences, 48 heads: prep 76 us, walk 269 us.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "gdn.h"
 #include "kv4_attn.h"
 #include "qmm_device.h"
@@ -385,7 +387,7 @@ __global__ __launch_bounds__(512, 2) void gdn_walk_kernel(GdnArgs g, int64_t n_s
           }
         }
       }
-      load(c + 1 < chunks ? c + 1 : c);
+      if (c + 1 < chunks) load(c + 1);
     }
     return;
   }
@@ -480,8 +482,8 @@ __global__ __launch_bounds__(512, 2) void gdn_walk_kernel(GdnArgs g, int64_t n_s
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) asm volatile("" : "+v"(st[dt][nt]));
   }
-  for (int c = 0; c < chunks; ++c) {
-    const int cn = c + 1 < chunks ? c + 1 : c;
+  auto chunk = [&](int c, auto more) {  // more: load the next one's operands as this one's were used
+    const int cn = c + 1;
     u32x4_t sp[NT][3];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -502,7 +504,7 @@ __global__ __launch_bounds__(512, 2) void gdn_walk_kernel(GdnArgs g, int64_t n_s
         for (int t = 0; t < 4; ++t) ks[nt][t] = mma(fk[t], sp[nt][p], p == 2 ? f32x4_t{0.f, 0.f, 0.f, 0.f} : ks[nt][t]);
       }
     }
-    load_rows(1, cn, fk);
+    if constexpr (more.value) load_rows(1, cn, fk);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -535,11 +537,11 @@ __global__ __launch_bounds__(512, 2) void gdn_walk_kernel(GdnArgs g, int64_t n_s
       for (int i = 0; i < 4; ++i) r[i] = fmaf(-fx[i], sum[i], bf16_bits_to_f32(fv[nt][i]));
       put4(s_x, nt, r);
     }
-    fx = load_fac(cn, 0);
-    load_v(cn);
+    if constexpr (more.value) fx = load_fac(cn, 0);
+    if constexpr (more.value) load_v(cn);
     __syncthreads();
     qs_mul(2);
-    load_rows(2, cn, fq);
+    if constexpr (more.value) load_rows(2, cn, fq);
     // D, as it is (for the outputs) and faded to the chunk's end (for the state)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -557,8 +559,8 @@ __global__ __launch_bounds__(512, 2) void gdn_walk_kernel(GdnArgs g, int64_t n_s
 #pragma unroll
       for (int t = 0; t < 4; ++t) s_qs[w][nt][t][lane] = qs[nt][t];
     }
-    load_tri(cn, kFragM, 3, fm);
-    fz = load_fac(cn, 2);
+    if constexpr (more.value) load_tri(cn, kFragM, 3, fm);
+    if constexpr (more.value) fz = load_fac(cn, 2);
     __syncthreads();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -577,9 +579,11 @@ __global__ __launch_bounds__(512, 2) void gdn_walk_kernel(GdnArgs g, int64_t n_s
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) st[dt][nt] = st[dt][nt] * decay + (a[dt][0] + a[dt][1]);
     }
-    load_kt(cn);
-    decay = load_decay(cn);
-  }
+    if constexpr (more.value) load_kt(cn);
+    if constexpr (more.value) decay = load_decay(cn);
+  };
+  for (int c = 0; c + 1 < chunks; ++c) chunk(c, std::true_type{});
+  if (chunks) chunk(chunks - 1, std::false_type{});
   if (kept) {
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) {
