@@ -5,15 +5,19 @@
 // so the codes enter the matrix product exactly and each group's scale and bias are two
 // fp32 multiply-adds on the product.  The output is
 //   sum_t p_t v_t = sum_t (p_t s_t) c_t + sum_t p_t b_t,
-// with p_t s_t rounded to fp16 (relative 2^-11, an eighth of the output's own rounding) and
-// the weights p in the sums' products likewise; the rest is fp32.  A nibble c masked in place
-// is the fp16 number c 2^-24 (or, in the next four bits, 16 c 2^-24): a subnormal that the
-// matrix cores take exactly, so a code costs half a mask instruction and no conversion; the
-// powers of two go into q (1/16 for the odd places) and into the final factor.
+// with p_t s_t rounded to fp16 (relative 2^-11 where 8 p_t s_t is a normal fp16 number) and
+// the weights p in the sums' products likewise; the rest is fp32.
+// Key codes enter as normal fp16 numbers.  Value codes stay masked in place, the fp16 numbers
+// c 2^-24 (or, in the next four bits, 16 c 2^-24): subnormals, half an instruction a code and no
+// conversion.  The matrix cores line up a product's eight neighbouring terms by their exponents, and
+// a subnormal's is not its own: terms below 2^-14 of the largest possible one are cut off (as a
+// probe shows).  For values that is 2^-14 of the largest weight times scale among eight keys,
+// an eighth of that weight's own rounding; queries, though, may span any range, and with codes in
+// place scores of 2^18 had no digits left for differences of 1 (conversion: 64 sequences 126
+// against 121 us, 131071 keys 36 against 34).
 //
-// Measured: 64 sequences of 100 to 16000 keys, 40/8 heads x 128: 120 us, 5.8 TB/s of cache (in the
-// order given, not longest first: 133); one of 131071 keys, 24/4 heads x 256: 34 us, 4.4 TB/s; one of
-// 517 keys: 8.0 us.
+// Measured: 64 sequences of 100 to 16000 keys, 40/8 heads x 128: 126 us, 5.5 TB/s of cache; one of 131071
+// keys, 24/4 heads x 256: 36 us, 4.1 TB/s; one of 517 keys: 8.5 us.
 //
 // Bound: the cache's bytes (HBM) for long contexts, launch and latency for short ones.
 //
@@ -72,8 +76,7 @@ __device__ __forceinline__ uint32_t row_next(uint32_t x) {
   else return uint32_t(__builtin_amdgcn_update_dpp(0, int(x), 0x100 + N, 0xf, 0xf, true));
 }
 
-// The four operands (dims 4n + 0..3 of the 16 rows n) of 8 keys' value codes, and the
-// operand of one key word: nibbles in place.
+// The four operands (dims 4n + 0..3 of the 16 rows n) of 8 keys' value codes: nibbles in place.
 __device__ __forceinline__ f16x8_t nib_operand(const u32x4_t& w, int j) {
   u32x4_t r;
 #pragma unroll
@@ -83,13 +86,16 @@ __device__ __forceinline__ f16x8_t nib_operand(const u32x4_t& w, int j) {
   }
   return __builtin_bit_cast(f16x8_t, r);
 }
-__device__ __forceinline__ f16x8_t key_operand(uint32_t w) {
+// The operand of one key word: its codes as normal fp16 numbers, from 1024 + c and 64 + c (m1024, m64: the bits
+// of those offsets, twice).
+__device__ __forceinline__ f16x8_t key_operand(uint32_t w, uint32_t m1024, uint32_t m64) {
+  constexpr f16x2_t k1024 = {(_Float16)1024.f, (_Float16)1024.f}, k64 = {(_Float16)64.f, (_Float16)64.f};
   u32x4_t r;
   const uint32_t x = w >> 8;
-  r[0] = w & 0x000F000Fu;
-  r[1] = w & 0x00F000F0u;
-  r[2] = x & 0x000F000Fu;
-  r[3] = x & 0x00F000F0u;
+  r[0] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, (w & 0x000F000Fu) | m1024) - k1024);
+  r[1] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, (w & 0x00F000F0u) | m64) - k64);
+  r[2] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, (x & 0x000F000Fu) | m1024) - k1024);
+  r[3] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, (x & 0x00F000F0u) | m64) - k64);
   return __builtin_bit_cast(f16x8_t, r);
 }
 __device__ __forceinline__ f32x4_t mma16(f16x8_t a, f16x8_t b, f32x4_t c) {
@@ -212,8 +218,8 @@ __global__ __launch_bounds__(NW * 64, 2) void kv4_decode_kernel(Kv4AttnArgs g, i
   }
 
   // q as operands: fp16 scaled by a power of two so that the row's largest is in
-  // [2^14, 2^15) (bf16 values stay exact), odd places by 1/16 more; and the groups' sums, in
-  // two fp16 pieces, against the biases
+  // [2^7, 2^8) (bf16 values stay exact, 64 of them add up within fp16); and the groups' sums, in
+  // two fp16 pieces (22 bits), against the biases
   f16x8_t qf[NG][2], xf;
   float qs;
   {
@@ -242,14 +248,14 @@ __global__ __launch_bounds__(NW * 64, 2) void kv4_decode_kernel(Kv4AttnArgs g, i
     mx = fmaxf(mx, __shfl_xor(mx, 16));
     mx = fmaxf(mx, __shfl_xor(mx, 32));
     const int ex = mx > 0.f ? int((__float_as_uint(mx) >> 23) & 255) - 127 : 0;
-    const int sh = 14 - ex;  // in [-113, 141]
-    qs = g.scale * kLog2e * ldexpf(1.f, 24 - sh);
+    const int sh = 7 - ex;  // in [-120, 134]
+    qs = fminf(g.scale * kLog2e * ldexpf(1.f, -sh), 3e38f);  // finite: it meets differences of 0
 #pragma unroll
     for (int i = 0; i < 8; ++i) xf[i] = static_cast<_Float16>(0.f);
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
       // the products' k places i and NG + i of the first lane group
-      const float y = hg == 0 ? ldexpf(xs[i], sh - 24) : 0.f;
+      const float y = hg == 0 ? ldexpf(xs[i], sh) : 0.f;
       xf[i] = static_cast<_Float16>(y);
       xf[NG + i] = static_cast<_Float16>(y - static_cast<float>(xf[i]));
 #pragma unroll
@@ -257,9 +263,8 @@ __global__ __launch_bounds__(NW * 64, 2) void kv4_decode_kernel(Kv4AttnArgs g, i
         // operand order: nibbles (0, 4), (1, 5), (2, 6), (3, 7)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int down = (e & 1) ? sh - 4 : sh;
-          qf[i][j][2 * e] = static_cast<_Float16>(ldexpf(x[i][j][e], down));
-          qf[i][j][2 * e + 1] = static_cast<_Float16>(ldexpf(x[i][j][e + 4], down));
+          qf[i][j][2 * e] = static_cast<_Float16>(ldexpf(x[i][j][e], sh));
+          qf[i][j][2 * e + 1] = static_cast<_Float16>(ldexpf(x[i][j][e + 4], sh));
         }
       }
     }
@@ -286,6 +291,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kv4_decode_kernel(Kv4AttnArgs g, i
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
+  const uint32_t m1024 = in_vgpr(0x64006400u), m64 = in_vgpr(0x54005400u);
   f16x8_t ones;
 #pragma unroll
   for (int i = 0; i < 8; ++i) ones[i] = static_cast<_Float16>(1.f);
@@ -327,7 +333,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kv4_decode_kernel(Kv4AttnArgs g, i
       for (int e = 0; e < NG * 2; ++e) {
         const int p = HD == 64 ? 0 : e / 4, j = HD == 64 ? e : e % 4;
         const int gi = HD == 64 ? 0 : 2 * p + (j >> 1);
-        d[gi] = mma16(key_operand(x.k[u][p][j]), qf[gi][j & 1], d[gi]);
+        d[gi] = mma16(key_operand(x.k[u][p][j], m1024, m64), qf[gi][j & 1], d[gi]);
       }
       static_for<4>([&](auto ic) {
         constexpr int i = decltype(ic)::value, tk = 4 * u + i;
@@ -367,11 +373,11 @@ __global__ __launch_bounds__(NW * 64, 2) void kv4_decode_kernel(Kv4AttnArgs g, i
         for (int j = 0; j < 4; ++j) acc[i][j] *= fac;
       }
     }
-    // probabilities times 8 (p <= 1 and scales below 2^13 keep p s within fp16)
-    const float off = fmaf(-m, qs, 3.f);
+    // probabilities times 8 (p <= 1 and scales below 2^13 keep p s within fp16).  The difference
+    // comes first: rounded products of scores of 2^20 and more would be off by a factor of their own.
     float p[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = exp2_hw(fmaf(sc[i], qs, off));
+    for (int i = 0; i < 8; ++i) p[i] = exp2_hw(fmaf(sc[i] - m, qs, 3.f));
     if (masked) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) p[i] = (vis >> i) & 1 ? p[i] : 0.f;

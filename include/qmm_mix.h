@@ -89,8 +89,8 @@ int qmm_kv4_append(const qmm_kv4_cache* cache, const void* k, const void* v, int
  *   causal = 1: query j of n (0-based) of a sequence stands at p = kv_len - n + j and sees
  *     keys t <= p, with window > 0 only t > p - window.  causal = 0 (window must be 0):
  *     every query sees all keys.
- *   A query that sees no key gives zeros.  scale > 0 and finite; |q| below 2^100, and for
- *   prompts scale * |q| * log2(e) below 65504 (larger ones are taken as that).
+ *   A query that sees no key gives zeros.  scale > 0 and finite; |q| below 2^100 and q . k
+ *   below 2^126, and for prompts scale * |q| * log2(e) below 65504 (larger ones are taken as that).
  *   gate (nullable) [T][n_q_heads][head_dim] bf16: out is multiplied by
  *     1 / (1 + exp(-gate)) (the output gate that qmm_fused_qkv_rope writes).
  * Sums, maxima and the softmax are fp32; codes enter the products exactly, probabilities

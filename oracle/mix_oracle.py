@@ -87,6 +87,25 @@ class Cache:
         self.v_codes[p, head, o // 8, :, o % 8] = q[:, 0] | (q[:, 1] << 4) | (q[:, 2] << 8) | (q[:, 3] << 12)
         self.v_meta[p, head, o] = self._meta(s, b)
 
+    def put_rows(self, slots, k, v):
+        """put() of many slots and all heads: k, v fp32 [n, n_kv, hd]."""
+        slots = np.asarray(slots)
+        p, o = slots // self.page, slots % self.page
+        at = [k_place(w, self.hd) for w in range(self.hd // 8)]
+        for h in range(self.n_kv):
+            c, s, b = quantize_f32(k[:, h])
+            c = c.reshape(len(slots), -1, 8).astype(np.uint32)
+            words = np.zeros(c.shape[:2], np.uint32)
+            for i in range(8):
+                words |= c[:, :, i] << np.uint32(4 * i)
+            row = np.empty_like(words)
+            row[:, at] = words
+            self.k_codes[p, h, o], self.k_meta[p, h, o] = row, self._meta(s, b)
+            c, s, b = quantize_f32(v[:, h])
+            c = c.reshape(len(slots), -1, 4).astype(np.uint16)
+            self.v_codes[p, h, o // 8, :, o % 8] = c[:, :, 0] | (c[:, :, 1] << 4) | (c[:, :, 2] << 8) | (c[:, :, 3] << 12)
+            self.v_meta[p, h, o] = self._meta(s, b)
+
     def get(self, slots, head):
         """(codes, scale, bias) of keys and of values of some slots, codes [n, hd]."""
         slots = np.asarray(slots)

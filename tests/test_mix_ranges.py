@@ -1,0 +1,68 @@
+"""GPU tests of the token mixers (qmm_mix.h) at the ends of their ranges: scores whose size leaves fp32
+few bits below the point, rows that see nothing in split calls, and the like."""
+import numpy as np
+import pytest
+import torch
+
+import gemm_affine_u4_amd as qmm
+from oracle import mix_oracle as mix
+from tests.gpu_util import Guarded, assert_within, bf16_bits_to_f64, dev
+from tests.test_mix_parity import bf16, gpu_cache
+
+pytestmark = pytest.mark.gpu
+
+
+def attend(c, table, q_bits, q_lens, kv_lens, scale=None):
+    """qmm_kv4_attn over an oracle's cache, NaN in its workspace: (out in fp64, rows' starts)."""
+    starts = np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32)
+    T, n_q, hd = q_bits.shape
+    out = Guarded((T, n_q, hd), False)
+    need = qmm.qmm_kv4_attn_workspace_bytes(T, len(kv_lens), max(q_lens), n_q, c.n_kv, hd, table.shape[1] * c.page)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    qmm.qmm_kv4_attn(dev(q_bits), gpu_cache(c), dev(table), dev(np.array(kv_lens, np.int32)), out.t, ws,
+                     q_start=dev(starts), max_q=max(q_lens), scale=scale)
+    torch.cuda.synchronize()
+    return bf16_bits_to_f64(out.values()), starts
+
+
+@pytest.mark.parametrize("hd,group,page", [(128, 5, 32), (64, 3, 16), (256, 6, 64)])
+@pytest.mark.parametrize("power", [0, 12, 60])
+@pytest.mark.parametrize("kv_lens", [[200, 77]])
+def test_weights_of_large_scores(hd, group, page, power, kv_lens):
+    """Scores near 2^22 (and 2^34, 2^82) whose differences are exact: a key is (15, c, 0, ..) with scale 1 and
+    bias 0, a query (2^18, 1, 0, ..) times 2^power, so a score is (15 2^18 + c) 2^power, 22 bits.  c is the same
+    for 32 neighbouring keys, so that waves and splits have maxima of their own.
+
+    The weights are then limited by fp16 alone: 2^-11 each of the weight times scale, of the weight with the
+    bias and of the weight in the sum, so 2 2^-11 of W = sum p (|s c| + |b|), 2^-18 W for all that is
+    fp32, and the output's rounding to bf16."""
+    rng = np.random.default_rng([60, hd, power, len(kv_lens)])
+    width = max(-(-n // page) for n in kv_lens)
+    c = mix.Cache(len(kv_lens) * width, 1, page, hd, rng)
+    table = rng.permutation(len(kv_lens) * width).astype(np.int32).reshape(len(kv_lens), width)
+    steps = []
+    for b, n in enumerate(kv_lens):
+        t = np.arange(n)
+        cs = rng.integers(0, 16, n // 32 + 1)[t // 32]
+        k = np.zeros((n, 1, hd), np.float32)
+        k[:, 0, 0], k[:, 0, 1] = 15, cs
+        v = rng.standard_normal((n, 1, hd)) + rng.standard_normal((n // 32 + 1, 1, hd))[t // 32]
+        c.put_rows(table[b, t // page] * page + t % page, k, v.astype(np.float32))
+        steps.append(cs)
+    q = np.zeros((2 * len(kv_lens), group, hd))
+    q[:, :, 0], q[:, :, 1] = 2.0 ** 18 * 2.0 ** power, 2.0 ** power
+    scale = np.float32(0.3)
+    got, starts = attend(c, table, bf16(q)[0], [2] * len(kv_lens), kv_lens, float(scale))
+    for b, n in enumerate(kv_lens):
+        t = np.arange(n)
+        _, (vc, vs, vb) = c.get(table[b, t // page] * page + t % page, 0)
+        v = mix.dequantize(vc, vs, vb)
+        va = mix.dequantize(vc, vs, np.zeros_like(vb)) + np.repeat(np.abs(vb.astype(np.float64)), 64, -1)
+        for j in range(2):
+            m = n - 1 + j
+            s = float(scale) * (steps[b][:m] - steps[b][:m].max()) * 2.0 ** power
+            p = np.exp(s) / np.exp(s).sum()
+            o, w = p @ v[:m], p @ va[:m]
+            e = w * (2 * 2.0 ** -11 + 2.0 ** -18)
+            for a in range(group):
+                assert_within(got[starts[b] + j, a], o, e + (np.abs(o) + e) * 2.0 ** -8, f"sequence {b} query {j} head {a}")
