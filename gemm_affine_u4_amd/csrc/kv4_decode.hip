@@ -482,8 +482,9 @@ __global__ __launch_bounds__(NW * 64, 2) void kv4_decode_kernel(Kv4AttnArgs g, i
       *reinterpret_cast<float4*>(po + at * HD + d) = o;
       if (d == 0) {
         float* pm = po + plan.nsplit * R0 * HD;
-        pm[at * 2] = cm * cqs;  // in powers of two
+        pm[at * 2] = cm;  // as it is: the join scales differences, as the waves do
         pm[at * 2 + 1] = cl;
+        if (split == 0) pm[plan.nsplit * R0 * 2 + row] = cqs;
       }
     }
   }
@@ -502,6 +503,7 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs g, int group,
   const int64_t row = (int64_t(sq.q0) + rr / group) * g.n_q + kvh * group + rr % group, R0 = g.T * g.n_q;
   const float* po = static_cast<const float*>(g.ws);
   const float* pm = po + plan.nsplit * R0 * HD;
+  const float qs = plan.rows == 16 ? pm[plan.nsplit * R0 * 2 + row] : 1.f;  // prompts' maxima are powers of two
   float mm = -INFINITY;
   for (int s = lane; s < count; s += 64) mm = fmaxf(mm, pm[(s * R0 + row) * 2]);
 #pragma unroll
@@ -513,7 +515,7 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs g, int group,
 #pragma unroll 4
   for (int s = wave; s < count; s += 4) {
     const int64_t at = s * R0 + row;
-    const float f = exp2_hw(pm[at * 2] - mm);
+    const float f = exp2_hw((pm[at * 2] - mm) * qs);
     l = fmaf(pm[at * 2 + 1], f, l);
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = fmaf(po[at * HD + lane * V + i], f, acc[i]);
@@ -548,6 +550,7 @@ __global__ __launch_bounds__(256) void kv4_join_rows_kernel(Kv4AttnArgs g, int g
   const int64_t row = (int64_t(sq.q0) + rr / group) * g.n_q + kvh * group + rr % group, R0 = g.T * g.n_q;
   const float* po = static_cast<const float*>(g.ws);
   const float* pm = po + plan.nsplit * R0 * HD;
+  const float qs = plan.rows == 16 ? pm[plan.nsplit * R0 * 2 + row] : 1.f;
   float mm = -INFINITY, l = 0.f;
 #pragma unroll 4
   for (int s = 0; s < count; ++s) mm = fmaxf(mm, pm[(s * R0 + row) * 2]);
@@ -555,7 +558,7 @@ __global__ __launch_bounds__(256) void kv4_join_rows_kernel(Kv4AttnArgs g, int g
 #pragma unroll 4
   for (int s = 0; s < count; ++s) {
     const int64_t at = s * R0 + row;
-    const float f = exp2_hw(pm[at * 2] - mm);
+    const float f = exp2_hw((pm[at * 2] - mm) * qs);
     const float4 v = *reinterpret_cast<const float4*>(po + at * HD + d);
     l = fmaf(pm[at * 2 + 1], f, l);
     o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
@@ -647,7 +650,8 @@ int launch_kv4_join(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t s) {
 uint64_t kv4_attn_workspace(int64_t T, int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t hd,
                             int64_t max_kv) {
   const uint64_t ns = uint64_t(attn_plan(B, max_q, n_q, n_kv, hd, max_kv).nsplit);
-  return ns > 1 ? ns * uint64_t(T) * uint64_t(n_q) * uint64_t(hd + 2) * 4 : 256;
+  // of a row: each split's output, maximum and sum; the factor of its scores
+  return ns > 1 ? uint64_t(T) * uint64_t(n_q) * (ns * uint64_t(hd + 2) + 1) * 4 : 256;
 }
 
 int launch_kv4_attn(const Kv4AttnArgs& a, hipStream_t s) {

@@ -27,7 +27,7 @@ def attend(c, table, q_bits, q_lens, kv_lens, scale=None):
 
 @pytest.mark.parametrize("hd,group,page", [(128, 5, 32), (64, 3, 16), (256, 6, 64)])
 @pytest.mark.parametrize("power", [0, 12, 60])
-@pytest.mark.parametrize("kv_lens", [[200, 77]])
+@pytest.mark.parametrize("kv_lens", [[200, 77], [4000]])
 def test_weights_of_large_scores(hd, group, page, power, kv_lens):
     """Scores near 2^22 (and 2^34, 2^82) whose differences are exact: a key is (15, c, 0, ..) with scale 1 and
     bias 0, a query (2^18, 1, 0, ..) times 2^power, so a score is (15 2^18 + c) 2^power, 22 bits.  c is the same
@@ -66,3 +66,38 @@ def test_weights_of_large_scores(hd, group, page, power, kv_lens):
             e = w * (2 * 2.0 ** -11 + 2.0 ** -18)
             for a in range(group):
                 assert_within(got[starts[b] + j, a], o, e + (np.abs(o) + e) * 2.0 ** -8, f"sequence {b} query {j} head {a}")
+
+
+@pytest.mark.parametrize("hd,n_q,n_kv", [(128, 5, 1), (64, 6, 2), (256, 4, 1)])
+def test_rows_of_large_queries_that_see_nothing(hd, n_q, n_kv):
+    """Split calls whose rows see no key give zeros, whatever the queries' size."""
+    rng = np.random.default_rng([61, hd])
+    page, n = 32, 6000
+    pages = -(-n // page)
+    c = mix.Cache(4, n_kv, page, hd, rng)
+    table = np.full((2, pages), -1, np.int32)
+    table[1, ::2] = c.n_pages + 7
+    q = bf16(2.0 ** 40 * rng.standard_normal((3, n_q, hd)))[0]
+    got, _ = attend(c, table, q, [1, 2], [n, n - 40])
+    assert np.all(got == 0), got
+
+
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 40])
+def test_absent_pages_beside_present_ones_in_a_split_call(size):
+    """One page is there among many splits that see nothing: its keys alone make the output."""
+    rng = np.random.default_rng(62)
+    page, n, hd, n_q = 32, 6000, 128, 5
+    pages = -(-n // page)
+    c = mix.Cache(4, 1, page, hd, rng)
+    row = rng.standard_normal((1, 1, hd)).astype(np.float32)  # one value in all of its keys
+    c.put_rows(2 * page + np.arange(page), rng.standard_normal((page, 1, hd)).astype(np.float32), np.repeat(row, page, 0))
+    (_, (vc, vs, vb)) = c.get([2 * page], 0)
+    v = mix.dequantize(vc, vs, vb)[0]
+    va = np.abs(mix.dequantize(vc, vs, np.zeros_like(vb))[0]) + np.abs(np.repeat(vb[0].astype(np.float64), 64))
+    e = va * (2 * 2.0 ** -11 + 2.0 ** -18)
+    for at in (0, 77, pages - 2):
+        table = np.full((1, pages), -1, np.int32)
+        table[0, at] = 2
+        got, _ = attend(c, table, bf16(size * rng.standard_normal((1, n_q, hd)))[0], [1], [n])
+        for a in range(n_q):
+            assert_within(got[0, a], v, e + (np.abs(v) + e) * 2.0 ** -8, f"page {at} head {a}")
