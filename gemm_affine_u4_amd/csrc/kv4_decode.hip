@@ -5,8 +5,9 @@
 // so the codes enter the matrix product exactly and each group's scale and bias are two
 // fp32 multiply-adds on the product.  The output is
 //   sum_t p_t v_t = sum_t (p_t s_t) c_t + sum_t p_t b_t,
-// with p_t s_t rounded to fp16 (relative 2^-11 where 8 p_t s_t is a normal fp16 number) and
-// the weights p in the sums' products likewise; the rest is fp32.
+// with p_t s_t rounded to fp16 and the weights p in the sums' products likewise (2^-11 of p_t s_t
+// and p_t; below 2^-28 of a wave's largest p and s, 2^-39 of those; below 2^-17 of the largest p,
+// 2^-28 of it); the rest is fp32.
 // Key codes enter as normal fp16 numbers.  Value codes stay masked in place, the fp16 numbers
 // c 2^-24 (or, in the next four bits, 16 c 2^-24): subnormals, half an instruction a code and no
 // conversion.  The matrix cores line up a product's eight neighbouring terms by their exponents, and
@@ -284,6 +285,9 @@ __global__ __launch_bounds__(NW * 64, 2) void kv4_decode_kernel(Kv4AttnArgs g, i
   // bacc[i], lane group 0) sums of weight times bias of group i, R + i
   f32x4_t acc[NG][4], bacc[R], lacc = {0.f, 0.f, 0.f, 0.f};
   float m = kFloor;
+  // Value scales are lifted by a power of two that brings the largest one met so far into
+  // [2^11, 2^12): all of them are below vtop, a power of two too.  acc is in these units.
+  float vtop = 0x1p-23f, lift = 4096.f / 0x1p-23f;
 #pragma unroll
   for (int i = 0; i < R; ++i) bacc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -298,7 +302,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kv4_decode_kernel(Kv4AttnArgs g, i
 
   auto step = [&](const B& x, int t0, const Where& w) {
     const bool masked = t0 < u_lo || t0 + kTile > u_hi || !w.ok0 || !w.ok1;
-    float sk[R], sv[R];
+    float sk[R], sv[R], top = 0.f;
     uint32_t vm[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -310,7 +314,23 @@ __global__ __launch_bounds__(NW * 64, 2) void kv4_decode_kernel(Kv4AttnArgs g, i
         vm[i] = (hg < 2 ? w.ok0 : w.ok1) && tk < sq.kv_len ? vm[i] : 0u;
       }
       sv[i] = half_lo(vm[i]);
+      top = fmaxf(top, sv[i]);
     }
+    if (__any(top >= vtop)) {  // larger value scales than the wave has met
+#pragma unroll
+      for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+      const uint32_t e = __builtin_amdgcn_readfirstlane(__float_as_uint(top) >> 23);
+      const float next = __uint_as_float((e + 1) << 23), fac = vtop / next;
+      vtop = next;
+      lift = 4096.f / next;
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] *= fac;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) sv[i] *= lift;
     float sc[8];
     static_for<2>([&](auto uc) {
       constexpr int u = decltype(uc)::value;
@@ -373,7 +393,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kv4_decode_kernel(Kv4AttnArgs g, i
         for (int j = 0; j < 4; ++j) acc[i][j] *= fac;
       }
     }
-    // probabilities times 8 (p <= 1 and scales below 2^13 keep p s within fp16).  The difference
+    // probabilities times 8 (p <= 1 and lifted scales below 2^12 keep p s within fp16).  The difference
     // comes first: rounded products of scores of 2^20 and more would be off by a factor of their own.
     float p[8];
 #pragma unroll
@@ -442,16 +462,16 @@ __global__ __launch_bounds__(NW * 64, 2) void kv4_decode_kernel(Kv4AttnArgs g, i
 #pragma unroll
   for (int i = 0; i < NW; ++i) mm = fmaxf(mm, s_m[i][n]);
   if (col_ok) {
-    const float fac = exp2_hw((m - mm) * qs);
+    const float fac = exp2_hw((m - mm) * qs), even = vtop * 4096.f, odd = vtop * 256.f;  // 2^24 / lift, 2^20 / lift
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         float4 o;
-        o.x = fmaf(acc[i][0][r], 16777216.f, bias[i]) * fac;
-        o.y = fmaf(acc[i][1][r], 1048576.f, bias[i]) * fac;
-        o.z = fmaf(acc[i][2][r], 16777216.f, bias[i]) * fac;
-        o.w = fmaf(acc[i][3][r], 1048576.f, bias[i]) * fac;
+        o.x = fmaf(acc[i][0][r], even, bias[i]) * fac;
+        o.y = fmaf(acc[i][1][r], odd, bias[i]) * fac;
+        o.z = fmaf(acc[i][2][r], even, bias[i]) * fac;
+        o.w = fmaf(acc[i][3][r], odd, bias[i]) * fac;
         *reinterpret_cast<float4*>(&s_o[wave][n][64 * i + 16 * hg + 4 * r]) = o;
       }
     }

@@ -101,3 +101,41 @@ def test_absent_pages_beside_present_ones_in_a_split_call(size):
         got, _ = attend(c, table, bf16(size * rng.standard_normal((1, n_q, hd)))[0], [1], [n])
         for a in range(n_q):
             assert_within(got[0, a], v, e + (np.abs(v) + e) * 2.0 ** -8, f"page {at} head {a}")
+
+
+@pytest.mark.parametrize("hd,page", [(128, 32), (64, 16), (256, 64)])
+@pytest.mark.parametrize("size,gap", [(1.0, 8.0), (1e-2, 8.0), (1e-3, 8.0), (1e-4, 8.0), (1e-5, 6.0), (1e4, 8.0)])
+def test_small_values_behind_dominant_keys(hd, page, size, gap):
+    """Values of any size under weights of any size: a key's part is rounded relative to itself.
+
+    256 sequences on one table, so that none is split and a wave walks a quarter of the keys; the first tile of
+    each wave has a key that stands `gap` above all others.  Weights times 8 stay normal in fp16.
+    Then, as above, the error is at most 2 2^-11 W, W = sum p (|s c| + |b|), 2^-18 W for fp32, and bf16's; scores
+    differ by what their fp32 sums of hd + 8 terms round, d, which changes a weight by e^(2 d)."""
+    rng = np.random.default_rng([63, hd, int(gap), int(np.log2(size)) + 100])
+    n, B, n_kv = 8000, 256, 8
+    pages = -(-n // page)
+    c = mix.Cache(pages, n_kv, page, hd, rng)
+    table = rng.permutation(pages).astype(np.int32)[None]
+    t = np.arange(n)
+    slots = table[0, t // page] * page + t % page
+    bits, q = bf16(rng.standard_normal((1, n_kv, hd)))
+    scale = hd ** -0.5
+    k = 0.02 * rng.standard_normal((n, n_kv, hd))
+    k[5:128:32] = q[0] * gap / (scale * (q[0] ** 2).sum(-1, keepdims=True))
+    c.put_rows(slots, k.astype(np.float32), (size * rng.standard_normal((n, n_kv, hd))).astype(np.float32))
+    got, _ = attend(c, np.repeat(table, B, 0), np.repeat(bits, B, 0), [1] * B, [n] * B)
+    assert np.array_equal(got, np.broadcast_to(got[:1], got.shape))
+    for h in range(n_kv):
+        (kc, ks, kb), (vc, vs, vb) = c.get(slots, h)
+        kd, v = mix.dequantize(kc, ks, kb), mix.dequantize(vc, vs, vb)
+        ka = mix.dequantize(kc, ks, np.zeros_like(kb)) + np.repeat(np.abs(kb.astype(np.float64)), 64, -1)
+        va = mix.dequantize(vc, vs, np.zeros_like(vb)) + np.repeat(np.abs(vb.astype(np.float64)), 64, -1)
+        s = scale * (kd @ q[0, h])
+        p = np.exp(s - s.max())
+        assert 8 * p.min() > 2.0 ** -14
+        p /= p.sum()
+        o, w = p @ v, p @ va
+        d = float((scale * (ka @ np.abs(q[0, h]))).max()) * (hd + 8) * 2.0 ** -24
+        e = w * (2 * 2.0 ** -11 + 2.0 ** -18 + np.expm1(2 * d))
+        assert_within(got[0, h], o, e + (np.abs(o) + e) * 2.0 ** -8, f"head {h}")
