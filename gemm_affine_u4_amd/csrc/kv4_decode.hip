@@ -14,11 +14,11 @@
 // a subnormal's is not its own: terms below 2^-14 of the largest possible one are cut off (as a
 // probe shows).  For values that is 2^-14 of the largest weight times scale among eight keys,
 // an eighth of that weight's own rounding; queries, though, may span any range, and with codes in
-// place scores of 2^18 had no digits left for differences of 1 (conversion: 64 sequences 126
-// against 121 us, 131071 keys 36 against 34).
+// place scores of 2^18 had no digits left for differences of 1 (this and the lift of the value
+// scales, below: 64 sequences 123 against 120 us, 131071 keys 36.2 against 33.7).
 //
-// Measured: 64 sequences of 100 to 16000 keys, 40/8 heads x 128: 126 us, 5.5 TB/s of cache; one of 131071
-// keys, 24/4 heads x 256: 36 us, 4.1 TB/s; one of 517 keys: 8.5 us.
+// Measured: 64 sequences of 100 to 16000 keys, 40/8 heads x 128: 123 us, 5.7 TB/s of cache; one of 131071
+// keys, 24/4 heads x 256: 36 us, 4.2 TB/s; one of 517 keys: 8.7 us.
 //
 // Bound: the cache's bytes (HBM) for long contexts, launch and latency for short ones.
 //
@@ -287,7 +287,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kv4_decode_kernel(Kv4AttnArgs g, i
   float m = kFloor;
   // Value scales are lifted by a power of two that brings the largest one met so far into
   // [2^11, 2^12): all of them are below vtop, a power of two too.  acc is in these units.
-  float vtop = 0x1p-23f, lift = 4096.f / 0x1p-23f;
+  float vtop = 0x1p-23f, lift = 0x1p35f;
 #pragma unroll
   for (int i = 0; i < R; ++i) bacc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -316,21 +316,6 @@ __global__ __launch_bounds__(NW * 64, 2) void kv4_decode_kernel(Kv4AttnArgs g, i
       sv[i] = half_lo(vm[i]);
       top = fmaxf(top, sv[i]);
     }
-    if (__any(top >= vtop)) {  // larger value scales than the wave has met
-#pragma unroll
-      for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-      const uint32_t e = __builtin_amdgcn_readfirstlane(__float_as_uint(top) >> 23);
-      const float next = __uint_as_float((e + 1) << 23), fac = vtop / next;
-      vtop = next;
-      lift = 4096.f / next;
-#pragma unroll
-      for (int i = 0; i < NG; ++i) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] *= fac;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < R; ++i) sv[i] *= lift;
     float sc[8];
     static_for<2>([&](auto uc) {
       constexpr int u = decltype(uc)::value;
@@ -378,21 +363,32 @@ __global__ __launch_bounds__(NW * 64, 2) void kv4_decode_kernel(Kv4AttnArgs g, i
       }
     }
     float mx = fmaxf(fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])), fmaxf(fmaxf(sc[4], sc[5]), fmaxf(sc[6], sc[7])));
-    if (__any(mx > m)) {
+    if (__any(mx > m || top >= vtop)) {
       mx = fmaxf(mx, __shfl_xor(mx, 16));
       mx = fmaxf(mx, __shfl_xor(mx, 32));
       const float mn = fmaxf(m, mx);
       const float fac = exp2_hw((m - mn) * qs);
       m = mn;
+      float vfac = fac;
+      if (__any(top >= vtop)) {  // larger value scales than the wave has met
+#pragma unroll
+        for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+        const uint32_t e = __builtin_amdgcn_readfirstlane(__float_as_uint(top) >> 23);
+        lift = __uint_as_float((265 - e) << 23);
+        vfac *= vtop * lift * 0x1p-12f;
+        vtop = __uint_as_float((e + 1) << 23);
+      }
       lacc *= fac;
 #pragma unroll
       for (int i = 0; i < R; ++i) bacc[i] *= fac;
 #pragma unroll
       for (int i = 0; i < NG; ++i) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] *= fac;
+        for (int j = 0; j < 4; ++j) acc[i][j] *= vfac;
       }
     }
+#pragma unroll
+    for (int i = 0; i < R; ++i) sv[i] *= lift;
     // probabilities times 8 (p <= 1 and lifted scales below 2^12 keep p s within fp16).  The difference
     // comes first: rounded products of scores of 2^20 and more would be off by a factor of their own.
     float p[8];
