@@ -15,6 +15,8 @@ constexpr int64_t kMaxHeads = 1024;
 constexpr int64_t kMaxTokens = int64_t(1) << 24;
 constexpr int64_t kMaxI32 = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxSeqs = 65535;  // a grid dimension
+// Keys of a page table: the kernels number keys in 32 bits and look up to 64 steps of 256 ahead.
+constexpr int64_t kMaxKeys = (int64_t(1) << 31) - (1 << 16);
 
 bool hd_ok(int64_t hd) { return hd == 64 || hd == 128 || hd == 256; }
 
@@ -50,7 +52,7 @@ bool gdn_sizes_ok(int64_t T, int64_t B, int64_t max_len, int64_t Hk, int64_t Hv,
 bool attn_sizes_ok(int64_t T, int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t hd, int64_t max_kv) {
   return T >= 0 && T <= kMaxTokens && B >= 1 && B <= kMaxSeqs && max_q >= 1 && max_q <= kMaxTokens && n_kv >= 1 &&
          n_kv <= kMaxHeads && n_q >= n_kv && n_q <= kMaxHeads && n_q % n_kv == 0 && hd_ok(hd) && max_kv >= 1 &&
-         max_kv <= kMaxI32 && (max_q * (n_q / n_kv) + 15) / 16 * n_kv <= 65535;
+         max_kv <= kMaxKeys && (max_q * (n_q / n_kv) + 15) / 16 * n_kv <= 65535;
 }
 
 }  // namespace
@@ -116,7 +118,7 @@ int qmm_kv4_attn(const uint16_t* q, int64_t T, const int32_t* q_start, const int
   if (!q || !kv_lens || !page_table || !workspace || !out) return QMM_ERR_NULL;
   const int64_t hd = cache->head_dim;
   if (causal != 0 && causal != 1) return QMM_ERR_ENUM;
-  if (max_pages < 1 || max_pages > kMaxI32 / cache->page_size ||
+  if (max_pages < 1 || max_pages > kMaxKeys / cache->page_size ||
       !attn_sizes_ok(T, B, max_q, n_q_heads, cache->n_kv_heads, hd, max_pages * cache->page_size) ||
       (!q_start && (T != B || max_q != 1)) || window < 0 || (window > 0 && !causal) || !(scale > 0.f) ||
       !std::isfinite(scale))

@@ -84,7 +84,8 @@ int qmm_kv4_append(const qmm_kv4_cache* cache, const void* k, const void* v, int
  *   kv_lens int32 [B]: keys of sequence b, its new tokens' (appended before) among them;
  *     clamped to [0, max_pages * page_size].
  *   page_table int32 [B][max_pages]: page of keys t of the sequence at entry t / page_size.
- *     An entry outside [0, n_pages) is "no page": its keys are not seen.
+ *     An entry outside [0, n_pages) is "no page": its keys are not seen.  max_pages * page_size
+ *     up to 2^31 - 65536.
  *   max_q: no sequence has more queries; rows of a sequence past max_q are left as they were.
  *   causal = 1: query j of n (0-based) of a sequence stands at p = kv_len - n + j and sees
  *     keys t <= p, with window > 0 only t > p - window.  causal = 0 (window must be 0):
