@@ -612,6 +612,8 @@ int join_hd(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t s) {
 
 }  // namespace
 
+int64_t kv4_attn_rows(int64_t rows, int64_t hd) { return rows <= decode_rows(hd) ? 16 : kAttnRows; }
+
 // Few queries: one block per compute unit for few long sequences (131071 keys x 4 heads: 64
 // splits 36 us, 128 splits 40 us: a block's fixed part is ~6 us), and up to 4 for many, whose
 // lengths may differ (64 sequences of 100 to 16000 keys x 8 heads: 141 us in 4, 156 us in 2).
@@ -627,7 +629,7 @@ int join_hd(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t s) {
 AttnPlan attn_plan(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t hd, int64_t max_kv) {
   const int64_t rows = max_q * (n_q / n_kv), cus = device_cus();
   AttnPlan p;
-  p.rows = rows <= decode_rows(hd) ? 16 : kAttnRows;
+  p.rows = int(kv4_attn_rows(rows, hd));
   const int64_t blocks = B * n_kv * ((rows + p.rows - 1) / p.rows);
   int64_t ns;
   if (p.rows == 16) {

@@ -45,6 +45,8 @@ struct Kv4AttnArgs {
   int32_t B, max_pages, max_q, n_q, causal;
   float scale;
 };
+// (Query, head) rows of a block, of a call with `rows` of them per sequence and KV head.
+int64_t kv4_attn_rows(int64_t rows, int64_t hd);
 // Bytes of workspace of a call's launch shape.
 uint64_t kv4_attn_workspace(int64_t T, int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t hd,
                             int64_t max_kv);

@@ -50,9 +50,11 @@ bool gdn_sizes_ok(int64_t T, int64_t B, int64_t max_len, int64_t Hk, int64_t Hv,
          Hv >= Hk && Hv <= kMaxHeads && Hv % Hk == 0 && gdn_dim_ok(Dk) && gdn_dim_ok(Dv);
 }
 bool attn_sizes_ok(int64_t T, int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t hd, int64_t max_kv) {
-  return T >= 0 && T <= kMaxTokens && B >= 1 && B <= kMaxSeqs && max_q >= 1 && max_q <= kMaxTokens && n_kv >= 1 &&
-         n_kv <= kMaxHeads && n_q >= n_kv && n_q <= kMaxHeads && n_q % n_kv == 0 && hd_ok(hd) && max_kv >= 1 &&
-         max_kv <= kMaxKeys && (max_q * (n_q / n_kv) + 15) / 16 * n_kv <= 65535;
+  if (T < 0 || T > kMaxTokens || B < 1 || B > kMaxSeqs || max_q < 1 || max_q > kMaxTokens || n_kv < 1 ||
+      n_kv > kMaxHeads || n_q < n_kv || n_q > kMaxHeads || n_q % n_kv || !hd_ok(hd) || max_kv < 1 || max_kv > kMaxKeys)
+    return false;
+  const int64_t rows = max_q * (n_q / n_kv), block = qmm::kv4_attn_rows(rows, hd);
+  return (rows + block - 1) / block * n_kv <= 65535;  // a grid dimension
 }
 
 }  // namespace

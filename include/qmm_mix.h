@@ -87,6 +87,8 @@ int qmm_kv4_append(const qmm_kv4_cache* cache, const void* k, const void* v, int
  *     An entry outside [0, n_pages) is "no page": its keys are not seen.  max_pages * page_size
  *     up to 2^31 - 65536.
  *   max_q: no sequence has more queries; rows of a sequence past max_q are left as they were.
+ *     n_kv_heads times the blocks of 128 rows in max_q * n_q_heads / n_kv_heads up to 65535 (40 / 8
+ *     heads: 209689 queries).  T and max_q up to 2^24, B up to 65535.
  *   causal = 1: query j of n (0-based) of a sequence stands at p = kv_len - n + j and sees
  *     keys t <= p, with window > 0 only t > p - window.  causal = 0 (window must be 0):
  *     every query sees all keys.

@@ -139,3 +139,17 @@ def test_small_values_behind_dominant_keys(hd, page, size, gap):
         d = float((scale * (ka @ np.abs(q[0, h]))).max()) * (hd + 8) * 2.0 ** -24
         e = w * (2 * 2.0 ** -11 + 2.0 ** -18 + np.expm1(2 * d))
         assert_within(got[0, h], o, e + (np.abs(o) + e) * 2.0 ** -8, f"head {h}")
+
+
+def test_a_prompt_of_many_blocks():
+    """More queries than 65535 blocks of 16 rows hold; rows are checked here and there, as single tokens are."""
+    rng = np.random.default_rng(65)
+    n_q, n_kv, hd, page, n = 40, 8, 64, 64, 26300
+    c = mix.Cache(5, n_kv, page, hd)
+    c.put_rows(np.arange(5 * page), *(rng.standard_normal((5 * page, n_kv, hd)).astype(np.float32) for _ in range(2)))
+    table = rng.integers(0, 5, (1, -(-n // page))).astype(np.int32)
+    bits, q = bf16(rng.standard_normal((n, n_q, hd)))
+    got, _ = attend(c, table, bits, [n], [n])
+    for j in (0, 1, 24, 25, 26, 51, 13107, 26213, 26214, n - 1):
+        ref, tol = mix.attention(q[j:j + 1], c, table[0], j + 1, 1, hd ** -0.5)
+        assert_within(got[j:j + 1], ref, tol, f"query {j}")

@@ -15,3 +15,19 @@ def test_tables_near_two_to_the_31_keys_are_refused(page):
         assert qmm.qmm_kv4_attn_workspace_bytes(1, 1, 1, 4, 2, 128, max_pages * page) == 0
     assert qmm.qmm_kv4_attn_workspace_bytes(1, 1, 1, 4, 2, 128, LIMIT) > 0
     assert qmm.qmm_kv4_attn_workspace_bytes(70, 1, 70, 4, 2, 128, LIMIT) > 0
+
+
+@pytest.mark.parametrize("n_q,n_kv,hd", [(40, 8, 128), (64, 8, 128), (24, 4, 256), (32, 8, 64), (64, 64, 64)])
+def test_long_prompts_are_taken(n_q, n_kv, hd):
+    """A prompt's blocks hold 128 rows (query x head of a group), and a grid's second dimension 65535 blocks."""
+    most = 65535 // n_kv * 128 // (n_q // n_kv)
+    for n in (16384, 32768, 131072, most):
+        if n <= most:
+            assert qmm.qmm_kv4_attn_workspace_bytes(n, 1, n, n_q, n_kv, hd, n) > 0, n
+    assert qmm.qmm_kv4_attn_workspace_bytes(most + 1, 1, most + 128, n_q, n_kv, hd, most + 128) == 0
+
+
+def test_few_rows_of_many_heads_are_taken():
+    """Blocks of 16 rows: as many as the heads allow."""
+    assert qmm.qmm_kv4_attn_workspace_bytes(128, 1, 128, 1024, 1024, 128, 4096) > 0
+    assert qmm.qmm_kv4_attn_workspace_bytes(64, 1, 64, 1024, 1024, 256, 4096) > 0
