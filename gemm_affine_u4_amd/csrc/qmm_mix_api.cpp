@@ -167,7 +167,7 @@ int qmm_gdn(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float
             const int32_t* seq_start, int64_t B, int64_t max_len, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
             float scale, int l2norm, const float* state_in, float* state_out, const int32_t* state_slots,
             int64_t n_slots, void* workspace, size_t workspace_bytes, void* y, int out_dtype, hipStream_t stream) {
-  if (!q || !k || !v || !g || !beta || !state_in || !state_out || !workspace || !y) return QMM_ERR_NULL;
+  if ((T != 0 && (!q || !k || !v || !g || !beta || !y)) || !state_in || !state_out || !workspace) return QMM_ERR_NULL;
   if ((out_dtype != QMM_OUT_BF16 && out_dtype != QMM_OUT_F32) || (l2norm != 0 && l2norm != 1)) return QMM_ERR_ENUM;
   if (!gdn_sizes_ok(T, B, max_len, Hk, Hv, Dk, Dv) || (!seq_start && (T != B || max_len != 1)) || n_slots < 1 ||
       n_slots > kMaxI32 || (!state_slots && n_slots < B) || !std::isfinite(scale))

@@ -125,7 +125,7 @@ int qmm_kv4_attn(const uint16_t* q, int64_t T, const int32_t* q_start, const int
  *     state_out == state_in updates in place; otherwise they must not overlap.  Sequence b
  *     reads and writes slot state_slots[b] (NULL: slot b).  A slot outside [0, n_slots):
  *     the sequence starts from zeros and its last state is not kept.  Slots in range must
- *     be distinct.  A sequence without tokens copies its state.
+ *     be distinct.  A sequence without tokens copies its state (T = 0: q, k, v, g, beta and y may be NULL).
  *   Dk and Dv 64 or 128.
  * The state and all sums are fp32.  Sequences of up to 16 tokens (max_len) run token by
  * token; longer ones in chunks of 64 tokens on the matrix cores with each fp32 factor as

@@ -153,3 +153,21 @@ def test_a_prompt_of_many_blocks():
     for j in (0, 1, 24, 25, 26, 51, 13107, 26213, 26214, n - 1):
         ref, tol = mix.attention(q[j:j + 1], c, table[0], j + 1, 1, hd ** -0.5)
         assert_within(got[j:j + 1], ref, tol, f"query {j}")
+
+
+@pytest.mark.parametrize("max_len", [1, 16, 100])
+def test_gdn_of_no_tokens_copies_its_states(max_len):
+    rng = np.random.default_rng(64)
+    hk, hv, d, n_slots = 2, 4, 128, 4
+    s_in = dev(rng.standard_normal((n_slots, hv, d, d)).astype(np.float32))
+    s_out = torch.full_like(s_in, 7.0)
+    empty = {h: torch.empty(0, h, d, dtype=torch.bfloat16, device="cuda") for h in (hk, hv)}
+    flat = torch.empty(0, hv, device="cuda")
+    ws = torch.empty(qmm.qmm_gdn_workspace_bytes(0, 3, max_len, hk, hv, d, d), dtype=torch.uint8, device="cuda")
+    args = empty[hk], empty[hk], empty[hv], flat, flat, s_in, torch.empty_like(empty[hv]), ws
+    start, slots = torch.zeros(4, dtype=torch.int32, device="cuda"), dev(np.array([2, n_slots, 0], np.int32))
+    qmm.qmm_gdn(*args, state_out=s_out, seq_start=start, state_slots=slots, max_len=max_len)
+    qmm.qmm_gdn(*args, seq_start=start, state_slots=slots, max_len=max_len)  # in place: nothing to do
+    torch.cuda.synchronize()
+    assert torch.equal(s_out[2], s_in[2]) and torch.equal(s_out[0], s_in[0])
+    assert torch.all(s_out[1] == 7) and torch.all(s_out[3] == 7)
