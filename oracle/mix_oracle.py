@@ -171,6 +171,77 @@ def attention(q, cache, table, kv_len, q_len, scale, causal=True, window=0, gate
     return out, tol
 
 
+def attention_spread(q, cache, table, kv_len, q_len, scale, few, causal=True, window=0, gate=None, hide=None,
+                     weight=None, bounds=True):
+    """One sequence as attention() takes it: (out, sigma, fixed) in fp64.  hide(t) and weight(t) plant mistakes:
+    keys that leave, and factors on the weights.
+
+    sigma: root mean square of what independent roundings add, key by key; unlike the bound of
+    attention() it shrinks as keys average out.  A rounding to fp16 is off by at most u = 2^-11 of the value,
+    u / sqrt(3) in the mean square.  With weights p, o = sum p v:
+      few queries:  dO = sum p e1 (s c) + sum p e2 (b - o)             (weight times scale; weight)
+      prompts:      dO = sum p e1 (v - o) + sum p e2 v                 (weight; value)
+                    + sum p ds (v - o), ds = scale sum_d q_d k_d e_td  (keys, for each key and dim)
+                    + scale sum_d e_d q_d sum_t p k_td (v - o)         (scaled queries, for each dim)
+    Weights among fp16's subnormals are off by 2^-25 of the largest weight, for few queries (times 8, scales
+    lifted to 2^11) by 2^-28 and 2^-39 of the largest scale.  Scores in fp32, hd + 8 roundings of 2^-24 of
+    M = scale sum |q| (|s c| + |b|), all of one sign: taken as the mean square of a key's ds.
+    fixed: the output's rounding to bf16, 2^-8 |o|, and 2^-18 of W = sum p (|s c| + |b|) for fp32 sums, exp2, the value
+    codes' cut (2^-14 of a weight times scale in eight) and the gate's sigmoid."""
+    n_q, hd = q.shape[1], q.shape[2]
+    group, u2 = n_q // cache.n_kv, 2.0 ** -22 / 3
+    out, sigma, fixed = (np.zeros((q_len, n_q, hd)) for _ in range(3))
+    t = np.arange(kv_len)
+    ids = np.asarray(table)[t // cache.page] if kv_len else np.zeros(0, int)
+    there = (ids >= 0) & (ids < cache.n_pages)
+    t, slots = t[there], ids[there].astype(np.int64) * cache.page + t[there] % cache.page
+    for h in range(cache.n_kv):
+        (kc, ks, kb), (vc, vs, vb) = cache.get(slots, h)
+        k, v = dequantize(kc, ks, kb), dequantize(vc, vs, vb)
+        kbr, vbr = (np.repeat(b.astype(np.float64), GROUP, -1) for b in (kb, vb))
+        vsr = np.repeat(vs.astype(np.float64), GROUP, -1)
+        for j in range(q_len):
+            p0 = kv_len - q_len + j
+            see = np.ones(t.shape, bool)
+            if causal:
+                see = t <= p0
+                if window:
+                    see &= t > p0 - window
+            if hide is not None:
+                see &= ~hide(t)
+            if not see.any():
+                continue
+            ki, vi, bi, ci, kbi = k[see], v[see], vbr[see], vc[see] * vsr[see], kbr[see]
+            for a in range(h * group, (h + 1) * group):
+                x = q[j, a]
+                s = scale * (ki @ x)
+                p = np.exp(s - s.max()) * (1.0 if weight is None else weight(t[see]))
+                p /= p.sum()
+                o = p @ vi
+                if not bounds:
+                    out[j, a] = o if gate is None else o / (1 + np.exp(-gate[j, a]))
+                    continue
+                w = p @ (ci + np.abs(bi))
+                p2, away = p * p, (vi - o) ** 2
+                m = scale * ((np.abs(ki - kbi) + np.abs(kbi)) @ np.abs(x)) * (hd + 8) * 2.0 ** -24
+                if few:
+                    var = u2 * (p2 @ (ci ** 2 + (bi - o) ** 2))
+                    var += p.max() ** 2 * (2.0 ** -56 * ((bi - o) ** 2).sum(0) + (2.0 ** -39 * 15 * vsr[see].max()) ** 2 * len(s))
+                    ds2 = m * m
+                else:
+                    var = u2 * (p2 @ (away + vi ** 2)) + p.max() ** 2 * 2.0 ** -50 * away.sum(0)
+                    var += u2 * scale ** 2 * ((x[:, None] * ((p[:, None] * ki).T @ (vi - o))) ** 2).sum(0)
+                    ds2 = u2 * scale ** 2 * ((ki * x) ** 2).sum(1) + m * m
+                sd = np.sqrt(var + (p2 * ds2) @ away)
+                f = 2.0 ** -18 * w
+                if gate is not None:
+                    sig = 1 / (1 + np.exp(-gate[j, a]))
+                    o, sd, f = o * sig, sd * sig, f * sig
+                out[j, a], sigma[j, a] = o, sd
+                fixed[j, a] = f + 2.0 ** -8 * (np.abs(o) + 8 * sd) + 1e-30
+    return out, sigma, fixed
+
+
 def gdn(q, k, v, g, beta, state, scale, l2norm):
     """One sequence in fp64: q, k [n, Hk, Dk], v [n, Hv, Dv], state [Hv, Dv, Dk].  Returns (y, state)."""
     s = np.array(state, np.float64)
