@@ -87,16 +87,15 @@ __device__ __forceinline__ f16x8_t nib_operand(const u32x4_t& w, int j) {
   }
   return __builtin_bit_cast(f16x8_t, r);
 }
-// The operand of one key word: its codes as normal fp16 numbers, from 1024 + c and 64 + c (m1024, m64: the bits
-// of those offsets, twice).
-__device__ __forceinline__ f16x8_t key_operand(uint32_t w, uint32_t m1024, uint32_t m64) {
-  constexpr f16x2_t k1024 = {(_Float16)1024.f, (_Float16)1024.f}, k64 = {(_Float16)64.f, (_Float16)64.f};
+// The operand of one key word: its codes as normal fp16 numbers, in the order 0 2 1 3 4 6 5 7.  The byte c is the
+// fp8 (e4m3) number c 2^-9, subnormal or not, so its conversion, times 512, gives the code exactly.
+__device__ __forceinline__ f16x8_t key_operand(uint32_t w) {
+  const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
   u32x4_t r;
-  const uint32_t x = w >> 8;
-  r[0] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, (w & 0x000F000Fu) | m1024) - k1024);
-  r[1] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, (w & 0x00F000F0u) | m64) - k64);
-  r[2] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, (x & 0x000F000Fu) | m1024) - k1024);
-  r[3] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, (x & 0x00F000F0u) | m64) - k64);
+  r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(even, 512.f, false));
+  r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(odd, 512.f, false));
+  r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(even, 512.f, true));
+  r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(odd, 512.f, true));
   return __builtin_bit_cast(f16x8_t, r);
 }
 __device__ __forceinline__ f32x4_t mma16(f16x8_t a, f16x8_t b, f32x4_t c) {
@@ -261,11 +260,11 @@ __global__ __launch_bounds__(NW * 64, 2) void kv4_decode_kernel(Kv4AttnArgs g, i
       xf[NG + i] = static_cast<_Float16>(y - static_cast<float>(xf[i]));
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        // operand order: nibbles (0, 4), (1, 5), (2, 6), (3, 7)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          qf[i][j][2 * e] = static_cast<_Float16>(ldexpf(x[i][j][e], sh));
-          qf[i][j][2 * e + 1] = static_cast<_Float16>(ldexpf(x[i][j][e + 4], sh));
+        for (int e = 0; e < 4; ++e) {  // operand order: codes (0, 2), (1, 3), (4, 6), (5, 7)
+          const int d = 4 * (e >> 1) + (e & 1);
+          qf[i][j][2 * e] = static_cast<_Float16>(ldexpf(x[i][j][d], sh));
+          qf[i][j][2 * e + 1] = static_cast<_Float16>(ldexpf(x[i][j][d + 2], sh));
         }
       }
     }
@@ -295,7 +294,6 @@ __global__ __launch_bounds__(NW * 64, 2) void kv4_decode_kernel(Kv4AttnArgs g, i
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
-  const uint32_t m1024 = in_vgpr(0x64006400u), m64 = in_vgpr(0x54005400u);
   f16x8_t ones;
 #pragma unroll
   for (int i = 0; i < 8; ++i) ones[i] = static_cast<_Float16>(1.f);
@@ -338,7 +336,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kv4_decode_kernel(Kv4AttnArgs g, i
       for (int e = 0; e < NG * 2; ++e) {
         const int p = HD == 64 ? 0 : e / 4, j = HD == 64 ? e : e % 4;
         const int gi = HD == 64 ? 0 : 2 * p + (j >> 1);
-        d[gi] = mma16(key_operand(x.k[u][p][j], m1024, m64), qf[gi][j & 1], d[gi]);
+        d[gi] = mma16(key_operand(x.k[u][p][j]), qf[gi][j & 1], d[gi]);
       }
       static_for<4>([&](auto ic) {
         constexpr int i = decltype(ic)::value, tk = 4 * u + i;
