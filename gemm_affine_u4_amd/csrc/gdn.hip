@@ -127,6 +127,10 @@ int launch_step(const GdnArgs& a, hipStream_t s) {
 
 }  // namespace
 
+bool gdn_launches(int64_t B, int64_t max_len, int64_t Hv, int64_t Dv) {
+  return max_len <= kGdnStepLen || (B * Hv + 7) / 8 * 8 * (Dv / 32) * 512 < (int64_t(1) << 32);  // the walk's grid
+}
+
 uint64_t gdn_workspace(int64_t T, int64_t B, int64_t max_len, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv) {
   return max_len <= kGdnStepLen ? 256 : gdn_chunk_workspace(T, B, Hk, Hv, Dk);
 }

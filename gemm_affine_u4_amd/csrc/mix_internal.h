@@ -68,6 +68,8 @@ struct GdnArgs {
   int32_t B, max_len, Hk, Hv, n_slots, l2norm, f32_out, Dk, Dv;
   float scale;
 };
+// Whether a launch can hold a call's threads (2^32 along a grid's dimension).
+bool gdn_launches(int64_t B, int64_t max_len, int64_t Hv, int64_t Dv);
 uint64_t gdn_workspace(int64_t T, int64_t B, int64_t max_len, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv);
 int launch_gdn(const GdnArgs& a, hipStream_t s);
 

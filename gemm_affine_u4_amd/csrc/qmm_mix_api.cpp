@@ -46,8 +46,10 @@ int check_cache(const qmm_kv4_cache* c, qmm::Kv4* out) {
 
 bool gdn_dim_ok(int64_t d) { return d == 64 || d == 128; }
 bool gdn_sizes_ok(int64_t T, int64_t B, int64_t max_len, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv) {
-  return T >= 0 && T <= kMaxTokens && B >= 1 && B <= kMaxSeqs && max_len >= 1 && max_len <= kMaxTokens && Hk >= 1 &&
-         Hv >= Hk && Hv <= kMaxHeads && Hv % Hk == 0 && gdn_dim_ok(Dk) && gdn_dim_ok(Dv);
+  if (T < 0 || T > kMaxTokens || B < 1 || B > kMaxSeqs || max_len < 1 || max_len > kMaxTokens || Hk < 1 || Hv < Hk ||
+      Hv > kMaxHeads || Hv % Hk || !gdn_dim_ok(Dk) || !gdn_dim_ok(Dv))
+    return false;
+  return qmm::gdn_launches(B, max_len, Hv, Dv);
 }
 bool attn_sizes_ok(int64_t T, int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t hd, int64_t max_kv) {
   if (T < 0 || T > kMaxTokens || B < 1 || B > kMaxSeqs || max_q < 1 || max_q > kMaxTokens || n_kv < 1 ||

@@ -126,7 +126,8 @@ int qmm_kv4_attn(const uint16_t* q, int64_t T, const int32_t* q_start, const int
  *     reads and writes slot state_slots[b] (NULL: slot b).  A slot outside [0, n_slots):
  *     the sequence starts from zeros and its last state is not kept.  Slots in range must
  *     be distinct.  A sequence without tokens copies its state (T = 0: q, k, v, g, beta and y may be NULL).
- *   Dk and Dv 64 or 128.
+ *   Dk and Dv 64 or 128.  T and max_len up to 2^24, B up to 65535, Hv up to 1024, and with max_len
+ *   above 16 B * Hv (rounded up to 8) * Dv below 2^28.
  * The state and all sums are fp32.  Sequences of up to 16 tokens (max_len) run token by
  * token; longer ones in chunks of 64 tokens on the matrix cores with each fp32 factor as
  * a sum of three bf16 values (two where only a bf16 y reads it).  Inputs are finite: in a

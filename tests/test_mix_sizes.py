@@ -2,7 +2,7 @@
 import pytest
 
 import gemm_affine_u4_amd as qmm
-from tests.test_mix_abi import B0, MB, S, attn, cache
+from tests.test_mix_abi import B0, MB, S, attn, cache, gdn
 
 LIMIT = (1 << 31) - (1 << 16)  # keys of a page table: key numbers of tiles ahead stay below 2^31
 
@@ -31,3 +31,11 @@ def test_few_rows_of_many_heads_are_taken():
     """Blocks of 16 rows: as many as the heads allow."""
     assert qmm.qmm_kv4_attn_workspace_bytes(128, 1, 128, 1024, 1024, 128, 4096) > 0
     assert qmm.qmm_kv4_attn_workspace_bytes(64, 1, 64, 1024, 1024, 256, 4096) > 0
+
+
+def test_more_delta_rule_prompts_than_a_launch_has_threads_for_are_refused():
+    """The walk of longer sequences takes 512 threads for 32 columns of each head: 2^32 threads a launch."""
+    assert qmm.qmm_gdn_workspace_bytes(1 << 20, 65535, 17, 8, 32, 128, 128) > 0
+    assert qmm.qmm_gdn_workspace_bytes(1 << 20, 65535, 17, 8, 48, 128, 128) == 0
+    assert qmm.qmm_gdn_workspace_bytes(1 << 20, 65535, 16, 8, 48, 128, 128) > 0  # token by token
+    assert gdn(T=1 << 20, B=65535, max_len=17, Hk=8, Hv=48, n_slots=1, q=B0 + (1 << 40)) == S["QMM_ERR_SHAPE"]
