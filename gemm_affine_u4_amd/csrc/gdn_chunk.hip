@@ -17,13 +17,15 @@
 // planes; the state always does).  T comes from
 // forward substitution and fp32 matrix products; sums are fp32, the running sum of g fp64.
 //
-// Bound: latency of the chunk's dependent products (three barriers a chunk, ~1.7 us for 16
-// columns; loads that all hit L2 take off 5%).  All slices of a head sit on one XCD, so that its
-// L2 serves them.  A wave's operands go straight to its registers, for the next chunk as soon
-// as this one's were used.
+// Bound: the walk's stages, three barriers a chunk, one after the other.  A chunk takes 1.6 us with 16
+// columns and 3.3 with 32, so a stage's time follows its work; matrix cores, vector unit and LDS
+// are busy for 20, 33 and 28 % (21, 33 and 30 % with 32 columns) and a wave waits for half of its
+// time, at barriers and for its own operands, with nothing beside it (loads that all hit L2 take
+// off 5%).  All slices of a head sit on one XCD, so that its L2 serves them.  A wave's operands
+// go straight to its registers, for the next chunk as soon as this one's were used.
 //
-// Measured: 4096 tokens, 32 heads x 128 x 128: prep 30 us, walk 111 us; 6813 tokens of six
-// sequences, 48 heads: prep 76 us, walk 269 us.
+// Measured: 4096 tokens, 32 heads x 128 x 128: prep 30 us, walk 104 to 111 us; 6813 tokens of six
+// sequences, 48 heads: prep 77 us, walk 258 to 276 us.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

@@ -55,11 +55,12 @@ __device__ __forceinline__ AttnSeq attn_seq(const Kv4AttnArgs& g, int b) {
   return s;
 }
 
-// The sequence of rank b by falling number of keys (b becomes its index), up to 64 of them; more
-// even out by themselves.  Blocks start in that order, so that the last ones to end are short:
-// 64 single tokens on 100 to 16000 keys 134 -> 126 us, five prompts on 2480 to 6695 keys 458 -> 400.  It
-// costs a block ~1.5 us at 64 sequences, so tables of up to 2048 keys keep the order given (64
-// single tokens on 500 keys each 12 us, ordered 14).
+// The sequence of rank b by falling number of keys (b becomes its index), up to 64 of them, one a
+// lane.  Blocks start in that order, so that the last ones to end are short: 64 single tokens on
+// 100 to 16000 keys 134 -> 126 us, five prompts on 2480 to 6695 keys 458 -> 400.  It costs a block
+// ~1.5 us at 64 sequences, so tables of up to 2048 keys keep the order given (64 single tokens on
+// 500 keys each 12 us, ordered 14).  More than 64 run in the order given, and do not even out by
+// themselves: 66 such tokens in any order 133 us, given longest first 114; 200 of them 362 and 296.
 __device__ __forceinline__ AttnSeq attn_longest_first(const Kv4AttnArgs& g, int& b, int lane) {
   const int n = int(gridDim.z);
   if (n == 1 || n > 64 || (int64_t(g.max_pages) << g.c.page_shift) <= 2048) return attn_seq(g, b);

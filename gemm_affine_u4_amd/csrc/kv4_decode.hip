@@ -14,11 +14,12 @@
 // a subnormal's is not its own: terms below 2^-14 of the largest possible one are cut off (as a
 // probe shows).  For values that is 2^-14 of the largest weight times scale among eight keys,
 // an eighth of that weight's own rounding; queries, though, may span any range, and with codes in
-// place scores of 2^18 had no digits left for differences of 1 (this and the lift of the value
-// scales, below: 64 sequences 123 against 120 us, 131071 keys 36.2 against 33.7).
+// place scores of 2^18 had no digits left for differences of 1.  (Conversion, differences before
+// products and the lift of the value scales, below, together: 64 sequences 123 against 120 us, 131071
+// keys 34.6 against 33.7, 16 x 12 queries on 2000 keys 28.6 against 26.3.)
 //
-// Measured: 64 sequences of 100 to 16000 keys, 40/8 heads x 128: 123 us, 5.7 TB/s of cache; one of 131071
-// keys, 24/4 heads x 256: 36 us, 4.2 TB/s; one of 517 keys: 8.7 us.
+// Measured: 64 sequences of 100 to 16000 keys, 40/8 heads x 128: 123 us, 5.6 TB/s of cache; one of 131071
+// keys, 24/4 heads x 256: 34.6 us, 4.4 TB/s; one of 517 keys: 8.5 us.
 //
 // Bound: the cache's bytes (HBM) for long contexts, launch and latency for short ones.
 //
@@ -47,8 +48,11 @@ constexpr int kTile = 32;  // keys of a wave's step
 constexpr float kFloor = -1e30f;  // maximum of a row that has seen no key yet
 constexpr float kLog2e = 1.4426950408889634f;
 // Calls of up to this many rows per KV head run here.  Against the prompts' kernel: 16 sequences of
-// 2000 keys x 8 heads x 128: 120 rows 49 against 67 us, 160 rows 60 against 54; four of 8000
-// keys x 4 heads x 256: 48 rows 34 against 41, 78 rows 52 against 42.
+// 2000 keys x 8 heads x 128: 60 rows 29 against 33 us, 90 rows 38 against 36, 125 rows 48 against 40; one
+// of 8000 keys: 50 rows 18 against 22, 125 rows 24 against 24; four of 1000 keys x 2 heads x 64: 126
+// rows 10 against 18; four of 8000 keys x 4 heads x 256: 48 rows 32 against 36, 60 rows 35 against 37.
+// So batches of 128 dims would cross at about 90 rows (40 sequences of 700 keys, 125 rows: 54 against 32); it stands
+// where single sequences and 64 dims still gain.
 constexpr int64_t decode_rows(int64_t hd) { return hd == 256 ? 64 : 128; }
 
 template <int HD>
@@ -614,7 +618,7 @@ int64_t kv4_attn_rows(int64_t rows, int64_t hd) { return rows <= decode_rows(hd)
 
 // Few queries: one block per compute unit for few long sequences (131071 keys x 4 heads: 64
 // splits 36 us, 128 splits 40 us: a block's fixed part is ~6 us), and up to 4 for many, whose
-// lengths may differ (64 sequences of 100 to 16000 keys x 8 heads: 141 us in 4, 156 us in 2).
+// lengths may differ (64 sequences of 100 to 16000 keys x 8 heads, before they were ordered: 141 us in 4, 156 in 2).
 // Splits of at least 1024 keys, and down to 128 while half of the units would idle (one
 // sequence of 4096 keys x 8 heads: 10.3 against 14.1 us; four of 2000: 10.9 against 15.4).  None up to
 // 768 keys or two splits, where the second launch costs more (517 keys: 8.3 against 10.0 us;

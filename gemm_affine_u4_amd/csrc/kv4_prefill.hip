@@ -1,13 +1,15 @@
 // Attention of prompts over the paged 4-bit cache (qmm_kv4_attn's prompt form).
 //
 // Mathematics: that of kv4_decode.hip, but a key tile serves many queries here, so its codes are
-// dequantized once per block: fp16(s c + b), one rounding (2^-11 of the value, an eighth of
-// the output's), into LDS.  Queries times scale log2(e) are rounded to fp16 likewise; scores,
-// maxima and sums are fp32, probabilities fp16.
+// dequantized once per block: fp16(s c + b), one rounding (2^-11 of the key or value), into LDS.
+// Queries times scale log2(e) are rounded to fp16 likewise (below 2^-14 by 2^-25); scores, maxima and
+// sums are fp32, probabilities fp16 (below 2^-14 by 2^-25, the largest being 1 or more).  Together the roundings
+// add a quarter of the output's own rounding to bf16 (prompts of 2048 and of 100 to 1500 against 64 bits).
 //
-// Bound: the matrix cores beside the softmax's and the dequantization's vector work, and LDS
-// reads: each 32x32x16 product takes 1 KB of the shared tile, which is the LDS rate at the
-// matrix rate.
+// Bound: no unit by itself.  Matrix cores, vector unit and LDS (each 32x32x16 product takes 1 KB of the
+// shared tile, its rate at the matrix rate) are busy for 28, 37 and 32 % of a prompt of 2048 x 128 dims and
+// 28, 34 and 36 % of five prompts x 256 dims, one after the other for the most part: a SIMD has two waves or
+// one.  At 128 dims its two places are filled for 68 % of the time, until the longest block ends.
 //
 // Split.  A block of 4 waves takes 128 (query, head) rows of one KV head (the heads of a
 // group share the tile) and walks the keys 64 at a time, in two steps of 32; a wave keeps 32
@@ -19,7 +21,8 @@
 //
 // Measured: a prompt of 2048, 40/8 heads x 128, causal: 63 us, 0.68 PFLOP/s (before the hand order
 // 77, with tiles dequantized by each wave for itself 129); five prompts on up to 9000 keys,
-// 24/4 heads x 256: 395 us, 0.71 PFLOP/s (sequences in the order given: 456).  8 waves, 16-column tiles and 32-key tiles were slower.
+// 24/4 heads x 256: 398 us, 0.70 PFLOP/s (sequences in the order given: 456).  8 waves, 16-column
+// tiles and 32-key tiles were slower.
 #include <hip/hip_runtime.h>
 
 #include "kv4_attn.h"

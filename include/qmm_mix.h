@@ -96,10 +96,13 @@ int qmm_kv4_append(const qmm_kv4_cache* cache, const void* k, const void* v, int
  *   below 2^126, and for prompts scale * |q| * log2(e) below 65504 (larger ones are taken as that).
  *   gate (nullable) [T][n_q_heads][head_dim] bf16: out is multiplied by
  *     1 / (1 + exp(-gate)) (the output gate that qmm_fused_qkv_rope writes).
- * Sums, maxima and the softmax are fp32; codes enter the products exactly, probabilities
- * times scale (few queries) or dequantized keys, values and probabilities (prompts) are
- * rounded to fp16 (values of a magnitude above 65504 do not occur in a cache that
- * qmm_kv4_append wrote), for prompts the scaled queries too.  The same call gives the same bits every time.
+ * Sums, maxima and the softmax are fp32.  Rounded to fp16 (2^-11 of the value) are, for few queries
+ * (up to 128 rows = queries x heads of a group, 64 at head_dim 256), the probabilities and the
+ * probabilities times scale, with keys and queries exact; for prompts the scaled queries, the dequantized
+ * keys and values (values of a magnitude above 65504 do not occur in a cache that qmm_kv4_append
+ * wrote) and the probabilities.  Below fp16's normal range such a value is off by an absolute amount: a
+ * prompt's scaled query and, of the row's largest, its probability by up to 2^-25, the few queries'
+ * probability by 2^-28.  The same call gives the same bits every time.
  * workspace: 256-byte aligned, at least qmm_kv4_attn_workspace_bytes of the same T, B, max_q,
  * heads and max_kv = max_pages * page_size (0 for sizes out of range; always > 0 otherwise).
  */
