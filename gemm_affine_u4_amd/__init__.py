@@ -2,7 +2,8 @@
 
 Argument marshalling only: every function here forwards device pointers, sizes
 and the current HIP stream to the C ABI of the same name (include/qmm.h) and
-raises QmmError on a non-zero status (the token mixers: include/qmm_mix.h).  Tensors are PyTorch device tensors used
+raises QmmError on a non-zero status (the token mixers: include/qmm_mix.h; a serving
+step's adapters, 8-bit cache and drafts: include/qmm_serve.h).  Tensors are PyTorch device tensors used
 as plain memory: bf16 arrays may be torch.bfloat16 or 16-bit integer tensors
 holding the bit patterns, codes any 32-bit integer tensor.  The library must be
 built (gemm_affine_u4_amd.build); there is no fallback.
@@ -21,6 +22,8 @@ __all__ = ["QmmError", "qmm_linear", "qmm_fused_qkv", "qmm_fused_qkv_rope", "qmm
            "QMM_STEP_LINEAR", "QMM_STEP_QKV", "QMM_STEP_GATE_UP_SWIGLU", "qmm_status_str", "qmm_abi_version", "load_library", "LIB_PATH",
            "KV4Cache", "kv4_cache_shapes", "qmm_kv4_append", "qmm_kv4_attn_workspace_bytes", "qmm_kv4_attn",
            "qmm_gdn_workspace_bytes", "qmm_gdn",
+           "KV8Cache", "kv8_cache_shapes", "qmm_kv8_append", "qmm_kv8_attn_workspace_bytes", "qmm_kv8_attn",
+           "qmm_spec_verify_workspace_bytes", "qmm_spec_verify", "qmm_lora_workspace_bytes", "qmm_lora",
            "QMM_OUT_BF16", "QMM_OUT_F32", "QMM_FP8_E4M3", "QMM_MOE_GATE_UP_SWIGLU", "QMM_MOE_DOWN_COMBINE", "STATUS"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqmm.so")
@@ -77,6 +80,15 @@ _SIGNATURES = {
     "qmm_gdn_workspace_bytes": [_I64] * 7,
     "qmm_gdn": [_P, _P, _P, _P, _P, _I64, _P, _I64, _I64, _I64, _I64, _I64, _I64, ctypes.c_float, _INT, _P, _P, _P,
                 _I64, _P, ctypes.c_size_t, _P, _INT, _P],
+    "qmm_kv8_append": [_P, _P, _P, _I64, _INT, _P, _P, _P, _I64, _I64, _I64, _P, _P, _I64, _I64, _P, _I64, _P, _P, _P,
+                       _P],
+    "qmm_kv8_attn_workspace_bytes": [_I64] * 9,
+    "qmm_kv8_attn": [_P, _I64, _P, _P, _P, _I64, _I64, _I64, _P, _I64, ctypes.c_float, _INT, _I64, _I64, _P, _P,
+                     ctypes.c_size_t, _P, _P],
+    "qmm_spec_verify_workspace_bytes": [_I64] * 2,
+    "qmm_spec_verify": [_P, _I64, _P, _I64, _I64, _P, _P, _I64, _INT, _P, _P, _P, _P, ctypes.c_size_t, _P],
+    "qmm_lora_workspace_bytes": [_I64] * 4,
+    "qmm_lora": [_P, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _INT, _P, _INT, _P, ctypes.c_size_t, _P],
 }
 
 
@@ -100,6 +112,9 @@ def load_library():
                          "qmm_moe_prefill_workspace_bytes": ctypes.c_size_t,
                          "qmm_kv4_attn_workspace_bytes": ctypes.c_size_t,
                          "qmm_gdn_workspace_bytes": ctypes.c_size_t,
+                         "qmm_kv8_attn_workspace_bytes": ctypes.c_size_t,
+                         "qmm_spec_verify_workspace_bytes": ctypes.c_size_t,
+                         "qmm_lora_workspace_bytes": ctypes.c_size_t,
                          "qmm_step_plan_bytes": ctypes.c_size_t}.get(name, ctypes.c_int)
         _LIB = lib
     return _LIB
@@ -488,21 +503,26 @@ MIX_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_qmm_mix.so
 _MIX = None
 
 
+def _binding(path: str, functions):
+    """A marshalling module (csrc/*_binding.cpp), over the loaded library's functions."""
+    import importlib.util
+
+    import torch  # noqa: F401  (the module uses its libraries)
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is not built; run `python -m gemm_affine_u4_amd.build`")
+    lib = load_library()
+    spec = importlib.util.spec_from_file_location(os.path.basename(path).split(".")[0], path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.bind(*(ctypes.cast(getattr(lib, f), _P).value for f in functions))
+    return mod
+
+
 def _mix():
     """The mixers' marshalling module (csrc/mix_binding.cpp), over the loaded library."""
     global _MIX
     if _MIX is None:
-        import importlib.util
-
-        import torch  # noqa: F401  (the module uses its libraries)
-        if not os.path.exists(MIX_PATH):
-            raise RuntimeError(f"{MIX_PATH} is not built; run `python -m gemm_affine_u4_amd.build`")
-        lib = load_library()
-        spec = importlib.util.spec_from_file_location("_qmm_mix", MIX_PATH)
-        mod = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(mod)
-        mod.bind(*(ctypes.cast(getattr(lib, f), _P).value for f in ("qmm_kv4_append", "qmm_kv4_attn", "qmm_gdn")))
-        _MIX = mod
+        _MIX = _binding(MIX_PATH, ("qmm_kv4_append", "qmm_kv4_attn", "qmm_gdn"))
     return _MIX
 
 
@@ -568,3 +588,98 @@ def qmm_gdn(q, k, v, g, beta, state, y, workspace, state_out=None, seq_start=Non
                               1 if l2norm else 0, _handle(stream))
     if st:
         raise QmmError(st, "qmm_gdn")
+
+
+# ---- a serving step: adapters, the paged 8-bit cache, drafted tokens (qmm_serve.h) --------------
+
+SERVE_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_qmm_serve.so")
+_SERVE = None
+
+
+def _serve():
+    """The serving step's marshalling module (csrc/serve_binding.cpp), over the loaded library."""
+    global _SERVE
+    if _SERVE is None:
+        _SERVE = _binding(SERVE_PATH, ("qmm_kv8_append", "qmm_kv8_attn", "qmm_spec_verify", "qmm_lora"))
+    return _SERVE
+
+
+def kv8_cache_shapes(n_pages: int, n_kv_heads: int, page_size: int, head_dim: int) -> dict:
+    """Shapes of a cache's arrays: k_codes and v_codes int8, k_scale and v_scale fp32."""
+    return {"k_codes": (n_pages, n_kv_heads, page_size, head_dim),
+            "k_scale": (n_pages, n_kv_heads, page_size // 16),
+            "v_codes": (n_pages, n_kv_heads, page_size // 8, head_dim, 8),
+            "v_scale": (n_pages, n_kv_heads, page_size // 16)}
+
+
+class KV8Cache:
+    """qmm_kv8_cache over four device tensors of kv8_cache_shapes(...)."""
+    __slots__ = ("tensors", "_c")
+
+    def __init__(self, k_codes, k_scale, v_codes, v_scale):
+        self._c = (_SERVE or _serve()).cache(k_codes, k_scale, v_codes, v_scale)
+        self.tensors = (k_codes, k_scale, v_codes, v_scale)
+
+
+def qmm_kv8_append(cache, k, v, page_table, kv_lens, q_start=None, max_q: int = 1, positions=None, cos_sin=None, q=None,
+                   q_out=None, k_held=None, v_held=None, stream=None) -> None:
+    """Keys and values k, v [T, n_kv, head_dim] (bf16 or fp32) of the new tokens of B sequences into the
+    cache: page_table int32 [B, max_pages], kv_lens int32 [B] (the new tokens counted), q_start int32
+    [B + 1] (None: one token a sequence).  With cos_sin fp32 [max_pos, rot_dim] keys, and q [T, n_q,
+    head_dim] -> q_out (bf16), are rotated first, by positions int32 [T] (None: the keys' places).
+    k_held, v_held: bf16 copies of what is stored."""
+    st = (_SERVE or _serve()).append(cache._c, k, v, page_table, kv_lens, q_start, max_q, positions, cos_sin, q, q_out,
+                                     k_held, v_held, _handle(stream))
+    if st:
+        raise QmmError(st, "qmm_kv8_append")
+
+
+def qmm_kv8_attn_workspace_bytes(T: int, B: int, max_q: int, n_q: int, n_kv: int, head_dim: int, max_kv: int,
+                                 window: int = 0, sinks: int = 0) -> int:
+    """Workspace bytes of qmm_kv8_attn (0 = sizes out of range); max_kv = page_table.shape[1] * page_size."""
+    return int(load_library().qmm_kv8_attn_workspace_bytes(T, B, max_q, n_q, n_kv, head_dim, max_kv, window, sinks))
+
+
+def qmm_kv8_attn(q, cache, page_table, kv_lens, out, workspace, q_start=None, max_q: int = 1, scale=None,
+                 causal: bool = True, window: int = 0, sinks: int = 0, gate=None, stream=None) -> None:
+    """Attention of q [T, n_q, head_dim] (bf16) over the cache of B sequences: page_table int32
+    [B, max_pages], kv_lens int32 [B], q_start int32 [B + 1] (None: one query a sequence); out as q.
+    window: only the last `window` keys are seen, and the first `sinks` ones.  scale: head_dim ** -0.5
+    unless given; gate (as q): out is multiplied by its sigmoid."""
+    st = (_SERVE or _serve()).attn(q, cache._c, page_table, kv_lens, out, workspace, q_start, max_q, scale,
+                                   1 if causal else 0, window, sinks, gate, _handle(stream))
+    if st:
+        raise QmmError(st, "qmm_kv8_attn")
+
+
+def qmm_spec_verify_workspace_bytes(B: int, V: int) -> int:
+    """Workspace bytes of qmm_spec_verify (0 = sizes out of range)."""
+    return int(load_library().qmm_spec_verify_workspace_bytes(B, V))
+
+
+def qmm_spec_verify(draft, target, u, tokens, accepted, workspace, draft_start, draft_probs=None, stream=None) -> None:
+    """Drafted tokens draft int32 [D] of B sequences (draft_start int32 [B + 1]) against the target's
+    probabilities [D + B, V] (bf16 or fp32), with random numbers u fp32 [D + B]; draft_probs [D, V] as
+    target (None: looked-up drafts).  tokens int32 [B, max_draft + 1]: kept drafts, the new token,
+    then -1; accepted int32 [B]."""
+    st = (_SERVE or _serve()).verify(draft, target, u, tokens, accepted, workspace, draft_start, draft_probs,
+                                     _handle(stream))
+    if st:
+        raise QmmError(st, "qmm_spec_verify")
+
+
+def qmm_lora_workspace_bytes(T: int, K: int, rank: int, n_parts: int = 1) -> int:
+    """Workspace bytes of qmm_lora (0 = sizes out of range)."""
+    return int(load_library().qmm_lora_workspace_bytes(T, K, rank, n_parts))
+
+
+def qmm_lora(x, a, b, ids, y, workspace, base=None, scales=None, stream=None) -> None:
+    """y = base + scales[i] B_i (A_i x), i = ids[t]: x [T, K] bf16, a [adapters, parts * rank, K] and b
+    [adapters, rows, rank] bf16, ids int32 [T] (outside the adapters: none), scales fp32 [adapters].
+    y: a tensor [T, rows] (bf16 or fp32) or a list of up to 3, the parts of one projection (their rows
+    follow each other in b); base likewise (None: y is updated in place)."""
+    one = not isinstance(y, (list, tuple))
+    st = (_SERVE or _serve()).lora(x, a, b, ids, (y,) if one else tuple(y), workspace,
+                                   base if base is None else (base,) if one else tuple(base), scales, _handle(stream))
+    if st:
+        raise QmmError(st, "qmm_lora")

@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libqmm.so")
 CEILING_OUT = os.path.join(PKG, "libqmm_ceiling.so")
-BINDING_OUT = os.path.join(PKG, "_qmm_mix.so")
+BINDINGS = (("mix_binding.cpp", os.path.join(PKG, "_qmm_mix.so")), ("serve_binding.cpp", os.path.join(PKG, "_qmm_serve.so")))
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 # (source, extra flags, object): the GEMV and GEMM sources are built once per code width.
@@ -30,7 +30,9 @@ SOURCES = ([("qmm_api.cpp", [], "qmm_api.o"), ("qmm_validate.cpp", [], "qmm_vali
             ("kv4_append.hip", [], "kv4_append.o"), ("kv4_decode.hip", [], "kv4_decode.o"),
             ("kv4_prefill.hip", [], "kv4_prefill.o"),
             ("gdn.hip", [], "gdn.o"),
-            ("gdn_chunk.hip", [], "gdn_chunk.o")]
+            ("gdn_chunk.hip", [], "gdn_chunk.o"), ("qmm_serve_api.cpp", [], "qmm_serve_api.o"),
+            ("kv8_append.hip", [], "kv8_append.o"), ("kv8_attn.hip", [], "kv8_attn.o"),
+            ("spec_verify.hip", [], "spec_verify.o"), ("lora.hip", [], "lora.o")]
            + [(src, [f"-DQMM_BITS={b}"], f"{src.split('.')[0]}_b{b}.o") for src in ("gemv_u4.hip", "gemm_u4.hip")
               for b in WIDTHS]
            + [(src, ["-DQMM_BITS=8", "-DQMM_FP8=1"], f"{src.split('.')[0]}_f8.o")
@@ -70,45 +72,46 @@ def _link(objs, out):
     os.replace(tmp, out)
 
 
-def _compile_binding() -> str:
-    """The token mixers' Python side (mix_binding.cpp): host code against torch's headers."""
+def _compile_binding(src: str) -> str:
+    """The Python side of the token mixers and of the serving step: host code against torch's headers."""
     import sysconfig
 
     import torch
     from torch.utils import cpp_extension
 
-    obj = os.path.join(BUILD_DIR, "mix_binding.o")
+    obj = os.path.join(BUILD_DIR, src.replace(".cpp", ".o"))
     inc = [INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths("cuda")]
     cmd = [HIPCC, "-O2", "-std=c++17", "-fPIC", "-x", "c++", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *sum((["-isystem", i] for i in inc), []),
-           "-c", os.path.join(CSRC, "mix_binding.cpp"), "-o", obj]
+           "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"compilation failed for mix_binding.cpp:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"compilation failed for {src}:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     return obj
 
 
-def _link_binding(obj: str) -> None:
+def _link_binding(obj: str, out: str) -> None:
     import torch
 
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    tmp = BINDING_OUT + ".tmp"
+    tmp = out + ".tmp"
     cmd = [HIPCC, "-shared", "-fPIC", obj, f"-L{lib}", "-lc10", "-lc10_hip", "-ltorch_cpu",
            "-ltorch_python", "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING_OUT)
+    os.replace(tmp, out)
 
 
 def build(jobs: int = 8) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     with ThreadPoolExecutor(max_workers=jobs) as ex:
-        binding = ex.submit(_compile_binding)
+        bindings = [(ex.submit(_compile_binding, src), out) for src, out in BINDINGS]
         objs = list(ex.map(_compile, SOURCES + [CEILING]))
     _link(objs[:-1], OUT)
     _link(objs[-1:], CEILING_OUT)
-    _link_binding(binding.result())
+    for obj, out in bindings:
+        _link_binding(obj.result(), out)
     return OUT
 
 

@@ -1,4 +1,4 @@
-// What the attention kernels over the paged 4-bit cache share: a sequence's place in the
+// What the attention kernels over the paged caches share (the split and the plan: 4 bits only): a sequence's place in the
 // call, the keys that a block's rows can see, their split over blocks, and the store.
 #pragma once
 #include <hip/hip_runtime.h>
@@ -38,7 +38,8 @@ struct AttnSeq {
   int first;  // position of query 0 (negative where there are more queries than keys)
 };
 // Sequence b: its rows of q (held inside [0, T] whatever q_start says) and its keys.
-__device__ __forceinline__ AttnSeq attn_seq(const Kv4AttnArgs& g, int b) {
+template <class Args>
+__device__ __forceinline__ AttnSeq attn_seq(const Args& g, int b) {
   AttnSeq s;
   int64_t a = b, e = int64_t(b) + 1;
   if (g.q_start) {
@@ -61,7 +62,8 @@ __device__ __forceinline__ AttnSeq attn_seq(const Kv4AttnArgs& g, int b) {
 // ~1.5 us at 64 sequences, so tables of up to 2048 keys keep the order given (64 single tokens on
 // 500 keys each 12 us, ordered 14).  More than 64 run in the order given, and do not even out by
 // themselves: 66 such tokens in any order 133 us, given longest first 114; 200 of them 362 and 296.
-__device__ __forceinline__ AttnSeq attn_longest_first(const Kv4AttnArgs& g, int& b, int lane) {
+template <class Args>
+__device__ __forceinline__ AttnSeq attn_longest_first(const Args& g, int& b, int lane) {
   const int n = int(gridDim.z);
   if (n == 1 || n > 64 || (int64_t(g.max_pages) << g.c.page_shift) <= 2048) return attn_seq(g, b);
   const AttnSeq s = attn_seq(g, lane < n ? lane : 0);
@@ -119,7 +121,8 @@ int launch_kv4_prefill(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t s);
 int launch_kv4_join(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t s);
 
 // Four neighbouring outputs: the weighted sum over its weight, times the gate's sigmoid.
-__device__ __forceinline__ void attn_store4(const Kv4AttnArgs& g, int64_t at, float4 o, float l) {
+template <class Args>
+__device__ __forceinline__ void attn_store4(const Args& g, int64_t at, float4 o, float l) {
   const float inv = l > 0.f ? 1.f / l : 0.f;
   float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
   if (g.gate) {

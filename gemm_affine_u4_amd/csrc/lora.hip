@@ -1,0 +1,350 @@
+// Low-rank adapters of many requests beside a shared projection (qmm_lora; include/qmm_serve.h).
+//
+// Mathematics: h = A x, then y = base + s B h, with the adapter of each token.  Both products are
+// small (a rank of 8 to 128), so they are bound by the bytes of x, base, y and the adapters
+// in use; each adapter's weights are read once for a tile of tokens that use it.
+// Split.  Tokens go in tiles of 16 (few tokens) or 64 as they stand: a block finds the distinct
+// adapters of its tile and takes those of its share of them one after the other, each as a product of
+// the adapter's weights with the whole tile, of which it keeps the columns of that adapter's tokens.
+// So nothing is sorted, requests that stand side by side share their weights' reads, and a
+// batch of many adapters is spread over blocks.
+//   shrink: weights' rows x tokens over a range of K; the block's waves take 64 inputs in turn and
+//     join in LDS; each range's sums go to the workspace.
+//   expand: adds the ranges' sums in order, times s, and takes them on as three bf16 pieces (24
+//     bits), which follow each other along the matrix product's k: for ranks up to 16 they fit
+//     in one or two instructions.  A lane ends with 16 neighbouring outputs of a token.
+#include <hip/hip_runtime.h>
+
+#include "qmm_device.h"
+#include "qmm_internal.h"
+#include "serve_internal.h"
+
+namespace qmm {
+namespace {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kWaves = 4;
+
+__device__ __forceinline__ f32x4_t mma(u32x4_t a, u32x4_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                 0, 0, 0);
+}
+
+// Waits until the last matrix instruction has written its result.  The compiler does so itself in
+// straight code, but not where a loop's last product is stored to LDS behind the loop, inside
+// another loop (seen in its output, and as a register stored too early).
+__device__ __forceinline__ void mma_settle(f32x4_t& c) { asm volatile("s_nop 7\n\ts_nop 7" : "+v"(c)); }
+
+// The distinct adapters of a tile of up to 64 tokens: lane t has token t.
+struct Tile {
+  int id;     // of the lane's token, -1: none
+  int index;  // of it among the distinct ones
+  int list;   // lane i: the i-th distinct adapter
+  int count;
+};
+__device__ __forceinline__ Tile tile_of(const LoraArgs& g, int64_t t0, int tokens, int lane) {
+  Tile r;
+  r.id = -1;
+  if (lane < tokens && t0 + lane < g.T) {
+    r.id = g.ids[t0 + lane];
+    if (uint32_t(r.id) >= uint32_t(g.n_adapters)) r.id = -1;
+  }
+  r.index = -1, r.list = 0, r.count = 0;
+  uint64_t left = __ballot(r.id >= 0);
+  while (left) {
+    const int id = __builtin_amdgcn_readlane(r.id, __ffsll(static_cast<unsigned long long>(left)) - 1);
+    const uint64_t same = __ballot(r.id == id);
+    if (r.id == id) r.index = r.count;
+    if (lane == r.count) r.list = id;
+    ++r.count;
+    left &= ~same;
+  }
+  return r;
+}
+
+// TT column tiles of 16 tokens, RT row tiles of 16 ranks.
+template <int TT, int RT>
+__global__ __launch_bounds__(kWaves * 64, 2) void lora_shrink_kernel(LoraArgs g, int row_groups, int splits, int shares) {
+  const int lane = threadIdx.x & 63, n = lane & 15, hg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int split = blockIdx.y % splits, share = blockIdx.y / splits;
+  const int64_t t0 = int64_t(blockIdx.x / row_groups) * (16 * TT);
+  const int R = g.n_parts * g.rank, r0 = int(blockIdx.x % row_groups) * (16 * RT);
+  const Tile tile = tile_of(g, t0, 16 * TT, lane);
+  if (share >= tile.count) return;
+
+  const int units = g.K / 64, u0 = units * split / splits, u1 = units * (split + 1) / splits;
+  const uint16_t* xp[TT];
+#pragma unroll
+  for (int i = 0; i < TT; ++i) {
+    const int64_t t = t0 + 16 * i + n;
+    xp[i] = g.x + (t < g.T ? t : g.T - 1) * g.K + 8 * hg;
+  }
+  __shared__ f32x4_t s_acc[kWaves][TT * RT][64];
+  for (int at = share; at < tile.count; at += shares) {
+    const int id = __builtin_amdgcn_readlane(tile.list, at);
+    const uint16_t* ap[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int r = r0 + 16 * i + n;
+      ap[i] = g.a + (int64_t(id) * R + (r < R ? r : R - 1)) * g.K + 8 * hg;
+    }
+    f32x4_t acc[TT][RT];
+#pragma unroll
+    for (int i = 0; i < TT; ++i)
+#pragma unroll
+      for (int j = 0; j < RT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int u = u0 + wave; u < u1; u += kWaves) {
+      u32x4_t xv[2][TT], av[2][RT];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i) av[k][i] = *reinterpret_cast<const u32x4_t*>(ap[i] + u * 64 + 32 * k);
+#pragma unroll
+        for (int i = 0; i < TT; ++i) xv[k][i] = *reinterpret_cast<const u32x4_t*>(xp[i] + u * 64 + 32 * k);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+#pragma unroll
+          for (int j = 0; j < RT; ++j) acc[i][j] = mma(av[k][j], xv[k][i], acc[i][j]);
+    }
+#pragma unroll
+    for (int i = 0; i < TT; ++i)
+#pragma unroll
+      for (int j = 0; j < RT; ++j) {
+        mma_settle(acc[i][j]);
+        s_acc[wave][i * RT + j][lane] = acc[i][j];
+      }
+    __syncthreads();
+    for (int e = wave; e < TT * RT; e += kWaves) {
+      f32x4_t v = s_acc[0][e][lane];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) v += s_acc[w][e][lane];
+      const int tt = 16 * (e / RT) + n, r = r0 + 16 * (e % RT) + 4 * hg;
+      if (__shfl(tile.index, tt) == at && r < R)
+        *reinterpret_cast<f32x4_t*>(g.ws + (int64_t(split) * g.T + t0 + tt) * R + r) = v;
+    }
+    __syncthreads();
+  }
+}
+
+// Rows of the part `p` from n0 on: 64 of them a wave.
+template <int RANK>
+struct Expand {
+  static constexpr int kChunks = RANK / 8;                        // of 8 along k
+  static constexpr int kSteps = (3 * kChunks + 3) / 4;            // matrix instructions of the three pieces
+  static constexpr int kLoads = RANK > 32 ? RANK / 32 : 1;        // distinct weight operands
+};
+
+template <bool BASE32>
+__device__ __forceinline__ float base_at(const void* p, int64_t at) {
+  if constexpr (BASE32) return static_cast<const float*>(p)[at];
+  else return bf16_bits_to_f32(static_cast<const uint16_t*>(p)[at]);
+}
+
+// VEC: every part's rows are a multiple of 16 and its arrays 16-byte aligned.
+template <int TT, int RANK, bool BASE32, bool OUT32, bool VEC>
+__global__ __launch_bounds__(kWaves * 64) void lora_expand_kernel(LoraArgs g, int row_chunks, int splits, int shares) {
+  using E = Expand<RANK>;
+  constexpr int TOK = 16 * TT, ROW = RANK + 8;  // bf16 of a token's piece in LDS, 16 bytes of pad
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, hg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t t0 = int64_t(blockIdx.x / row_chunks) * TOK;
+  const int share = blockIdx.y;
+  // the block's part and rows
+  int chunk = blockIdx.x % row_chunks, part = 0, first = 0;
+  for (;; ++part) {
+    const int c = (g.rows[part] + 255) / 256;
+    if (chunk < c) break;
+    chunk -= c;
+    first += g.rows[part];
+  }
+  const int N = g.rows[part], n0 = chunk * 256 + wave * 64;
+  const void* base = g.base[part];
+  void* y = g.y[part];
+  const int total = g.rows[0] + g.rows[1] + g.rows[2], R = g.n_parts * RANK;
+
+  const Tile tile = tile_of(g, t0, TOK, lane);
+  if (share > 0 && share >= tile.count) return;
+
+  // h of the tile's tokens that are this block's, times the adapter's factor, in three pieces
+  __shared__ __attribute__((aligned(16))) uint16_t s_h[3][TOK][ROW];
+  for (int e0 = 0; e0 < TOK * RANK / 4; e0 += kWaves * 64) {
+    const int e = e0 + tid, t = e / (RANK / 4), r = e % (RANK / 4) * 4;
+    const int index = __shfl(tile.index, t & 63), id = __shfl(tile.id, t & 63);
+    if (t >= TOK || index < 0 || index % shares != share) continue;
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+    const float* p = g.ws + (t0 + t) * R + part * RANK + r;
+    for (int i = 0; i < splits; ++i) v += *reinterpret_cast<const f32x4_t*>(p + int64_t(i) * g.T * R);
+    const float f = g.scales ? g.scales[id] : 1.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x = v[i] * f;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const uint16_t h = f32_to_bf16_bits(x);
+        s_h[k][t][r + i] = h;
+        x -= bf16_bits_to_f32(h);
+      }
+    }
+  }
+  __syncthreads();
+  if (n0 >= N) return;
+
+  // rows 4h + i of product j are outputs n0 + 16 h + 4 j + i: a lane ends with 16 neighbours
+  const int wrow = n0 + 16 * (n >> 2) + (n & 3);
+  auto columns = [&](auto keep, const f32x4_t (&acc)[TT][4]) {
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+      const int64_t t = t0 + 16 * i + n;
+      const int o0 = n0 + 16 * hg;
+      const int index = __shfl(tile.index, 16 * i + n);
+      if (t >= g.T || !keep(index) || o0 >= N) continue;
+      const int64_t at = t * N + o0;
+      if constexpr (VEC) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f32x4_t v;
+          if constexpr (BASE32) {
+            v = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(base) + at + 4 * j);
+          } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + at + 4 * j);
+            v = f32x4_t{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+          }
+          v += acc[i][j];
+          if constexpr (OUT32) *reinterpret_cast<f32x4_t*>(static_cast<float*>(y) + at + 4 * j) = v;
+          else
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + at + 4 * j) =
+                uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (o0 + e < N) store_out(y, at + e, base_at<BASE32>(base, at + e) + acc[i][e >> 2][e & 3], OUT32);
+      }
+    }
+  };
+  f32x4_t acc[TT][4];
+  for (int at = share; at < tile.count; at += shares) {
+    const int id = __builtin_amdgcn_readlane(tile.list, at);
+    const uint16_t* b = g.b + (int64_t(id) * total + first) * RANK;
+    u32x4_t w[4][E::kLoads];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = wrow + 4 * j < N ? wrow + 4 * j : N - 1;
+#pragma unroll
+      for (int l = 0; l < E::kLoads; ++l)
+        w[j][l] = *reinterpret_cast<const u32x4_t*>(b + int64_t(row) * RANK + 8 * ((4 * l + hg) % E::kChunks));
+    }
+#pragma unroll
+    for (int i = 0; i < TT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int m = 0; m < E::kSteps; ++m) {
+      const int c = 4 * m + hg, piece = c / E::kChunks, k8 = c % E::kChunks;
+#pragma unroll
+      for (int i = 0; i < TT; ++i) {
+        u32x4_t h = {0, 0, 0, 0};
+        if (piece < 3) h = *reinterpret_cast<const u32x4_t*>(&s_h[piece < 3 ? piece : 0][16 * i + n][8 * k8]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = mma(w[j][m % E::kLoads], h, acc[i][j]);
+      }
+    }
+    columns([&](int index) { return index == at; }, acc);
+  }
+  if (share == 0 && (base != y || BASE32 != OUT32)) {  // tokens without an adapter
+#pragma unroll
+    for (int i = 0; i < TT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    columns([&](int index) { return index < 0; }, acc);
+  }
+}
+
+// How a call is cut: a function of the sizes that its workspace is asked for with.
+struct Plan {
+  int tt, rt, row_groups, splits, shares;
+  int64_t tiles;
+};
+Plan plan_of(int64_t T, int64_t K, int64_t rank, int64_t n_parts) {
+  Plan p;
+  const int64_t R = rank * n_parts;
+  p.tt = T > 256 ? 4 : 1;
+  p.rt = T > 256 && R > 16 ? (R > 32 ? 4 : 2) : 1;
+  p.tiles = (T + 16 * p.tt - 1) / (16 * p.tt);
+  p.row_groups = int((R + 16 * p.rt - 1) / (16 * p.rt));
+  p.shares = p.tt == 1 ? int(T < 16 ? T < 1 ? 1 : T : 16) : 4;
+  const int64_t blocks = p.tiles * p.row_groups * (p.tt == 1 ? p.shares : 1), most = (K / 64 + kWaves - 1) / kWaves;
+  int64_t s = (4 * device_cus() + blocks - 1) / (blocks ? blocks : 1);
+  s = s > most ? most : s;
+  p.splits = int(s < 1 ? 1 : s > 64 ? 64 : s);
+  return p;
+}
+
+template <int TT, int RT>
+void shrink(const LoraArgs& a, const Plan& p, hipStream_t s) {
+  lora_shrink_kernel<TT, RT><<<dim3(uint32_t(p.tiles * p.row_groups), uint32_t(p.splits * p.shares)), kWaves * 64, 0,
+                               s>>>(a, p.row_groups, p.splits, p.shares);
+}
+
+template <int TT, int RANK, bool B32, bool O32>
+void expand_v(const LoraArgs& a, const Plan& p, hipStream_t s) {
+  int chunks = 0;
+  bool vec = true;
+  for (int i = 0; i < 3; ++i) {
+    chunks += (a.rows[i] + 255) / 256;
+    vec = vec && a.rows[i] % 16 == 0 &&
+          (reinterpret_cast<uintptr_t>(a.base[i]) | reinterpret_cast<uintptr_t>(a.y[i])) % 16 == 0;
+  }
+  const dim3 grid(uint32_t(p.tiles * chunks), uint32_t(p.shares));
+  if (vec) lora_expand_kernel<TT, RANK, B32, O32, true><<<grid, kWaves * 64, 0, s>>>(a, chunks, p.splits, p.shares);
+  else lora_expand_kernel<TT, RANK, B32, O32, false><<<grid, kWaves * 64, 0, s>>>(a, chunks, p.splits, p.shares);
+}
+template <int TT, int RANK>
+void expand_r(const LoraArgs& a, const Plan& p, hipStream_t s) {
+  if (a.base_f32) a.out_f32 ? expand_v<TT, RANK, true, true>(a, p, s) : expand_v<TT, RANK, true, false>(a, p, s);
+  else a.out_f32 ? expand_v<TT, RANK, false, true>(a, p, s) : expand_v<TT, RANK, false, false>(a, p, s);
+}
+template <int TT>
+void expand(const LoraArgs& a, const Plan& p, hipStream_t s) {
+  switch (a.rank) {
+    case 8: return expand_r<TT, 8>(a, p, s);
+    case 16: return expand_r<TT, 16>(a, p, s);
+    case 32: return expand_r<TT, 32>(a, p, s);
+    case 64: return expand_r<TT, 64>(a, p, s);
+    default: return expand_r<TT, 128>(a, p, s);
+  }
+}
+
+}  // namespace
+
+bool lora_launches(int64_t T, const int32_t (&rows)[3]) {
+  const int64_t chunks = (int64_t(rows[0]) + 255) / 256 + (int64_t(rows[1]) + 255) / 256 + (int64_t(rows[2]) + 255) / 256;
+  return ((T + 63) / 64 + 16) * chunks < int64_t(1) << 24;
+}
+
+uint64_t lora_workspace(int64_t T, int64_t K, int64_t rank, int64_t n_parts) {
+  const uint64_t n = uint64_t(plan_of(T, K, rank, n_parts).splits) * uint64_t(T) * uint64_t(rank * n_parts) * 4;
+  return n ? n : 256;
+}
+
+int launch_lora(const LoraArgs& a, hipStream_t s) {
+  const Plan p = plan_of(a.T, a.K, a.rank, a.n_parts);
+  if (p.tt == 1) {
+    shrink<1, 1>(a, p, s);
+    expand<1>(a, p, s);
+  } else {
+    if (p.rt == 1) shrink<4, 1>(a, p, s);
+    else if (p.rt == 2) shrink<4, 2>(a, p, s);
+    else shrink<4, 4>(a, p, s);
+    expand<4>(a, p, s);
+  }
+  return hipGetLastError() == hipSuccess ? 0 : 6;
+}
+
+}  // namespace qmm
