@@ -1,0 +1,472 @@
+// Attention of few queries over the paged 8-bit cache (qmm_kv8_attn's serving form).
+//
+// Mathematics.  With the scales s_k, s_v of a key's block, the score is s_k (q . c_k) and the output
+// sum_t (p_t s_v) c_v / sum_t p_t: codes enter both matrix products exactly (as fp16 numbers), queries
+// exactly (bf16 values times a power of two).  Weights times scales are rounded to fp16
+// (2^-11; with the scales lifted by a power of two that brings a wave's largest one so far to 2^11, below
+// 2^-28 of the largest weight and scale by 2^-39 of it); the rest is fp32.
+//
+// Bound: the cache's bytes (HBM) for long contexts, launch and latency for short ones.
+//
+// Split.  A block of 4 or 8 waves takes one KV head's up to 16 (query, head) rows and a range of
+// keys; its waves take 32 keys at a time and keep an online softmax of their own (maximum,
+// sum and output in registers, no barrier), joined once at the end.  Keys are the rows of
+// the first product (S^T = K Q^T) and dims the rows of the second (O^T = V^T P^T), so a lane
+// that gets the scores of keys 8h .. 8h+7 of its column holds exactly the weights that the
+// second product wants from it: nothing crosses lanes between the two, and its eight keys
+// share their scales.
+#include <hip/hip_runtime.h>
+
+#include "kv8_attn.h"
+#include "qmm_internal.h"
+
+namespace qmm {
+namespace {
+
+constexpr int kTile = 32;         // keys of a wave's step
+constexpr float kFloor = -1e30f;  // maximum of a row that has seen no key yet
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ f32x4_t mma16(f16x8_t a, f16x8_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+template <int HD>
+struct Buf {
+  static constexpr int NK = HD / 64, NV = HD / 32;
+  u32x4_t k[2][NK];  // key codes of the two 16-key products: 16 dims each
+  u32x4_t v[NV];     // value codes: 8 keys x 2 dims of each 32
+  float ks, vs;      // scales of the lane's keys (lane group's eight)
+};
+
+template <int HD, bool PG32, int NW>
+__global__ __launch_bounds__(NW * 64, 2) void kv8_decode_kernel(Kv8AttnArgs g, int group, Attn8Plan plan) {
+  using B = Buf<HD>;
+  constexpr int NK = B::NK, NV = B::NV;
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, hg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int split = blockIdx.x;
+  int b = blockIdx.z;
+  const int kvh = blockIdx.y % g.c.n_kv, rt = blockIdx.y / g.c.n_kv;
+
+  const AttnSeq sq = attn_longest_first(g, b, lane);
+  const int row0 = rt * 16, rows = sq.q_len * group - row0;
+  if (rows <= 0) return;
+  const Attn8Tiles pl = attn8_tiles(g, sq, row0, rows < 16 ? rows : 16, group, plan, split);
+  if (split >= pl.count) return;
+
+  // Pages, a window of 64 of the wave's tiles at a time: lane i holds the page of its i-th
+  // tile from the window's first on (and of its second half, where pages are of 16).
+  const int psh = g.c.page_shift, pmask = (1 << psh) - 1;
+  const int32_t* __restrict__ table = g.table + int64_t(b) * g.max_pages;
+  const int last_key = sq.kv_len > 0 ? sq.kv_len - 1 : 0;
+  int t = pl.begin + wave, window = t;  // tiles by number
+  int pages0 = 0, pages1 = 0;           // 0 where there is no page,
+  uint64_t there0 = 0, there1 = 0;      // its bit clear then
+  auto enter = [&](int v) {
+    window = v;
+    const int64_t key = int64_t(pl.at(v + lane * NW)) * kTile;
+    const int k = int(key < last_key ? key : last_key), k1 = int(key + 16 < last_key ? key + 16 : last_key);
+    // checked here, so that the wait for the entries stays in this rare branch
+    const int id0 = table[k >> psh];
+    there0 = __ballot(uint32_t(id0) < uint32_t(g.c.n_pages));
+    pages0 = uint32_t(id0) < uint32_t(g.c.n_pages) ? id0 : 0;
+    if constexpr (!PG32) {
+      const int id1 = table[k1 >> psh];
+      there1 = __ballot(uint32_t(id1) < uint32_t(g.c.n_pages));
+      pages1 = uint32_t(id1) < uint32_t(g.c.n_pages) ? id1 : 0;
+    }
+  };
+  enter(t);
+
+  // a tile's first key, the rows (token slots of this head) of its two halves, and whether their page exists
+  struct Where {
+    int64_t r0, r1;
+    int key;
+    bool ok0, ok1;
+  };
+  auto where = [&](int v) {
+    Where w;
+    const int i = (v - window) / NW;
+    w.key = pl.at(v) * kTile;
+    w.ok0 = (there0 >> i) & 1;
+    w.r0 = ((int64_t(__builtin_amdgcn_readlane(pages0, i)) * g.c.n_kv + kvh) << psh) + (w.key & pmask);
+    if constexpr (PG32) {
+      w.ok1 = w.ok0;
+      w.r1 = w.r0 + 16;
+    } else {
+      w.ok1 = (there1 >> i) & 1;
+      w.r1 = ((int64_t(__builtin_amdgcn_readlane(pages1, i)) * g.c.n_kv + kvh) << psh) + ((w.key + 16) & pmask);
+    }
+    return w;
+  };
+  auto load = [&](const Where& w, B& x) {
+    // the lane's key of product u: 8 (n / 4) + 4u + n % 4
+    const int64_t rk = (n < 8 ? w.r0 : w.r1) + 8 * ((n >> 2) & 1) + (n & 3);
+    const int64_t rv = (hg < 2 ? w.r0 : w.r1) + 8 * (hg & 1);
+    const int8_t* kp = g.c.k_codes + rk * HD + 16 * hg;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int p = 0; p < NK; ++p)
+        x.k[u][p] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(kp + 4 * u * HD + 64 * p));
+    x.ks = g.c.k_scale[rv >> 4];
+    x.vs = g.c.v_scale[rv >> 4];
+    const int8_t* vp = g.c.v_codes + rv * HD + 16 * n;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) x.v[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(vp + i * 256));
+  };
+
+  // Behind its last tile a wave loads that one again: were the loads conditional, the wait for
+  // a tile's own would have to wait for the next one's too.
+  const int t_last = t + (t < pl.end ? (pl.end - 1 - t) / NW * NW : 0);
+  auto ahead = [&](int v, Where& w, B& x) {
+    const int tc = v < t_last ? v : t_last;
+    if (tc - window >= 64 * NW) enter(tc);
+    w = where(tc);
+    load(w, x);
+  };
+  B x0, x1;
+  Where w0, w1;
+  ahead(t, w0, x0);  // under way while the queries are laid out
+
+  // the lane's column: one (query, head) row
+  const bool col_ok = n < rows;
+  const int cj = (row0 + n) / group, ch = kvh * group + (row0 + n) % group;
+  const int64_t qrow = (int64_t(sq.q0) + cj) * g.n_q + ch;
+  int c_lo = 0, c_hi = sq.kv_len;
+  if (col_ok && g.causal) {
+    const int64_t p = int64_t(sq.first) + cj;
+    c_hi = p < 0 ? 0 : int(p) + 1;
+    c_lo = g.window > 0 && p - g.window + 1 > 0 ? int(p - g.window + 1) : 0;
+  }
+  const int sinks = int(g.sinks < sq.kv_len ? g.sinks : sq.kv_len);
+
+  // q as operands: fp16 scaled by a power of two so that the row's largest is in [2^7, 2^8) (a
+  // code's product stays below 2^15); bf16 values stay exact down to 2^-24 of that
+  f16x8_t qf[NK][2];
+  float qs;
+  {
+    u32x4_t raw[NK][2];
+    float mx = 0.f;
+#pragma unroll
+    for (int p = 0; p < NK; ++p)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        raw[p][e] = u32x4_t{0, 0, 0, 0};
+        if (col_ok) raw[p][e] = *reinterpret_cast<const u32x4_t*>(g.q + qrow * HD + 64 * p + 16 * hg + 8 * e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(raw[p][e][i])), fabsf(bf16_hi(raw[p][e][i]))));
+      }
+    mx = fmaxf(mx, __shfl_xor(mx, 16));
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    const int ex = mx > 0.f ? int((__float_as_uint(mx) >> 23) & 255) - 127 : 0;
+    const int sh = 7 - ex;  // in [-120, 134]
+    qs = fminf(g.scale * kLog2e * ldexpf(1.f, -sh), 3e38f);  // finite: it meets differences of 0
+#pragma unroll
+    for (int p = 0; p < NK; ++p)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          qf[p][e][2 * i] = static_cast<_Float16>(ldexpf(bf16_lo(raw[p][e][i]), sh));
+          qf[p][e][2 * i + 1] = static_cast<_Float16>(ldexpf(bf16_hi(raw[p][e][i]), sh));
+        }
+  }
+
+  // wave-uniform: tiles wholly inside [u_lo, u_hi) or the first keys need no mask
+  int u_lo = c_lo, u_hi = c_hi;
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) {
+    u_lo = max(u_lo, __shfl_xor(u_lo, o));
+    u_hi = min(u_hi, __shfl_xor(u_hi, o));
+  }
+  u_lo = __builtin_amdgcn_readfirstlane(u_lo);
+  u_hi = __builtin_amdgcn_readfirstlane(u_hi);
+
+  f32x4_t acc[NV][2];  // in units of 1 / lift
+  float m = kFloor, l = 0.f;
+  // All value scales met so far are below vtop, a power of two; lift brings that to 2^12.
+  float vtop = 0x1p-100f, lift = 0x1p112f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  auto step = [&](const B& x, const Where& w) {
+    const bool masked = w.key + kTile > u_hi || (w.key < u_lo && w.key + kTile > sinks) || !w.ok0 || !w.ok1;
+    const int tb = w.key + 8 * hg;
+    float vs = x.vs;
+    // keys that are not there may have any scale, NaN among them
+    if (masked) vs = (hg < 2 ? w.ok0 : w.ok1) && tb < sq.kv_len ? vs : 0.f;
+    float sc[8];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      f32x4_t d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int p = 0; p < NK; ++p) {
+        d = mma16(code_operand(x.k[u][p][0], x.k[u][p][1]), qf[p][0], d);
+        d = mma16(code_operand(x.k[u][p][2], x.k[u][p][3]), qf[p][1], d);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sc[4 * u + i] = x.ks * d[i];
+    }
+    uint32_t vis = 0xFF;
+    if (masked) {
+      const bool ok = hg < 2 ? w.ok0 : w.ok1;
+      vis = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool see = ok && (tb + i >= c_lo || tb + i < sinks) && tb + i < c_hi;
+        vis |= see ? 1u << i : 0u;
+        sc[i] = see ? sc[i] : -INFINITY;
+      }
+    }
+    float mx = fmaxf(fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])), fmaxf(fmaxf(sc[4], sc[5]), fmaxf(sc[6], sc[7])));
+    if (__any(mx > m || vs >= vtop)) {
+      mx = fmaxf(mx, __shfl_xor(mx, 16));
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      const float mn = fmaxf(m, mx);
+      const float fac = exp2_hw((m - mn) * qs);
+      m = mn;
+      float vfac = fac;
+      if (__any(vs >= vtop)) {  // larger value scales than the wave has met
+        float top = vs;
+#pragma unroll
+        for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+        const uint32_t e = __builtin_amdgcn_readfirstlane(__float_as_uint(top) >> 23);
+        lift = __uint_as_float((265 - e) << 23);
+        vfac *= vtop * lift * 0x1p-12f;
+        vtop = __uint_as_float((e + 1) << 23);
+      }
+      l *= fac;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] *= vfac;
+    }
+    vs *= lift;
+    // weights times 8 (p <= 1 and lifted scales below 2^12 keep p s within fp16).  The difference comes
+    // first: rounded products of scores of 2^20 and more would be off by a factor of their own.
+    f16x8_t pf;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      float p0 = exp2_hw(fmaf(sc[i] - m, qs, 3.f)), p1 = exp2_hw(fmaf(sc[i + 1] - m, qs, 3.f));
+      if (masked) {
+        p0 = (vis >> i) & 1 ? p0 : 0.f;
+        p1 = (vis >> (i + 1)) & 1 ? p1 : 0.f;
+      }
+      l += p0;
+      l += p1;
+      const f16x2_t h = half_pair(p0 * vs, p1 * vs);
+      pf[i] = h[0], pf[i + 1] = h[1];
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[i][j] = mma16(code_operand(x.v[i][2 * j], x.v[i][2 * j + 1]), pf, acc[i][j]);
+  };
+
+  // the wave's tiles, the next one's loads under way while one is computed
+  if (t < pl.end) {
+    for (;;) {
+      ahead(t + NW, w1, x1);
+      step(x0, w0);
+      if ((t += NW) > t_last) break;
+      ahead(t + NW, w0, x0);
+      step(x1, w1);
+      if ((t += NW) > t_last) break;
+    }
+  }
+
+  // join the waves
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  __shared__ __attribute__((aligned(16))) float s_o[NW][16][HD + 4];
+  __shared__ float s_m[NW][16], s_l[NW][16], s_qs[16];
+  if (hg == 0) {
+    s_m[wave][n] = m;
+    s_l[wave][n] = l;
+    if (wave == 0) s_qs[n] = qs;
+  }
+  __syncthreads();
+  float mm = kFloor;
+#pragma unroll
+  for (int i = 0; i < NW; ++i) mm = fmaxf(mm, s_m[i][n]);
+  if (col_ok) {
+    const float fac = exp2_hw((m - mm) * qs), unit = vtop * 0x1p-12f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {  // rows 4h + e are dims 8h + 2e + j
+        o[2 * e] = acc[i][0][e] * unit * fac;
+        o[2 * e + 1] = acc[i][1][e] * unit * fac;
+      }
+      float* to = &s_o[wave][n][32 * i + 8 * hg];
+      *reinterpret_cast<float4*>(to) = float4{o[0], o[1], o[2], o[3]};
+      *reinterpret_cast<float4*>(to + 4) = float4{o[4], o[5], o[6], o[7]};
+    }
+  }
+  __syncthreads();
+  const int cols = rows < 16 ? rows : 16;
+  constexpr int Q = HD / 4;  // float4s of a row
+  for (int e = tid; e < cols * Q; e += NW * 64) {
+    const int c = e / Q, d = (e % Q) * 4;
+    float cm = kFloor, cl = 0.f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) cm = fmaxf(cm, s_m[i][c]);
+    const float cqs = s_qs[c];
+    float4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      cl = fmaf(s_l[i][c], exp2_hw((s_m[i][c] - cm) * cqs), cl);
+      const float4 v = *reinterpret_cast<const float4*>(&s_o[i][c][d]);
+      o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+    }
+    const int j = (row0 + c) / group, h = kvh * group + (row0 + c) % group;
+    const int64_t row = (int64_t(sq.q0) + j) * g.n_q + h;
+    if (pl.count == 1) {
+      attn_store4(g, row * HD + d, o, cl);
+    } else {
+      const int64_t R0 = g.T * g.n_q, at = split * R0 + row;
+      float* po = static_cast<float*>(g.ws);
+      *reinterpret_cast<float4*>(po + at * HD + d) = o;
+      if (d == 0) {
+        float* pm = po + plan.nsplit * R0 * HD;
+        pm[at * 2] = cm;  // as it is: the join scales differences, as the waves do
+        pm[at * 2 + 1] = cl;
+        if (split == 0) pm[plan.nsplit * R0 * 2 + row] = cqs;
+      }
+    }
+  }
+}
+
+// Joins the splits of (query, head) rows.  S groups of HD / 4 lanes a row share its splits: one
+// where rows are many or splits few.
+template <int HD, int S>
+__global__ __launch_bounds__(256) void kv8_join_kernel(Kv8AttnArgs g, int group, Attn8Plan plan) {
+  constexpr int LPR = HD / 4, RPB = 256 / LPR / S;  // lanes of a row's group, rows of a block
+  const int b = blockIdx.z, kvh = blockIdx.y;
+  const int part = (threadIdx.x / LPR) % S, slot = threadIdx.x / LPR / S;
+  const int rr = int(blockIdx.x) * RPB + slot, d = (threadIdx.x % LPR) * 4;
+  const AttnSeq sq = attn_seq(g, b);
+  int count = 0;
+  if (rr < sq.q_len * group) {
+    const int row0 = rr / plan.rows * plan.rows, rows = sq.q_len * group - row0;
+    count = attn8_tiles(g, sq, row0, rows < plan.rows ? rows : plan.rows, group, plan, 0).count;
+  }
+  const int64_t row = (int64_t(sq.q0) + rr / group) * g.n_q + kvh * group + rr % group, R0 = g.T * g.n_q;
+  const float* po = static_cast<const float*>(g.ws);
+  const float* pm = po + plan.nsplit * R0 * HD;
+  float4 o = {0.f, 0.f, 0.f, 0.f};
+  float l = 0.f;
+  if (count > 1) {
+    const float qs = pm[plan.nsplit * R0 * 2 + row];
+    float mm = -INFINITY;
+#pragma unroll 4
+    for (int s = 0; s < count; ++s) mm = fmaxf(mm, pm[(s * R0 + row) * 2]);
+#pragma unroll 4
+    for (int s = part; s < count; s += S) {
+      const int64_t at = s * R0 + row;
+      const float f = exp2_hw((pm[at * 2] - mm) * qs);
+      const float4 v = *reinterpret_cast<const float4*>(po + at * HD + d);
+      l = fmaf(pm[at * 2 + 1], f, l);
+      o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+    }
+  }
+  if constexpr (S > 1) {
+    __shared__ float4 s_o[256];
+    __shared__ float s_l[256];
+    s_o[threadIdx.x] = o;
+    s_l[threadIdx.x] = l;
+    __syncthreads();
+    if (part == 0) {
+#pragma unroll
+      for (int i = 1; i < S; ++i) {
+        const float4 v = s_o[threadIdx.x + i * LPR];
+        o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+        l += s_l[threadIdx.x + i * LPR];
+      }
+    }
+  }
+  if (count > 1 && part == 0) attn_store4(g, row * HD + d, o, l);
+}
+
+template <int HD>
+int launch_hd(const Kv8AttnArgs& a, const Attn8Plan& p, hipStream_t s) {
+  const int group = a.n_q / a.c.n_kv;
+  const int64_t rts = (int64_t(a.max_q) * group + 15) / 16;
+  const dim3 grid(uint32_t(p.nsplit), uint32_t(a.c.n_kv * rts), uint32_t(a.B));
+  if (p.waves == 8) {
+    if (a.c.page_shift >= 5) kv8_decode_kernel<HD, true, 8><<<grid, 512, 0, s>>>(a, group, p);
+    else kv8_decode_kernel<HD, false, 8><<<grid, 512, 0, s>>>(a, group, p);
+  } else {
+    if (a.c.page_shift >= 5) kv8_decode_kernel<HD, true, 4><<<grid, 256, 0, s>>>(a, group, p);
+    else kv8_decode_kernel<HD, false, 4><<<grid, 256, 0, s>>>(a, group, p);
+  }
+  return hipGetLastError() == hipSuccess ? 0 : 6;
+}
+
+template <int HD>
+int join_hd(const Kv8AttnArgs& a, const Attn8Plan& p, hipStream_t s) {
+  constexpr int RPB = 1024 / HD;  // groups of HD / 4 lanes in a block
+  const int group = a.n_q / a.c.n_kv;
+  const uint32_t rows = uint32_t(a.max_q * group);
+  if (p.nsplit > 8)
+    kv8_join_kernel<HD, RPB><<<dim3(rows, uint32_t(a.c.n_kv), uint32_t(a.B)), 256, 0, s>>>(a, group, p);
+  else
+    kv8_join_kernel<HD, 1><<<dim3((rows + RPB - 1) / RPB, uint32_t(a.c.n_kv), uint32_t(a.B)), 256, 0, s>>>(a, group, p);
+  return hipGetLastError() == hipSuccess ? 0 : 6;
+}
+
+}  // namespace
+
+Attn8Plan attn8_plan(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t hd, int64_t max_kv, int64_t window,
+                     int64_t sinks) {
+  const int64_t rows = max_q * (n_q / n_kv), cus = device_cus();
+  // keys that the rows of a block can see at most
+  int64_t seen = max_kv;
+  if (window > 0 && window + max_q + sinks + 64 < max_kv) seen = window + max_q + sinks + 64;
+  Attn8Plan p;
+  p.rows = 16;
+  const int64_t blocks = B * n_kv * ((rows + p.rows - 1) / p.rows);
+  p.shift = 5, p.keys = 1024;
+  while (p.keys > 128 && blocks * ((seen + p.keys - 1) / p.keys) <= cus / 2) p.keys /= 2;
+  int64_t ns = 8 * cus / blocks < 4 ? 8 * cus / blocks : 4;
+  if (ns < cus / blocks) ns = cus / blocks;
+  if (seen <= 768 || seen <= 2 * p.keys) ns = 1;
+  const int64_t most = (seen + p.keys - 1) / p.keys;
+  ns = ns > most ? most : ns;
+  p.nsplit = int(ns > 256 ? 256 : ns < 1 ? 1 : ns);
+  p.waves = blocks * p.nsplit <= cus / 2 ? 8 : 4;
+  return p;
+}
+
+int launch_kv8_decode(const Kv8AttnArgs& a, const Attn8Plan& p, hipStream_t s) {
+  if (a.c.hd == 64) return launch_hd<64>(a, p, s);
+  if (a.c.hd == 128) return launch_hd<128>(a, p, s);
+  return launch_hd<256>(a, p, s);
+}
+
+int launch_kv8_join(const Kv8AttnArgs& a, const Attn8Plan& p, hipStream_t s) {
+  if (a.c.hd == 64) return join_hd<64>(a, p, s);
+  if (a.c.hd == 128) return join_hd<128>(a, p, s);
+  return join_hd<256>(a, p, s);
+}
+
+uint64_t kv8_attn_workspace(int64_t T, int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t hd,
+                            int64_t max_kv, int64_t window, int64_t sinks) {
+  const uint64_t ns = uint64_t(attn8_plan(B, max_q, n_q, n_kv, hd, max_kv, window, sinks).nsplit);
+  // of a row: each split's output, maximum and sum; the factor of its scores
+  return ns > 1 ? uint64_t(T) * uint64_t(n_q) * (ns * uint64_t(hd + 2) + 1) * 4 : 256;
+}
+
+int launch_kv8_attn(const Kv8AttnArgs& a, hipStream_t s) {
+  const Attn8Plan p = attn8_plan(a.B, a.max_q, a.n_q, a.c.n_kv, a.c.hd, int64_t(a.max_pages) << a.c.page_shift,
+                                 a.window, a.sinks);
+  const int st = launch_kv8_decode(a, p, s);
+  return st || p.nsplit == 1 ? st : launch_kv8_join(a, p, s);
+}
+
+}  // namespace qmm

@@ -57,6 +57,9 @@ bool attn_sizes_ok(int64_t T, int64_t B, int64_t max_q, int64_t n_q, int64_t n_k
   return (max_q * (n_q / n_kv) + 127) / 128 * n_kv <= 65535;  // a grid dimension
 }
 
+// Windows and first keys beyond any table are as good as that.
+int64_t within_keys(int64_t x) { return x < kMaxI32 ? x : kMaxI32; }
+
 bool lora_sizes_ok(int64_t T, int64_t K, int64_t rank, int64_t n_parts) {
   return T >= 0 && T <= kMaxTokens && qmm::k_ok(K) && n_parts >= 1 && n_parts <= 3 &&
          (rank == 8 || rank == 16 || rank == 32 || rank == 64 || rank == 128);
@@ -122,7 +125,8 @@ int qmm_kv8_append(const qmm_kv8_cache* cache, const void* k, const void* v, int
 size_t qmm_kv8_attn_workspace_bytes(int64_t T, int64_t B, int64_t max_q, int64_t n_q_heads, int64_t n_kv_heads,
                                     int64_t head_dim, int64_t max_kv, int64_t window, int64_t sinks) {
   if (!attn_sizes_ok(T, B, max_q, n_q_heads, n_kv_heads, head_dim, max_kv, window, sinks)) return 0;
-  return size_t(qmm::kv8_attn_workspace(T, B, max_q, n_q_heads, n_kv_heads, head_dim, max_kv, window, sinks));
+  return size_t(qmm::kv8_attn_workspace(T, B, max_q, n_q_heads, n_kv_heads, head_dim, max_kv, within_keys(window),
+                                        within_keys(sinks)));
 }
 
 int qmm_kv8_attn(const uint16_t* q, int64_t T, const int32_t* q_start, const int32_t* kv_lens,
@@ -139,6 +143,7 @@ int qmm_kv8_attn(const uint16_t* q, int64_t T, const int32_t* q_start, const int
       !attn_sizes_ok(T, B, max_q, n_q_heads, cache->n_kv_heads, hd, max_pages * cache->page_size, window, sinks) ||
       (!q_start && (T != B || max_q != 1)) || (window > 0 && !causal) || !(scale > 0.f) || !std::isfinite(scale))
     return QMM_ERR_SHAPE;
+  window = within_keys(window), sinks = within_keys(sinks);
   const uint64_t need = qmm::kv8_attn_workspace(T, B, max_q, n_q_heads, cache->n_kv_heads, hd,
                                                 max_pages * cache->page_size, window, sinks);
   if (workspace_bytes < need) return QMM_ERR_SHAPE;
