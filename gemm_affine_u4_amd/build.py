@@ -32,6 +32,7 @@ SOURCES = ([("qmm_api.cpp", [], "qmm_api.o"), ("qmm_validate.cpp", [], "qmm_vali
             ("gdn.hip", [], "gdn.o"),
             ("gdn_chunk.hip", [], "gdn_chunk.o"), ("qmm_serve_api.cpp", [], "qmm_serve_api.o"),
             ("kv8_append.hip", [], "kv8_append.o"), ("kv8_decode.hip", [], "kv8_decode.o"),
+            ("kv8_prefill.hip", [], "kv8_prefill.o"),
             ("spec_verify.hip", [], "spec_verify.o"), ("lora.hip", [], "lora.o")]
            + [(src, [f"-DQMM_BITS={b}"], f"{src.split('.')[0]}_b{b}.o") for src in ("gemv_u4.hip", "gemm_u4.hip")
               for b in WIDTHS]

@@ -9,13 +9,13 @@ namespace qmm {
 
 // How a call is cut: a function of its sizes alone (host), the same for its workspace.
 struct Attn8Plan {
-  int rows;    // (query, head) rows of a block: 16 (kv8_decode.hip) or kAttn8Rows (kv8_prefill.hip)
+  int rows;    // (query, head) rows of a block: 16 (kv8_decode.hip) or attn8_rows (kv8_prefill.hip)
   int waves;   // of a block
   int shift;   // log2 of the keys of a tile
   int nsplit;  // at most this many splits of a block's keys ...
   int keys;    // ... of at least this many keys
 };
-constexpr int kAttn8Rows = 128;
+constexpr int attn8_rows(int64_t hd) { return hd == 256 ? 128 : 256; }
 Attn8Plan attn8_plan(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t hd, int64_t max_kv, int64_t window,
                      int64_t sinks);
 
@@ -75,6 +75,7 @@ __device__ __forceinline__ f16x2_t half_pair(float a, float b) {
 }
 
 int launch_kv8_decode(const Kv8AttnArgs& a, const Attn8Plan& p, hipStream_t s);
+int launch_kv8_prefill(const Kv8AttnArgs& a, const Attn8Plan& p, hipStream_t s);
 int launch_kv8_join(const Kv8AttnArgs& a, const Attn8Plan& p, hipStream_t s);
 
 }  // namespace qmm

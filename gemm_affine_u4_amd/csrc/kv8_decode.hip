@@ -420,6 +420,9 @@ int join_hd(const Kv8AttnArgs& a, const Attn8Plan& p, hipStream_t s) {
   return hipGetLastError() == hipSuccess ? 0 : 6;
 }
 
+// Calls of up to this many rows per KV head run here, others as prompts.
+constexpr int64_t decode_rows(int64_t hd) { return hd == 256 ? 64 : 128; }
+
 }  // namespace
 
 Attn8Plan attn8_plan(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t hd, int64_t max_kv, int64_t window,
@@ -429,11 +432,20 @@ Attn8Plan attn8_plan(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_
   int64_t seen = max_kv;
   if (window > 0 && window + max_q + sinks + 64 < max_kv) seen = window + max_q + sinks + 64;
   Attn8Plan p;
-  p.rows = 16;
+  p.rows = rows <= decode_rows(hd) ? 16 : attn8_rows(hd);
   const int64_t blocks = B * n_kv * ((rows + p.rows - 1) / p.rows);
+  int64_t ns;
+  if (p.rows != 16) {
+    p.shift = 6, p.keys = 512, p.waves = 4;
+    ns = cus / blocks;
+    const int64_t longs = (seen + p.keys - 1) / p.keys;
+    ns = ns > longs ? longs : ns;
+    p.nsplit = int(ns > 256 ? 256 : ns < 1 ? 1 : ns);
+    return p;
+  }
   p.shift = 5, p.keys = 1024;
   while (p.keys > 128 && blocks * ((seen + p.keys - 1) / p.keys) <= cus / 2) p.keys /= 2;
-  int64_t ns = 8 * cus / blocks < 4 ? 8 * cus / blocks : 4;
+  ns = 8 * cus / blocks < 4 ? 8 * cus / blocks : 4;
   if (ns < cus / blocks) ns = cus / blocks;
   if (seen <= 768 || seen <= 2 * p.keys) ns = 1;
   const int64_t most = (seen + p.keys - 1) / p.keys;
@@ -465,7 +477,7 @@ uint64_t kv8_attn_workspace(int64_t T, int64_t B, int64_t max_q, int64_t n_q, in
 int launch_kv8_attn(const Kv8AttnArgs& a, hipStream_t s) {
   const Attn8Plan p = attn8_plan(a.B, a.max_q, a.n_q, a.c.n_kv, a.c.hd, int64_t(a.max_pages) << a.c.page_shift,
                                  a.window, a.sinks);
-  const int st = launch_kv8_decode(a, p, s);
+  const int st = p.rows == 16 ? launch_kv8_decode(a, p, s) : launch_kv8_prefill(a, p, s);
   return st || p.nsplit == 1 ? st : launch_kv8_join(a, p, s);
 }
 

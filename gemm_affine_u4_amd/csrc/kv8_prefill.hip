@@ -1,0 +1,452 @@
+// Attention of prompts over the paged 8-bit cache (qmm_kv8_attn's prompt form).
+//
+// Mathematics.  Codes enter both products exactly, as fp16 numbers in LDS, queries too (bf16 values
+// times a power of two).  With a block's scales s_k and s_v a key's weight times its value scale is
+//   2^(s_k (q . c) + log2 s_v - m),
+// one multiply-add and one exponential, m being the running maximum of that exponent: so the weights
+// that are rounded to fp16 (2^-11) are those of the output's own terms, and off by 2^-36 of the largest
+// one where they are below 2^-25 of it.  The sum of the weights alone is that of each block's, in fp32,
+// over its s_v.
+//
+// Bound: the vector unit (7 issue slots a score, the exponential being 4, and 1.3 a code) beside the
+// matrix cores.
+//
+// Split.  A block of 4 waves takes (query, head) rows of one KV head (the heads of a group share the
+// tile) and walks the keys 64 at a time, in two steps of 32.  A wave keeps 64 rows (32 at 256 dims,
+// where registers end), their queries as operands and their outputs in registers: each LDS operand
+// serves two products, as reading it takes as long as one.  Keys and dims are the rows of the products,
+// so that a lane's scores are its share of the next operand.  A step is ordered by hand: a wave issues
+// in order, so vector work is placed between matrix instructions, beside which it runs.
+#include <hip/hip_runtime.h>
+
+#include "kv8_attn.h"
+#include "qmm_internal.h"
+
+namespace qmm {
+namespace {
+
+constexpr int kKeys = 64;
+constexpr int NW = 4;             // waves of a block
+constexpr float kFloor = -1e30f;  // maximum of a row that has seen no key
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 4.f;     // a row's reference maximum may lag by 2^4,
+constexpr float kShift = 11.f;    // weights are 2^11 of it: below 2^15, within fp16's range
+constexpr float kTiny = 0x1p-100f;  // scales of blocks of zeros, whose values are 0 at any scale
+
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+// LDS rows, in fp16: 16 bytes more than a key's dims or a tile's keys, so that rows at one
+// chunk meet no bank twice.
+template <int HD>
+constexpr int kRowK = HD + 8;
+constexpr int kRowV = kKeys + 8;
+
+template <int HD>
+__global__ __launch_bounds__(NW * 64, 1) void kv8_prefill_kernel(Kv8AttnArgs g, int group, Attn8Plan plan, int tiles) {
+  constexpr int CT = HD == 256 ? 1 : 2;  // column tiles of 32 rows
+  constexpr int ROWS = NW * 32 * CT, OT = HD / 32, NS = HD / 16, NV = 2 * OT, PER = HD / 64;
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, hh = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int split = blockIdx.x;
+  int b = blockIdx.z;
+  const int kvh = blockIdx.y % g.c.n_kv, rt = tiles - 1 - int(blockIdx.y) / g.c.n_kv;  // longest rows first
+
+  const AttnSeq sq = attn_longest_first(g, b, lane);
+  const int row0 = rt * ROWS, rows = sq.q_len * group - row0;
+  if (rows <= 0) return;
+  const Attn8Tiles pl = attn8_tiles(g, sq, row0, rows < ROWS ? rows : ROWS, group, plan, split);
+  if (split >= pl.count) return;
+
+  __shared__ __attribute__((aligned(16))) _Float16 s_k[2][kKeys * kRowK<HD>], s_v[2][HD * kRowV];
+
+  // the lane's rows, and the keys that they see
+  int c_lo[CT], c_hi[CT], u_lo = 0, u_hi = sq.kv_len;  // u: that all rows of the wave see
+  const int sinks = int(g.sinks < sq.kv_len ? g.sinks : sq.kv_len);
+  f16x8_t qf[CT][NS];
+  float qs[CT];
+  static_for<CT>([&](auto cx) {
+    constexpr int c = decltype(cx)::value;
+    const int r = wave * 32 * CT + 32 * c + n, j = (row0 + r) / group;
+    const bool ok = r < rows;
+    c_lo[c] = 0, c_hi[c] = sq.kv_len;
+    if (ok && g.causal) {
+      const int64_t p = int64_t(sq.first) + j;
+      c_hi[c] = p < 0 ? 0 : int(p) + 1;
+      c_lo[c] = g.window > 0 && p - g.window + 1 > 0 ? int(p - g.window + 1) : 0;
+    }
+    u_lo = max(u_lo, c_lo[c]);
+    u_hi = min(u_hi, c_hi[c]);
+    // q as operands: operand e takes dims 16e + 8 hh .. + 7; fp16 scaled by a power of two so that the
+    // row's largest is in [2^7, 2^8)
+    const int64_t qrow = (int64_t(sq.q0) + j) * g.n_q + kvh * group + (row0 + r) % group;
+    u32x4_t raw[NS];
+    float mx = 0.f;
+#pragma unroll
+    for (int e = 0; e < NS; ++e) {
+      raw[e] = u32x4_t{0, 0, 0, 0};
+      if (ok) raw[e] = *reinterpret_cast<const u32x4_t*>(g.q + qrow * HD + 16 * e + 8 * hh);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(raw[e][i])), fabsf(bf16_hi(raw[e][i]))));
+    }
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    const int ex = mx > 0.f ? int((__float_as_uint(mx) >> 23) & 255) - 127 : 0;
+    const int sh = 7 - ex;
+    qs[c] = fminf(g.scale * kLog2e * ldexpf(1.f, -sh), 1e35f);
+#pragma unroll
+    for (int e = 0; e < NS; ++e)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        qf[c][e][2 * i] = static_cast<_Float16>(ldexpf(bf16_lo(raw[e][i]), sh));
+        qf[c][e][2 * i + 1] = static_cast<_Float16>(ldexpf(bf16_hi(raw[e][i]), sh));
+      }
+  });
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    u_lo = max(u_lo, __shfl_xor(u_lo, o));
+    u_hi = min(u_hi, __shfl_xor(u_hi, o));
+  }
+  u_lo = __builtin_amdgcn_readfirstlane(u_lo);
+  u_hi = __builtin_amdgcn_readfirstlane(u_hi);
+
+  // Pages, 16 tiles (a window) at a time: lane i has the 16 keys i % 4 of tile window + i / 4.
+  const int psh = g.c.page_shift, pmask = (1 << psh) - 1;
+  const int32_t* __restrict__ table = g.table + int64_t(b) * g.max_pages;
+  const int last_key = sq.kv_len > 0 ? sq.kv_len - 1 : 0;
+  auto key_of = [&](int v) { return int64_t(pl.at(v + (lane >> 2))) * kKeys + 16 * (lane & 3); };
+  auto page_of = [&](int v) {
+    const int64_t k = key_of(v);
+    return table[(k < last_key ? k : last_key) >> psh];
+  };
+  const uint32_t n_pages = uint32_t(g.c.n_pages);
+
+  // the window of the tiles whose codes are loaded
+  int lw = pl.begin, l_pages = 0, l_next = 0;
+  auto place = [&](int v, int t16) {  // the row of the first of 16 keys of tile v in the cache
+    const int key = pl.at(v) * kKeys + 16 * t16;
+    return ((int64_t(__builtin_amdgcn_readlane(l_pages, 4 * (v - lw) + t16)) * g.c.n_kv + kvh) << psh) + (key & pmask);
+  };
+  // the window of the tiles that are computed: the scales of lane i's 16 keys, the logarithm and the
+  // reciprocal of the values' one; whether any of the keys is there
+  int sw = pl.begin, s_page = 0;
+  float s_ks = 0.f, s_lv = 0.f, s_iv = 0.f, n_ks = 0.f, n_vs = 0.f;
+  uint64_t there = 0;
+  auto fetch_scales = [&](int v, int page) {  // of the window from v on
+    const int64_t k = key_of(v);
+    const bool ok = uint32_t(page) < n_pages && k < sq.kv_len;
+    n_ks = 0.f, n_vs = 0.f;
+    if (ok) {
+      const int64_t at = (((int64_t(page) * g.c.n_kv + kvh) << psh) + (int(k) & pmask)) >> 4;
+      n_ks = g.c.k_scale[at];
+      n_vs = g.c.v_scale[at];
+    }
+    return __ballot(ok);
+  };
+  uint64_t n_there = 0;
+  auto take_scales = [&]() {
+    const float vs = fmaxf(n_vs, kTiny);
+    s_ks = n_ks;
+    s_lv = __builtin_amdgcn_logf(vs);
+    s_iv = 1.f / vs;
+    there = n_there;
+  };
+
+  // a lane's share of a tile's codes: 16 dims of a key, two dims of 8 keys
+  constexpr int KL = HD / 16, UK = 64 / KL;  // lanes of a key, keys of a wave's load
+  const int k_key = lane / KL, k_dim = 16 * (lane % KL);
+  u32x4_t ck[2][PER], cv[2][PER];  // of the next two tiles
+  auto load_k = [&](int set, int i, int v) {
+    const int key = UK * (wave + NW * i);  // of the tile
+    ck[set][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(
+        g.c.k_codes + (place(v, key >> 4) + (key & 15)) * HD + (k_key * HD + k_dim)));
+  };
+  auto load_v = [&](int set, int i, int v) {
+    const int unit = wave + NW * i;  // of 1 KB: 128 / HD octets of keys
+    cv[set][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(
+        g.c.v_codes + place(v, unit * 64 / HD) * HD + unit * 1024 % (16 * HD) + 16 * lane));
+  };
+  // Codes into LDS, four at a time: word a of the lane's share (of all loads).
+  constexpr int WORDS = 4 * PER;
+  uint32_t held[4];
+  auto unpack_k = [&](int set, auto ac, int buf) {
+    constexpr int i = decltype(ac)::value / 4, w = decltype(ac)::value % 4;
+    code_pairs(ck[set][i][w], held[2 * (w & 1)], held[2 * (w & 1) + 1]);
+    if constexpr (w & 1)
+      *reinterpret_cast<u32x4_t*>(&s_k[buf][(UK * (wave + NW * i) + k_key) * kRowK<HD> + k_dim + 8 * (w >> 1)]) =
+          u32x4_t{held[0], held[1], held[2], held[3]};
+  };
+  auto unpack_v = [&](int set, auto ac, int buf) {
+    constexpr int i = decltype(ac)::value / 4, w = decltype(ac)::value % 4;
+    code_pairs(cv[set][i][w], held[2 * (w & 1)], held[2 * (w & 1) + 1]);
+    if constexpr (w & 1) {
+      const int at = (wave + NW * i) * 64 + lane;  // of the tile's 16-byte units, HD / 2 an octet
+      const int octet = at / (HD / 2), dim = 2 * (at % (HD / 2)) + (w >> 1);
+      *reinterpret_cast<u32x4_t*>(&s_v[buf][dim * kRowV + 8 * octet]) = u32x4_t{held[0], held[1], held[2], held[3]};
+    }
+  };
+
+  f32x16_t acc[CT][OT], sa[CT], sb[CT];  // scores of this step and the next, in turn
+  float m[CT], l[CT];
+  float kq[CT][2], ad[CT][2], iv[2];  // of the step's two blocks of 16 keys: a score's factor and what is added
+  static_for<CT>([&](auto cx) {
+    constexpr int c = decltype(cx)::value;
+    m[c] = kFloor, l[c] = 0.f;
+#pragma unroll
+    for (int i = 0; i < OT; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[c][i][e] = 0.f;
+  });
+  // rows 8a + 4h + e of a product's 32 are keys 16 (a / 2) + 8h + 4 (a % 2) + e, so that a lane's
+  // eight scores of 16 keys are neighbours
+  const int krow = 16 * (n >> 4) + 8 * ((n >> 2) & 1) + 4 * ((n >> 3) & 1) + (n & 3);
+  const int k_src = krow * kRowK<HD> + 8 * hh, v_src = n * kRowV + 8 * hh;
+
+  // The scores of a step, 32 keys of tile v from tile key 32 * half on, before their exponentials: factors and
+  // what is added; hidden keys leave; the reference maximum moves where the scores ran away from it.
+  // gm: the largest scores of the two blocks if none is hidden.
+  auto settle = [&](f32x16_t (&x)[CT], const float (&gm)[CT][2], int v, int half) __attribute__((always_inline)) {
+    const int i0 = 4 * (v - sw) + 2 * half;
+    const float ks0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s_ks), i0));
+    const float ks1 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s_ks), i0 + 1));
+    const float lv0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s_lv), i0));
+    const float lv1 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s_lv), i0 + 1));
+    iv[0] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s_iv), i0));
+    iv[1] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s_iv), i0 + 1));
+    const uint32_t blocks = uint32_t(there >> i0) & 3;
+    const int tb = pl.at(v) * kKeys + 32 * half;
+    const bool masked = tb + 32 > u_hi || (tb < u_lo && tb + 32 > sinks) || blocks != 3;
+    float mx[CT];
+    bool run = false;
+    static_for<CT>([&](auto cx) {
+      constexpr int c = decltype(cx)::value;
+      kq[c][0] = ks0 * qs[c], kq[c][1] = ks1 * qs[c];
+      ad[c][0] = lv0, ad[c][1] = lv1;
+      mx[c] = fmaxf(fmaf(gm[c][0], kq[c][0], lv0), fmaf(gm[c][1], kq[c][1], lv1));
+    });
+    if (masked) {
+      static_for<CT>([&](auto cx) {
+        constexpr int c = decltype(cx)::value;
+        mx[c] = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int k = tb + 16 * (e >> 3) + 8 * hh + (e & 7);
+          const bool see = ((blocks >> (e >> 3)) & 1) && (k >= c_lo[c] || k < sinks) && k < c_hi[c];
+          x[c][e] = see ? fmaf(x[c][e], kq[c][e >> 3], ad[c][e >> 3]) : -INFINITY;
+          mx[c] = fmaxf(mx[c], x[c][e]);
+        }
+        kq[c][0] = kq[c][1] = 1.f;
+        ad[c][0] = ad[c][1] = 0.f;
+      });
+    }
+    static_for<CT>([&](auto cx) {
+      constexpr int c = decltype(cx)::value;
+      run |= mx[c] > m[c] + kSlack;
+    });
+    if (__any(run)) {
+      static_for<CT>([&](auto cx) {
+        constexpr int c = decltype(cx)::value;
+        const float top = fmaxf(m[c], fmaxf(mx[c], __shfl_xor(mx[c], 32)));
+        const float fac = exp2_hw(m[c] - top);
+        m[c] = top;
+        l[c] *= fac;
+#pragma unroll
+        for (int i = 0; i < OT; ++i) acc[c][i] *= fac;
+      });
+    }
+    static_for<CT>([&](auto cx) {
+      constexpr int c = decltype(cx)::value;
+      ad[c][0] -= m[c] - kShift, ad[c][1] -= m[c] - kShift;
+    });
+  };
+
+  f16x8_t pv[CT][2];
+  float ps[CT][2];
+  auto weigh = [&](const f32x16_t (&sc)[CT], auto cc, auto wc) __attribute__((always_inline)) {  // weights w, w + 1 of a lane's 16
+    constexpr int c = decltype(cc)::value, w = decltype(wc)::value;
+    const float a = exp2_hw(fmaf(sc[c][w], kq[c][w >> 3], ad[c][w >> 3]));
+    const float d = exp2_hw(fmaf(sc[c][w + 1], kq[c][w >> 3], ad[c][w >> 3]));
+    const f16x2_t h = half_pair(a, d);
+    pv[c][w >> 3][w & 7] = h[0], pv[c][w >> 3][(w & 7) + 1] = h[1];
+    ps[c][w >> 3] = (w & 7) == 0 ? a + d : ps[c][w >> 3] + (a + d);
+  };
+  // One step of 32 keys (half of tile v, in buffer buf): the next step's scores (from kbuf, its half ka) beside the
+  // first rows' weights, then the values beside the others' weights and the next tile's unpacking.
+  auto step = [&](auto half, auto set, const f32x16_t (&sc)[CT], f32x16_t (&next)[CT], int kbuf, int ka, int buf, float (&gm)[CT][2], int v) __attribute__((always_inline)) {
+    constexpr int h = decltype(half)::value, st = decltype(set)::value;
+    const int dst = buf ^ 1;
+    const _Float16* kb = &s_k[kbuf][k_src + 32 * ka * kRowK<HD>];
+    const _Float16* vb = &s_v[buf][v_src + 32 * h];
+    constexpr int LEAD = 4;
+    f16x8_t kf[NS], vf[NV];
+    auto read_k = [&](auto ec) {
+      constexpr int e = decltype(ec)::value;
+      if constexpr (e < NS) kf[e] = *reinterpret_cast<const f16x8_t*>(kb + 16 * e);
+    };
+    auto read_v = [&](auto qc) {
+      constexpr int q = decltype(qc)::value;
+      if constexpr (q >= 0 && q < NV) vf[q] = *reinterpret_cast<const f16x8_t*>(vb + 32 * (q % OT) * kRowV + 16 * (q / OT));
+    };
+    static_for<LEAD>([&](auto ec) { read_k(ec); });
+    f32x16_t zero;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) zero[e] = 0.f;
+    static_for<NS>([&](auto ec) {
+      constexpr int e = decltype(ec)::value;
+      read_k(Int<e + LEAD>{});
+      read_v(Int<e + LEAD - NS>{});
+      static_for<CT>([&](auto cx) {
+        constexpr int c = decltype(cx)::value;
+        next[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[e], qf[c][e], e == 0 ? zero : next[c], 0, 0, 0);
+      });
+      static_for<8>([&](auto wc) {  // the first rows' weights: elements 16 e / NS on
+        constexpr int w = 2 * decltype(wc)::value;
+        if constexpr (w * NS >= 16 * e && w * NS < 16 * (e + 1)) weigh(sc, Int<0>{}, Int<w>{});
+      });
+      // two tiles ahead, into the set that the step before emptied
+      if constexpr (e < PER && h == 0) load_v(1 - st, e, v + 2);
+      if constexpr (e < PER && h == 1) load_k(st, e, v + 3);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    constexpr int P = (WORDS + NV - 1) / NV;
+    static_for<CT>([&](auto cc) {
+      constexpr int c = decltype(cc)::value;
+      static_for<NV>([&](auto qc) {
+        constexpr int q = decltype(qc)::value;
+        if constexpr (c == 0) read_v(Int<q + LEAD>{});
+        acc[c][q % OT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[q], pv[c][q / OT], acc[c][q % OT], 0, 0, 0);
+        if constexpr (CT > 1 && c + 1 < CT) {
+          static_for<8>([&](auto wc) {
+            constexpr int w = 2 * decltype(wc)::value;
+            if constexpr (w * NV >= 16 * q && w * NV < 16 * (q + 1)) weigh(sc, Int<CT - 1>{}, Int<w>{});
+          });
+        }
+        if constexpr (c == CT - 1) {
+          static_for<P>([&](auto ic) {
+            constexpr int a = q * P + decltype(ic)::value;
+            if constexpr (a < WORDS) {
+              if constexpr (h == 0) unpack_k(st, Int<a>{}, dst);
+              else unpack_v(st, Int<a>{}, dst);
+            }
+          });
+          if constexpr (q >= NV / 2) {  // the next scores' maxima, when they are through
+            static_for<CT * 16>([&](auto xc) {
+              constexpr int x = decltype(xc)::value, k = x / 16, e = x % 16;
+              if constexpr (x * (NV / 2) >= CT * 16 * (q - NV / 2) && x * (NV / 2) < CT * 16 * (q + 1 - NV / 2))
+                gm[k][e >> 3] = (e & 7) == 0 ? next[k][e] : fmaxf(gm[k][e >> 3], next[k][e]);
+            });
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
+    static_for<CT>([&](auto cx) {
+      constexpr int c = decltype(cx)::value;
+      l[c] = fmaf(ps[c][0], iv[0], fmaf(ps[c][1], iv[1], l[c]));
+    });
+  };
+
+  if (pl.begin < pl.end) {
+    auto checked = [&](int page) { return uint32_t(page) < n_pages ? page : 0; };
+    s_page = page_of(pl.begin);
+    l_pages = checked(s_page);
+    l_next = page_of(pl.begin + 16);
+    n_there = fetch_scales(pl.begin, s_page);
+    static_for<PER>([&](auto i) {
+      load_k(0, i, pl.begin);
+      load_v(0, i, pl.begin);
+    });
+    static_for<PER>([&](auto i) {
+      load_k(1, i, pl.begin + 1);
+      load_v(1, i, pl.begin + 1);
+    });
+    take_scales();
+    static_for<WORDS>([&](auto a) { unpack_k(0, a, 0); });
+    static_for<WORDS>([&](auto a) { unpack_v(0, a, 0); });
+    static_for<PER>([&](auto i) { load_k(0, i, pl.begin + 2); });
+    __syncthreads();
+    float gm[CT][2];
+    static_for<CT>([&](auto cx) {
+      constexpr int c = decltype(cx)::value;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sa[c][e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < NS; ++e)
+        sa[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const f16x8_t*>(&s_k[0][k_src + 16 * e]),
+                                                       qf[c][e], sa[c], 0, 0, 0);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) gm[c][e >> 3] = (e & 7) == 0 ? sa[c][e] : fmaxf(gm[c][e >> 3], sa[c][e]);
+    });
+    settle(sa, gm, pl.begin, 0);
+    // a tile: `set` holds the next tile's codes, the other one the keys of the one after (its values are loaded in the
+    // first step)
+    auto tile = [&](auto set, int v) __attribute__((always_inline)) {
+      constexpr int buf = 1 - decltype(set)::value;
+      step(Int<0>{}, set, sa, sb, buf, 1, buf, gm, v);
+      settle(sb, gm, v, 1);
+      __syncthreads();
+      if (v + 3 - lw >= 16) {  // the window of the loads moves on
+        lw += 16;
+        l_pages = checked(l_next);
+        l_next = page_of(lw + 16);
+      }
+      // the next window's scales: its pages, then they, some tiles before it begins
+      if (v - sw == 4) s_page = page_of(sw + 16);
+      if (v - sw == 9) n_there = fetch_scales(sw + 16, s_page);
+      step(Int<1>{}, set, sb, sa, buf ^ 1, 0, buf, gm, v);
+      if (v + 1 - sw >= 16) {
+        sw += 16;
+        take_scales();
+      }
+      settle(sa, gm, v + 1, 0);
+      __syncthreads();
+    };
+    for (int v = pl.begin;;) {
+      tile(Int<1>{}, v);
+      if (++v >= pl.end) break;
+      tile(Int<0>{}, v);
+      if (++v >= pl.end) break;
+    }
+  }
+
+  const int64_t R0 = g.T * g.n_q;
+  float* po = static_cast<float*>(g.ws);
+  static_for<CT>([&](auto cx) {
+    constexpr int c = decltype(cx)::value;
+    const float sum = l[c] + __shfl_xor(l[c], 32);
+    const int r = wave * 32 * CT + 32 * c + n;
+    if (r >= rows) return;
+    const int64_t qrow = (int64_t(sq.q0) + (row0 + r) / group) * g.n_q + kvh * group + (row0 + r) % group;
+#pragma unroll
+    for (int i = 0; i < OT; ++i)
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const float4 o = {acc[c][i][4 * a], acc[c][i][4 * a + 1], acc[c][i][4 * a + 2], acc[c][i][4 * a + 3]};
+        const int d = 32 * i + 8 * a + 4 * hh;
+        if (pl.count == 1) attn_store4(g, qrow * HD + d, o, sum);
+        else *reinterpret_cast<float4*>(po + (split * R0 + qrow) * HD + d) = o;
+      }
+    if (pl.count > 1 && hh == 0) {
+      float* pm = po + plan.nsplit * R0 * HD;
+      pm[(split * R0 + qrow) * 2] = m[c];
+      pm[(split * R0 + qrow) * 2 + 1] = sum;
+      if (split == 0) pm[plan.nsplit * R0 * 2 + qrow] = 1.f;  // maxima are in powers of two
+    }
+  });
+}
+
+template <int HD>
+int launch(const Kv8AttnArgs& a, const Attn8Plan& p, hipStream_t s) {
+  const int group = a.n_q / a.c.n_kv, tiles = int((int64_t(a.max_q) * group + p.rows - 1) / p.rows);
+  kv8_prefill_kernel<HD>
+      <<<dim3(uint32_t(p.nsplit), uint32_t(a.c.n_kv * tiles), uint32_t(a.B)), NW * 64, 0, s>>>(a, group, p, tiles);
+  return hipGetLastError() == hipSuccess ? 0 : 6;
+}
+
+}  // namespace
+
+int launch_kv8_prefill(const Kv8AttnArgs& a, const Attn8Plan& p, hipStream_t s) {
+  if (a.c.hd == 256) return launch<256>(a, p, s);
+  return a.c.hd == 128 ? launch<128>(a, p, s) : launch<64>(a, p, s);
+}
+
+}  // namespace qmm

@@ -96,9 +96,9 @@ int qmm_kv8_append(const qmm_kv8_cache* cache, const void* k, const void* v, int
  *   below 2^126.
  *   gate (nullable) [T][n_q_heads][head_dim] bf16: out is multiplied by 1 / (1 + exp(-gate)).
  * Scores, sums, maxima and the softmax are fp32, from exact codes and queries (of a query row,
- * values below 2^-24 of its largest lose digits); the probabilities times the values' scales are
- * rounded to fp16 (2^-11 of the value, and 2^-24 of the largest scale of its keys where the
- * probability is small).
+ * values below 2^-24 of its largest lose digits).  A key's weight times its values' scale is rounded to
+ * fp16: 2^-11 of it; where it is small, for few queries (up to 128 rows = queries x heads of a group, 64 at
+ * head_dim 256) 2^-39 of the largest scale, for prompts 2^-36 of the row's largest such product.
  * workspace: 256-byte aligned, at least qmm_kv8_attn_workspace_bytes of the same T, B, max_q,
  * heads, max_kv = max_pages * page_size, window and sinks (0 for sizes out of range; always > 0
  * otherwise).

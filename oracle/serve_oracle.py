@@ -91,12 +91,14 @@ class Cache:
         return k, v, vs
 
 
-def attention(q, cache, table, kv_len, q_len, scale, causal=True, window=0, sinks=0, gate=None):
+def attention(q, cache, table, kv_len, q_len, scale, causal=True, window=0, sinks=0, gate=None, few=True):
     """One sequence: q fp64 [n, n_q, hd], table of page ids.  Returns (out fp64, tol fp64).
 
     The tolerance of the GPU's evaluation, per element: the output's rounding to bf16, 2^-8 |o|; the fp16
-    rounding of p s, 2^-11 of W = sum p |v|, and for weights below fp16's normal range 2^-38 of the largest value
-    scale times 127 a key; and the scores' error d (fp32 sums of hd + 8 terms, M = scale sum |q k|), which changes each
+    rounding of p s, 2^-11 of W = sum p |v|, and where p s is below fp16's normal range its steps of 2^-24, half of one
+    a key times codes up to 127: for few queries p s is held times 8 with the largest scale s at 2^11 or more, so
+    that is 2^-25 / 2^14 = 2^-39 of the largest scale; for prompts with the row's largest p s at 2^11 or more, 2^-36 of
+    that; and the scores' error d (fp32 sums of hd + 8 terms, M = scale sum |q k|), which changes each
     p by at most a factor e^(2 d) once normalised: (e^(2 d) - 1) W.  The hardware's exp2 (2^-22) and the
     normalising sum (2^-20) sit in the 2^-18 added to the relative part."""
     n_q, hd = q.shape[1], q.shape[2]
@@ -125,7 +127,8 @@ def attention(q, cache, table, kv_len, q_len, scale, causal=True, window=0, sink
             p /= p.sum(1, keepdims=True)
             o, w = p @ v, p @ np.abs(v)
             d = np.where(see[some], scale * (np.abs(x) @ np.abs(k).T), 0).max(1, keepdims=True) * (hd + 8) * 2.0 ** -24
-            e = w * (2.0 ** -11 + 2.0 ** -18 + np.expm1(2 * d)) + len(t) * 127 * 2.0 ** -38 * vs.max()
+            low = 2.0 ** -39 * vs.max() if few else 2.0 ** -36 * (p * vs).max(1, keepdims=True)
+            e = w * (2.0 ** -11 + 2.0 ** -18 + np.expm1(2 * d)) + len(t) * 127 * low
             if gate is not None:
                 sig = 1 / (1 + np.exp(-gate[some, a]))
                 o, e = o * sig, e * sig + np.abs(o * sig) * 2.0 ** -20
