@@ -33,6 +33,19 @@ constexpr float kSlack = 4.f;     // a row's reference maximum may lag by 2^4,
 constexpr float kShift = 11.f;    // weights are 2^11 of it: below 2^15, within fp16's range
 constexpr float kTiny = 0x1p-100f;  // scales of blocks of zeros, whose values are 0 at any scale
 
+// Scores: keys (LDS operands) x queries.  The compiler would keep every product's result in accumulation
+// registers, and queries in turn spilled: scores are wanted by the vector unit, outputs (and queries, which
+// the matrix cores read there as well) are not.  So this product is written out, with its result in
+// vector registers; what reads it is kept away by score_settle or by the products in between.
+__device__ __forceinline__ void score_first(f32x16_t& d, f16x8_t k, f16x8_t q) {
+  asm volatile("v_mfma_f32_32x32x16_f16 %0, %1, %2, 0" : "=&v"(d) : "v"(k), "a"(q));
+}
+__device__ __forceinline__ void score_more(f32x16_t& d, f16x8_t k, f16x8_t q) {
+  asm volatile("v_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+v"(d) : "v"(k), "a"(q));
+}
+// Wait states between a score product and the vector unit's read (12 are needed).
+__device__ __forceinline__ void score_settle(f32x16_t& d) { asm volatile("s_nop 15" : "+v"(d)); }
+
 template <int N>
 using Int = std::integral_constant<int, N>;
 
@@ -100,6 +113,8 @@ __global__ __launch_bounds__(NW * 64, 1) void kv8_prefill_kernel(Kv8AttnArgs g, 
         qf[c][e][2 * i] = static_cast<_Float16>(ldexpf(bf16_lo(raw[e][i]), sh));
         qf[c][e][2 * i + 1] = static_cast<_Float16>(ldexpf(bf16_hi(raw[e][i]), sh));
       }
+#pragma unroll
+    for (int e = 0; e < NS; ++e) asm volatile("" : "+a"(qf[c][e]));
   });
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -287,16 +302,14 @@ __global__ __launch_bounds__(NW * 64, 1) void kv8_prefill_kernel(Kv8AttnArgs g, 
       if constexpr (q >= 0 && q < NV) vf[q] = *reinterpret_cast<const f16x8_t*>(vb + 32 * (q % OT) * kRowV + 16 * (q / OT));
     };
     static_for<LEAD>([&](auto ec) { read_k(ec); });
-    f32x16_t zero;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) zero[e] = 0.f;
     static_for<NS>([&](auto ec) {
       constexpr int e = decltype(ec)::value;
       read_k(Int<e + LEAD>{});
       read_v(Int<e + LEAD - NS>{});
       static_for<CT>([&](auto cx) {
         constexpr int c = decltype(cx)::value;
-        next[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[e], qf[c][e], e == 0 ? zero : next[c], 0, 0, 0);
+        if constexpr (e == 0) score_first(next[c], kf[e], qf[c][e]);
+        else score_more(next[c], kf[e], qf[c][e]);
       });
       static_for<8>([&](auto wc) {  // the first rows' weights: elements 16 e / NS on
         constexpr int w = 2 * decltype(wc)::value;
@@ -367,12 +380,13 @@ __global__ __launch_bounds__(NW * 64, 1) void kv8_prefill_kernel(Kv8AttnArgs g, 
     float gm[CT][2];
     static_for<CT>([&](auto cx) {
       constexpr int c = decltype(cx)::value;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) sa[c][e] = 0.f;
-#pragma unroll
-      for (int e = 0; e < NS; ++e)
-        sa[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*reinterpret_cast<const f16x8_t*>(&s_k[0][k_src + 16 * e]),
-                                                       qf[c][e], sa[c], 0, 0, 0);
+      static_for<NS>([&](auto ec) {
+        constexpr int e = decltype(ec)::value;
+        const f16x8_t k = *reinterpret_cast<const f16x8_t*>(&s_k[0][k_src + 16 * e]);
+        if constexpr (e == 0) score_first(sa[c], k, qf[c][e]);
+        else score_more(sa[c], k, qf[c][e]);
+      });
+      score_settle(sa[c]);
 #pragma unroll
       for (int e = 0; e < 16; ++e) gm[c][e >> 3] = (e & 7) == 0 ? sa[c][e] : fmaxf(gm[c][e >> 3], sa[c][e]);
     });
