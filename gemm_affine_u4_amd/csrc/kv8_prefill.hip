@@ -135,11 +135,18 @@ __global__ __launch_bounds__(NW * 64, 1) void kv8_prefill_kernel(Kv8AttnArgs g, 
   };
   const uint32_t n_pages = uint32_t(g.c.n_pages);
 
-  // the window of the tiles whose codes are loaded
-  int lw = pl.begin, l_pages = 0, l_next = 0;
-  auto place = [&](int v, int t16) {  // the row of the first of 16 keys of tile v in the cache
-    const int key = pl.at(v) * kKeys + 16 * t16;
-    return ((int64_t(__builtin_amdgcn_readlane(l_pages, 4 * (v - lw) + t16)) * g.c.n_kv + kvh) << psh) + (key & pmask);
+  // the window of the tiles whose codes are loaded: the cache's row of a lane's 16 keys (of page 0 where there is
+  // no page)
+  int lw = pl.begin, l_next = 0;
+  int64_t l_row = 0;
+  auto rows_of = [&](int v, int page) {
+    return ((int64_t(uint32_t(page) < n_pages ? page : 0) * g.c.n_kv + kvh) << psh) + (int(key_of(v)) & pmask);
+  };
+  auto place = [&](int v, int t16) {  // that of 16 keys of tile v
+    const int i = 4 * (v - lw) + t16;
+    const uint32_t lo = __builtin_amdgcn_readlane(uint32_t(l_row), i);
+    const uint32_t hi = __builtin_amdgcn_readlane(uint32_t(l_row >> 32), i);
+    return int64_t(uint64_t(hi) << 32 | lo);
   };
   // the window of the tiles that are computed: the scales of lane i's 16 keys, the logarithm and the
   // reciprocal of the values' one; whether any of the keys is there
@@ -169,16 +176,17 @@ __global__ __launch_bounds__(NW * 64, 1) void kv8_prefill_kernel(Kv8AttnArgs g, 
   // a lane's share of a tile's codes: 16 dims of a key, two dims of 8 keys
   constexpr int KL = HD / 16, UK = 64 / KL;  // lanes of a key, keys of a wave's load
   const int k_key = lane / KL, k_dim = 16 * (lane % KL);
+  const uint32_t k_off = uint32_t(k_key * HD + k_dim);
   u32x4_t ck[2][PER], cv[2][PER];  // of the next two tiles
   auto load_k = [&](int set, int i, int v) {
     const int key = UK * (wave + NW * i);  // of the tile
-    ck[set][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(
-        g.c.k_codes + (place(v, key >> 4) + (key & 15)) * HD + (k_key * HD + k_dim)));
+    const int8_t* from = g.c.k_codes + (place(v, key >> 4) + (key & 15)) * HD;
+    ck[set][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(from + k_off));
   };
   auto load_v = [&](int set, int i, int v) {
     const int unit = wave + NW * i;  // of 1 KB: 128 / HD octets of keys
-    cv[set][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(
-        g.c.v_codes + place(v, unit * 64 / HD) * HD + unit * 1024 % (16 * HD) + 16 * lane));
+    const int8_t* from = g.c.v_codes + place(v, unit * 64 / HD) * HD + unit * 1024 % (16 * HD);
+    cv[set][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(from + uint32_t(16 * lane)));
   };
   // Codes into LDS, four at a time: word a of the lane's share (of all loads).
   constexpr int WORDS = 4 * PER;
@@ -202,7 +210,7 @@ __global__ __launch_bounds__(NW * 64, 1) void kv8_prefill_kernel(Kv8AttnArgs g, 
 
   f32x16_t acc[CT][OT], sa[CT], sb[CT];  // scores of this step and the next, in turn
   float m[CT], l[CT];
-  float kq[CT][2], ad[CT][2], iv[2];  // of the step's two blocks of 16 keys: a score's factor and what is added
+  float kq[CT][2], ad[CT][2];  // of a step's two blocks of 16 keys: a score's factor and what is added
   static_for<CT>([&](auto cx) {
     constexpr int c = decltype(cx)::value;
     m[c] = kFloor, l[c] = 0.f;
@@ -216,36 +224,46 @@ __global__ __launch_bounds__(NW * 64, 1) void kv8_prefill_kernel(Kv8AttnArgs g, 
   const int krow = 16 * (n >> 4) + 8 * ((n >> 2) & 1) + 4 * ((n >> 3) & 1) + (n & 3);
   const int k_src = krow * kRowK<HD> + 8 * hh, v_src = n * kRowV + 8 * hh;
 
-  // The scores of a step, 32 keys of tile v from tile key 32 * half on, before their exponentials: factors and
-  // what is added; hidden keys leave; the reference maximum moves where the scores ran away from it.
-  // gm: the largest scores of the two blocks if none is hidden.
-  auto settle = [&](f32x16_t (&x)[CT], const float (&gm)[CT][2], int v, int half) __attribute__((always_inline)) {
-    const int i0 = 4 * (v - sw) + 2 * half;
-    const float ks0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s_ks), i0));
-    const float ks1 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s_ks), i0 + 1));
-    const float lv0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s_lv), i0));
-    const float lv1 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s_lv), i0 + 1));
-    iv[0] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s_iv), i0));
-    iv[1] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s_iv), i0 + 1));
-    const uint32_t blocks = uint32_t(there >> i0) & 3;
-    const int tb = pl.at(v) * kKeys + 32 * half;
-    const bool masked = tb + 32 > u_hi || (tb < u_lo && tb + 32 > sinks) || blocks != 3;
+  // What a step of 32 keys, half of tile v, needs besides its scores.
+  struct Facts {
+    float ks[2], lv[2], iv[2];  // of its two blocks of 16 keys
+    int key;                    // the first one
+    uint32_t blocks;            // those that are there
+    bool masked;                // some row does not see all of them
+  };
+  auto facts = [&](int v, int half) {
+    Facts f;
+    const int i = 4 * (v - sw) + 2 * half;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      f.ks[k] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s_ks), i + k));
+      f.lv[k] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s_lv), i + k));
+      f.iv[k] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s_iv), i + k));
+    }
+    f.blocks = uint32_t(there >> i) & 3;
+    f.key = pl.at(v) * kKeys + 32 * half;
+    f.masked = f.key + 32 > u_hi || (f.key < u_lo && f.key + 32 > sinks) || f.blocks != 3;
+    return f;
+  };
+  // Scores before their exponentials: factors and what is added; hidden keys leave; the reference
+  // maximum moves where the scores ran away from it.  gm: the largest scores of the two blocks if none is hidden.
+  auto settle = [&](f32x16_t (&x)[CT], const float (&gm)[CT][2], const Facts& f) __attribute__((always_inline)) {
     float mx[CT];
     bool run = false;
     static_for<CT>([&](auto cx) {
       constexpr int c = decltype(cx)::value;
-      kq[c][0] = ks0 * qs[c], kq[c][1] = ks1 * qs[c];
-      ad[c][0] = lv0, ad[c][1] = lv1;
-      mx[c] = fmaxf(fmaf(gm[c][0], kq[c][0], lv0), fmaf(gm[c][1], kq[c][1], lv1));
+      kq[c][0] = f.ks[0] * qs[c], kq[c][1] = f.ks[1] * qs[c];
+      ad[c][0] = f.lv[0], ad[c][1] = f.lv[1];
+      mx[c] = fmaxf(fmaf(gm[c][0], kq[c][0], f.lv[0]), fmaf(gm[c][1], kq[c][1], f.lv[1]));
     });
-    if (masked) {
+    if (f.masked) {
       static_for<CT>([&](auto cx) {
         constexpr int c = decltype(cx)::value;
         mx[c] = -INFINITY;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const int k = tb + 16 * (e >> 3) + 8 * hh + (e & 7);
-          const bool see = ((blocks >> (e >> 3)) & 1) && (k >= c_lo[c] || k < sinks) && k < c_hi[c];
+          const int k = f.key + 16 * (e >> 3) + 8 * hh + (e & 7);
+          const bool see = ((f.blocks >> (e >> 3)) & 1) && (k >= c_lo[c] || k < sinks) && k < c_hi[c];
           x[c][e] = see ? fmaf(x[c][e], kq[c][e >> 3], ad[c][e >> 3]) : -INFINITY;
           mx[c] = fmaxf(mx[c], x[c][e]);
         }
@@ -274,25 +292,45 @@ __global__ __launch_bounds__(NW * 64, 1) void kv8_prefill_kernel(Kv8AttnArgs g, 
     });
   };
 
+  // The first key operands of a step are read before its weights' factors are settled.
+  constexpr int LEAD = 4;
+  f16x8_t kf[NS];
+  auto lead = [&](int kbuf, int ka) {
+    const _Float16* kb = &s_k[kbuf][k_src + 32 * ka * kRowK<HD>];
+    static_for<LEAD>([&](auto ec) {
+      constexpr int e = decltype(ec)::value;
+      kf[e] = *reinterpret_cast<const f16x8_t*>(kb + 16 * e);
+    });
+  };
   f16x8_t pv[CT][2];
   float ps[CT][2];
-  auto weigh = [&](const f32x16_t (&sc)[CT], auto cc, auto wc) __attribute__((always_inline)) {  // weights w, w + 1 of a lane's 16
-    constexpr int c = decltype(cc)::value, w = decltype(wc)::value;
-    const float a = exp2_hw(fmaf(sc[c][w], kq[c][w >> 3], ad[c][w >> 3]));
-    const float d = exp2_hw(fmaf(sc[c][w + 1], kq[c][w >> 3], ad[c][w >> 3]));
-    const f16x2_t h = half_pair(a, d);
-    pv[c][w >> 3][w & 7] = h[0], pv[c][w >> 3][(w & 7) + 1] = h[1];
-    ps[c][w >> 3] = (w & 7) == 0 ? a + d : ps[c][w >> 3] + (a + d);
+  // Weights 2p, 2p + 1 of a lane's 16 of rows c: their exponentials, and, one turn later so that nothing waits for
+  // them, the rest.
+  float e0, e1;
+  auto raise = [&](const f32x16_t (&sc)[CT], auto cc, auto pc) __attribute__((always_inline)) {
+    constexpr int c = decltype(cc)::value, w = 2 * decltype(pc)::value;
+    e0 = exp2_hw(fmaf(sc[c][w], kq[c][w >> 3], ad[c][w >> 3]));
+    e1 = exp2_hw(fmaf(sc[c][w + 1], kq[c][w >> 3], ad[c][w >> 3]));
   };
-  // One step of 32 keys (half of tile v, in buffer buf): the next step's scores (from kbuf, its half ka) beside the
-  // first rows' weights, then the values beside the others' weights and the next tile's unpacking.
-  auto step = [&](auto half, auto set, const f32x16_t (&sc)[CT], f32x16_t (&next)[CT], int kbuf, int ka, int buf, float (&gm)[CT][2], int v) __attribute__((always_inline)) {
+  auto gather = [&](auto cc, auto pc) __attribute__((always_inline)) {
+    constexpr int c = decltype(cc)::value, w = 2 * decltype(pc)::value;
+    const f16x2_t h = half_pair(e0, e1);
+    pv[c][w >> 3][w & 7] = h[0], pv[c][w >> 3][(w & 7) + 1] = h[1];
+    ps[c][w >> 3] = (w & 7) == 0 ? e0 + e1 : ps[c][w >> 3] + (e0 + e1);
+    asm volatile("" : "+v"(ps[c][w >> 3]));  // here, not behind the products
+  };
+  // One step of 32 keys (half of tile v, in buffer buf): the next step's scores (from kbuf, its half ka), then the
+  // values.  Each matrix instruction is a turn, with its share of the vector work behind it: pairs of weights, which
+  // have to be there by the products that take them (so all by the last PV / 2 turns), the next tile's
+  // unpacking, and at the end the next scores' maxima.
+  auto step = [&](auto half, auto set, const f32x16_t (&sc)[CT], f32x16_t (&next)[CT], int kbuf, int ka, int buf,
+                  float (&gm)[CT][2], int v, const Facts& now, Facts& then) __attribute__((always_inline)) {
     constexpr int h = decltype(half)::value, st = decltype(set)::value;
+    constexpr int TURNS = CT * (NS + NV), PAIRS = 8 * CT, DUE = TURNS - NV / 2;
     const int dst = buf ^ 1;
     const _Float16* kb = &s_k[kbuf][k_src + 32 * ka * kRowK<HD>];
     const _Float16* vb = &s_v[buf][v_src + 32 * h];
-    constexpr int LEAD = 4;
-    f16x8_t kf[NS], vf[NV];
+    f16x8_t vf[NV];
     auto read_k = [&](auto ec) {
       constexpr int e = decltype(ec)::value;
       if constexpr (e < NS) kf[e] = *reinterpret_cast<const f16x8_t*>(kb + 16 * e);
@@ -301,67 +339,61 @@ __global__ __launch_bounds__(NW * 64, 1) void kv8_prefill_kernel(Kv8AttnArgs g, 
       constexpr int q = decltype(qc)::value;
       if constexpr (q >= 0 && q < NV) vf[q] = *reinterpret_cast<const f16x8_t*>(vb + 32 * (q % OT) * kRowV + 16 * (q / OT));
     };
-    static_for<LEAD>([&](auto ec) { read_k(ec); });
-    static_for<NS>([&](auto ec) {
-      constexpr int e = decltype(ec)::value;
-      read_k(Int<e + LEAD>{});
-      read_v(Int<e + LEAD - NS>{});
-      static_for<CT>([&](auto cx) {
-        constexpr int c = decltype(cx)::value;
+    static_for<TURNS>([&](auto tc) {
+      constexpr int t = decltype(tc)::value;
+      if constexpr (t < CT * NS) {
+        constexpr int e = t / CT, c = t % CT;
+        if constexpr (c == 0) {
+          read_k(Int<e + LEAD>{});
+          read_v(Int<e + LEAD - NS>{});
+        }
         if constexpr (e == 0) score_first(next[c], kf[e], qf[c][e]);
         else score_more(next[c], kf[e], qf[c][e]);
-      });
-      static_for<8>([&](auto wc) {  // the first rows' weights: elements 16 e / NS on
-        constexpr int w = 2 * decltype(wc)::value;
-        if constexpr (w * NS >= 16 * e && w * NS < 16 * (e + 1)) weigh(sc, Int<0>{}, Int<w>{});
-      });
-      // two tiles ahead, into the set that the step before emptied
-      if constexpr (e < PER && h == 0) load_v(1 - st, e, v + 2);
-      if constexpr (e < PER && h == 1) load_k(st, e, v + 3);
-      __builtin_amdgcn_sched_barrier(0);
-    });
-    constexpr int P = (WORDS + NV - 1) / NV;
-    static_for<CT>([&](auto cc) {
-      constexpr int c = decltype(cc)::value;
-      static_for<NV>([&](auto qc) {
-        constexpr int q = decltype(qc)::value;
+        // two tiles ahead, into the set that the step before emptied
+        if constexpr (e < PER && c == CT - 1 && h == 0) load_v(1 - st, e, v + 2);
+        if constexpr (e < PER && c == CT - 1 && h == 1) load_k(st, e, v + 3);
+      } else {
+        constexpr int c = (t - CT * NS) / NV, q = (t - CT * NS) % NV;
         if constexpr (c == 0) read_v(Int<q + LEAD>{});
         acc[c][q % OT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[q], pv[c][q / OT], acc[c][q % OT], 0, 0, 0);
-        if constexpr (CT > 1 && c + 1 < CT) {
-          static_for<8>([&](auto wc) {
-            constexpr int w = 2 * decltype(wc)::value;
-            if constexpr (w * NV >= 16 * q && w * NV < 16 * (q + 1)) weigh(sc, Int<CT - 1>{}, Int<w>{});
-          });
+      }
+      static_for<PAIRS + 1>([&](auto kc) {  // pair k's turn is k DUE / PAIRS
+        constexpr int k = decltype(kc)::value;
+        if constexpr (k < PAIRS ? k * DUE / PAIRS == t : t == DUE - 1) {
+          if constexpr (k > 0) gather(Int<(k - 1) / 8>{}, Int<(k - 1) % 8>{});
+          if constexpr (k < PAIRS) raise(sc, Int<k / 8>{}, Int<k % 8>{});
         }
-        if constexpr (c == CT - 1) {
-          static_for<P>([&](auto ic) {
-            constexpr int a = q * P + decltype(ic)::value;
-            if constexpr (a < WORDS) {
-              if constexpr (h == 0) unpack_k(st, Int<a>{}, dst);
-              else unpack_v(st, Int<a>{}, dst);
-            }
-          });
-          if constexpr (q >= NV / 2) {  // the next scores' maxima, when they are through
-            static_for<CT * 16>([&](auto xc) {
-              constexpr int x = decltype(xc)::value, k = x / 16, e = x % 16;
-              if constexpr (x * (NV / 2) >= CT * 16 * (q - NV / 2) && x * (NV / 2) < CT * 16 * (q + 1 - NV / 2))
-                gm[k][e >> 3] = (e & 7) == 0 ? next[k][e] : fmaxf(gm[k][e >> 3], next[k][e]);
-            });
-          }
-        }
-        __builtin_amdgcn_sched_barrier(0);
       });
+      static_for<WORDS>([&](auto ac) {
+        constexpr int a = decltype(ac)::value;
+        if constexpr (a * (TURNS - NV) / WORDS == t) {
+          if constexpr (h == 0) unpack_k(st, ac, dst);
+          else unpack_v(st, ac, dst);
+        }
+      });
+      if constexpr (t == CT * NS) then = facts(h ? v + 1 : v, 1 - h);
+      constexpr int M = NV / 2, m0 = TURNS - M;  // the next scores have long been through
+      if constexpr (t >= m0) {
+        static_for<CT * 8>([&](auto xc) {
+          constexpr int x = decltype(xc)::value, k = x / 8, e = 2 * (x % 8);
+          if constexpr (x * M / (CT * 8) == t - m0) {
+            const float top = fmaxf(next[k][e], next[k][e + 1]);
+            gm[k][e >> 3] = (e & 7) == 0 ? top : fmaxf(gm[k][e >> 3], top);
+            asm volatile("" : "+v"(gm[k][e >> 3]));
+          }
+        });
+      }
+      __builtin_amdgcn_sched_barrier(0);
     });
     static_for<CT>([&](auto cx) {
       constexpr int c = decltype(cx)::value;
-      l[c] = fmaf(ps[c][0], iv[0], fmaf(ps[c][1], iv[1], l[c]));
+      l[c] = fmaf(ps[c][0], now.iv[0], fmaf(ps[c][1], now.iv[1], l[c]));
     });
   };
 
   if (pl.begin < pl.end) {
-    auto checked = [&](int page) { return uint32_t(page) < n_pages ? page : 0; };
     s_page = page_of(pl.begin);
-    l_pages = checked(s_page);
+    l_row = rows_of(pl.begin, s_page);
     l_next = page_of(pl.begin + 16);
     n_there = fetch_scales(pl.begin, s_page);
     static_for<PER>([&](auto i) {
@@ -390,29 +422,33 @@ __global__ __launch_bounds__(NW * 64, 1) void kv8_prefill_kernel(Kv8AttnArgs g, 
 #pragma unroll
       for (int e = 0; e < 16; ++e) gm[c][e >> 3] = (e & 7) == 0 ? sa[c][e] : fmaxf(gm[c][e >> 3], sa[c][e]);
     });
-    settle(sa, gm, pl.begin, 0);
+    lead(0, 1);
+    Facts fa = facts(pl.begin, 0), fb;
+    settle(sa, gm, fa);
     // a tile: `set` holds the next tile's codes, the other one the keys of the one after (its values are loaded in the
     // first step)
     auto tile = [&](auto set, int v) __attribute__((always_inline)) {
       constexpr int buf = 1 - decltype(set)::value;
-      step(Int<0>{}, set, sa, sb, buf, 1, buf, gm, v);
-      settle(sb, gm, v, 1);
+      step(Int<0>{}, set, sa, sb, buf, 1, buf, gm, v, fa, fb);
       __syncthreads();
+      lead(buf ^ 1, 0);
+      settle(sb, gm, fb);
       if (v + 3 - lw >= 16) {  // the window of the loads moves on
         lw += 16;
-        l_pages = checked(l_next);
+        l_row = rows_of(lw, l_next);
         l_next = page_of(lw + 16);
       }
       // the next window's scales: its pages, then they, some tiles before it begins
       if (v - sw == 4) s_page = page_of(sw + 16);
       if (v - sw == 9) n_there = fetch_scales(sw + 16, s_page);
-      step(Int<1>{}, set, sb, sa, buf ^ 1, 0, buf, gm, v);
-      if (v + 1 - sw >= 16) {
+      if (v - sw == 15) {
         sw += 16;
         take_scales();
       }
-      settle(sa, gm, v + 1, 0);
+      step(Int<1>{}, set, sb, sa, buf ^ 1, 0, buf, gm, v, fb, fa);
       __syncthreads();
+      lead(buf ^ 1, 1);
+      settle(sa, gm, fa);
     };
     for (int v = pl.begin;;) {
       tile(Int<1>{}, v);
