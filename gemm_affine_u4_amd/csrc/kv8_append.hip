@@ -7,11 +7,11 @@
 // Bound: HBM (the inputs once, q_out, held values, a byte per cached value), and the launch
 // and two round trips to memory for a decode batch.
 // Split: a wave takes one block of 16 keys of one head at a time (an item: a query, key or value
-// head), with all its values in registers between the largest magnitude and the codes.  For queries
-// and keys hd/8 lanes share a token, each with the 4 + 4 dims of four rotation pairs, so that a
-// pair needs one load of each value and of its angle; a wave's items follow each other over the
-// heads, and the angles stay in registers.  For values a lane holds two dims of eight neighbouring
-// keys, which are its 16 bytes of codes.
+// head), with all its values in registers between the largest magnitude and the codes, and the next
+// item's loads under way.  For queries and keys hd/16 lanes share a token, each with the 8 + 8 dims of
+// eight rotation pairs, so that a pair needs one load of each value and of its angle; a wave's items
+// follow each other over the heads, and the angles stay in registers.  For values a lane holds 4 dims
+// (2 of 64) of eight neighbouring keys, which are its 32 bytes of codes.
 #include <hip/hip_runtime.h>
 
 #include "kv4_attn.h"
@@ -25,33 +25,41 @@ namespace {
 constexpr int kBlock = 16;  // keys that share a scale
 constexpr float kLimit = 57344.0f;
 
-template <bool F32>
-__device__ __forceinline__ void load4(const void* p, int64_t at, float* x) {
-  if constexpr (F32) {
-    const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  } else {
-    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
-    x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
+// N neighbouring values of an fp32 or bf16 array, as loaded.
+template <bool F32, int N>
+struct Raw {
+  static constexpr int kWords = F32 ? N : N / 2;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const void* p, int64_t at) {
+    const uint32_t* from = reinterpret_cast<const uint32_t*>(static_cast<const char*>(p) + at * (F32 ? 4 : 2));
+    if constexpr (kWords % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4) {
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(from + i);
+        w[i] = v[0], w[i + 1] = v[1], w[i + 2] = v[2], w[i + 3] = v[3];
+      }
+    } else if constexpr (kWords == 2) {
+      const uint2 v = *reinterpret_cast<const uint2*>(from);
+      w[0] = v.x, w[1] = v.y;
+    } else {
+      w[0] = *from;
+    }
   }
-}
-template <bool F32>
-__device__ __forceinline__ void load2(const void* p, int64_t at, float* x) {
-  if constexpr (F32) {
-    const float2 a = *reinterpret_cast<const float2*>(static_cast<const float*>(p) + at);
-    x[0] = a.x, x[1] = a.y;
-  } else {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + at);
-    x[0] = bf16_lo(w), x[1] = bf16_hi(w);
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (F32) return __uint_as_float(w[i]);
+    else return i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
   }
-}
+};
 template <bool F32>
 __device__ __forceinline__ float load1(const void* p, int64_t at) {
   if constexpr (F32) return static_cast<const float*>(p)[at];
   else return bf16_bits_to_f32(static_cast<const uint16_t*>(p)[at]);
 }
-__device__ __forceinline__ void store4_bf16(uint16_t* p, const float* x) {
-  *reinterpret_cast<uint2*>(p) = uint2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+__device__ __forceinline__ void store8_bf16(uint16_t* p, const float* x) {
+  u32x4_t w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+  *reinterpret_cast<u32x4_t*>(p) = w;
 }
 
 __device__ __forceinline__ float clamped(float x) { return fminf(fmaxf(x, -kLimit), kLimit); }
@@ -84,202 +92,246 @@ __device__ __forceinline__ uint32_t recode(uint32_t byte, float ratio) {
   return byte_of(__builtin_rintf(float(int8_t(byte)) * ratio));
 }
 
-// VEC: rot a multiple of 8, a lane's dims are two runs of 4 that pair up; otherwise 8 neighbours.
+// VEC: rot a multiple of 16, a lane's dims are two runs of 8 that pair up; otherwise 16 neighbours.
 template <int HD, bool F32, bool VEC>
 __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendArgs g, int blocks, int groups, int per_wave) {
-  constexpr int LPT = HD / 8, PPT = 64 / LPT, PASSES = kBlock / PPT;  // lanes of a token, tokens of a pass
+  constexpr int LPT = HD / 16, PPT = 64 / LPT, PASSES = kBlock / PPT;  // lanes of a token, tokens of a pass
   const int lane = threadIdx.x & 63;
-  const int64_t wid = int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t unit = wid / groups;  // (sequence, block)
-  const int b = int(unit / blocks);
+  const uint32_t wid = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t unit = wid / uint32_t(groups);  // (sequence, block)
+  const int b = int(unit / uint32_t(blocks));
   if (b >= g.B) return;
   const AttnSeq sq = attn_seq(g, b);
-  const int64_t k0 = ((int64_t(sq.first) >> 4) + unit % blocks) * kBlock;  // the block's first key (it may lie below 0)
+  const int64_t k0 = ((int64_t(sq.first) >> 4) + unit % uint32_t(blocks)) * kBlock;  // the block's first key (it may lie below 0)
   const int64_t end = int64_t(sq.first) + sq.q_len;
   const int lo = int(sq.first > k0 ? sq.first - k0 : 0), hi = int(end < k0 + kBlock ? end - k0 : kBlock);
   if (lo >= hi) return;
   const int64_t row0 = sq.q0 + (k0 - sq.first);  // token row of place 0 of the block
-  const int items = g.n_q + 2 * g.c.n_kv, u0 = int(wid % groups) * per_wave;
-  const int u1 = u0 + per_wave < items ? u0 + per_wave : items;
+  const int n_k = g.n_q + g.c.n_kv, items = n_k + g.c.n_kv, u0 = int(wid % uint32_t(groups)) * per_wave;
+  int u1 = u0 + per_wave < items ? u0 + per_wave : items;
 
   // keys below 0 do not occur in a block that starts at 0 or later
   int page = -1;
   if (k0 >= 0) page = g.table[int64_t(b) * g.max_pages + (k0 >> g.c.page_shift)];
   const bool kept = uint32_t(page) < uint32_t(g.c.n_pages);
   const int place0 = int(k0 & ((1 << g.c.page_shift) - 1));
+  if (!kept) u1 = u1 < g.n_q ? u1 : g.n_q;
+  auto slot_of = [&](int head) { return ((int64_t(page) * g.c.n_kv + head) << g.c.page_shift) + place0; };
 
+  // ---- queries and keys
   const int li = lane % LPT, sub = lane / LPT;
-  const int half = g.rot >> 1, pairs = g.rot >> 3;
+  const int half = g.rot >> 1, pairs = g.rot >> 4;
   const bool paired = VEC && li < pairs;
-  const int da = !VEC ? 8 * li : paired ? 4 * li : g.rot + 8 * (li - pairs);
-  const int db = paired ? half + 4 * li : da + 4;
-
-  // angles of the lane's pairs, for each pass's token (keys and queries)
-  float c[PASSES][VEC ? 4 : 1], s[PASSES][VEC ? 4 : 1];
-  int64_t angle[PASSES];
-  if (u0 < g.n_q + g.c.n_kv && g.rot) {
+  const int da = !VEC ? 16 * li : paired ? 8 * li : g.rot + 16 * (li - pairs);
+  const int db = paired ? half + 8 * li : da + 8;
+  auto live = [&](int p) { return p * PPT + sub >= lo && p * PPT + sub < hi; };
+  using Run = Raw<F32, 8>;
+  const int u_k = u1 < n_k ? u1 : n_k;
+  if (u0 < u_k) {
+    auto fetch = [&](int u, Run (&a)[PASSES], Run (&o)[PASSES]) {
+      const void* src = u < g.n_q ? g.q : g.k;
+      const int heads = u < g.n_q ? g.n_q : g.c.n_kv, head = u < g.n_q ? u : u - g.n_q;
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p)
+        if (live(p)) {
+          const int64_t at = ((row0 + p * PPT + sub) * heads + head) * HD;
+          a[p].load(src, at + da);
+          o[p].load(src, at + db);
+        }
+    };
+    Run xa[PASSES], xb[PASSES];
+    fetch(u0, xa, xb);
+    // angles of the lane's pairs, for each pass's token
+    Raw<true, 8> c[PASSES], s[PASSES];
+    int64_t angle[PASSES];
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
-      const int i = p * PPT + sub;
       angle[p] = 0;
-      if (i < lo || i >= hi) continue;
+      if (!g.rot || !live(p)) continue;
+      const int i = p * PPT + sub;
       int64_t pos = g.positions ? g.positions[row0 + i] : k0 + i;
       pos = pos < 0 ? 0 : pos >= g.max_pos ? g.max_pos - 1 : pos;
       angle[p] = pos * g.rot;
-      if constexpr (VEC) {
-        if (paired) {
+      if (paired) {
+        const float* cs = g.cos_sin + angle[p] + 8 * li;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            c[p][e] = g.cos_sin[angle[p] + 4 * li + e];
-            s[p][e] = g.cos_sin[angle[p] + half + 4 * li + e];
+        for (int e = 0; e < 8; ++e) c[p].w[e] = __float_as_uint(cs[e]), s[p].w[e] = __float_as_uint(cs[half + e]);
+      }
+    }
+    for (int u = u0; u < u_k; ++u) {
+      Run na[PASSES], nb[PASSES];
+      if (u + 1 < u_k) fetch(u + 1, na, nb);
+      const bool is_q = u < g.n_q;
+      const int head = is_q ? u : u - g.n_q, heads = is_q ? g.n_q : g.c.n_kv;
+      float x[PASSES][16];
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+#pragma clang fp contract(off)
+        if (!live(p)) continue;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[p][e] = xa[p].at(e), x[p][8 + e] = xb[p].at(e);
+        if constexpr (VEC) {
+          if (paired) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float a = x[p][e], o = x[p][8 + e], cc = c[p].at(e), ss = s[p].at(e);
+              const float ac = a * cc, os = o * ss, oc = o * cc, as = a * ss;
+              x[p][e] = ac - os;
+              x[p][8 + e] = oc + as;
+            }
+          }
+        } else {
+          const int64_t at = ((row0 + p * PPT + sub) * heads + head) * HD;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int d = da + e;
+            if (d < g.rot) {
+              const int j = d < half ? d : d - half;
+              const float cc = g.cos_sin[angle[p] + j], ss = g.cos_sin[angle[p] + half + j];
+              const float o = load1<F32>(is_q ? g.q : g.k, at + (d < half ? d + half : j));
+              const float xc = x[p][e] * cc, os = o * ss;
+              x[p][e] = d < half ? xc - os : xc + os;
+            }
           }
         }
       }
+      if (is_q) {
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p)
+          if (live(p)) {
+            uint16_t* to = g.q_out + ((row0 + p * PPT + sub) * heads + head) * HD;
+            store8_bf16(to + da, x[p]);
+            store8_bf16(to + db, x[p] + 8);
+          }
+      } else {
+        const int64_t base = slot_of(head);
+        float* scale = g.c.k_scale + (base >> 4);
+        const float old = lo > 0 ? *scale : 0.f;
+        float most = 0.f;
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p)
+          if (live(p)) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              x[p][e] = clamped(x[p][e]);
+              most = fmaxf(most, fabsf(x[p][e]));
+            }
+          }
+        const Scale sc = block_scale(max_wave(most), old, lo == 0);
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) {
+          const int i = p * PPT + sub;
+          uint2* ca = reinterpret_cast<uint2*>(g.c.k_codes + (base + i) * HD + da);
+          uint2* cb = reinterpret_cast<uint2*>(g.c.k_codes + (base + i) * HD + db);
+          uint32_t w[4] = {0, 0, 0, 0};
+          if (i < lo) {
+            if (sc.ratio == 1.f) continue;
+            const uint2 oa = *ca, ob = *cb;
+            const uint32_t o[4] = {oa.x, oa.y, ob.x, ob.y};
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e / 4] |= recode(o[e / 4] >> (8 * (e % 4)), sc.ratio) << (8 * (e % 4));
+          } else if (i < hi) {
+            float held[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float cv = code_of(x[p][e], sc.inv);
+              w[e / 4] |= byte_of(cv) << (8 * (e % 4));
+              held[e] = cv * sc.s;
+            }
+            if (g.k_held) {
+              uint16_t* to = g.k_held + ((row0 + i) * g.c.n_kv + head) * HD;
+              store8_bf16(to + da, held);
+              store8_bf16(to + db, held + 8);
+            }
+          } else {
+            continue;
+          }
+          *ca = uint2{w[0], w[1]};
+          *cb = uint2{w[2], w[3]};
+        }
+        if (lane == 0 && (lo == 0 || sc.s != old)) *scale = sc.s;
+      }
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) xa[p] = na[p], xb[p] = nb[p];
     }
   }
-  // a pass's token of a head, rotated: the lane's dims da .. da + 3, db .. db + 3
-  auto turned = [&](const void* src, int64_t at, int p, float (&x)[8]) {
-#pragma clang fp contract(off)
-    load4<F32>(src, at + da, x);
-    load4<F32>(src, at + db, x + 4);
-    if constexpr (VEC) {
-      if (paired) {
+
+  // ---- values
+  constexpr int DV = HD == 64 ? 2 : 4, NU = HD * 2 / DV / 64;  // dims of a lane's unit, units: HD / DV for each of two octets
+  using Few = Raw<F32, DV>;
+  auto unit_dim = [&](int j) { return DV * ((lane + 64 * j) % (HD / DV)); };
+  auto unit_key = [&](int j) { return 8 * ((lane + 64 * j) / (HD / DV)); };
+  auto fetch_v = [&](int u, Few (&x)[NU][8]) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float a = x[e], o = x[4 + e];
-          const float ac = a * c[p][e], os = o * s[p][e], oc = o * c[p][e], as = a * s[p][e];
-          x[e] = ac - os;
-          x[4 + e] = oc + as;
-        }
-      }
-    } else {
+    for (int j = 0; j < NU; ++j)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int d = da + e;
-        if (d < g.rot) {
-          const int j = d < half ? d : d - half;
-          const float cc = g.cos_sin[angle[p] + j], ss = g.cos_sin[angle[p] + half + j];
-          const float o = load1<F32>(src, at + (d < half ? d + half : j));
-          const float xc = x[e] * cc, os = o * ss;
-          x[e] = d < half ? xc - os : xc + os;
-        }
-      }
-    }
-  };
-
-  for (int u = u0; u < u1; ++u) {
-    if (u < g.n_q) {  // query head: rotate and round
+        const int i = unit_key(j) + e;
+        if (i >= lo && i < hi) x[j][e].load(g.v, ((row0 + i) * g.c.n_kv + (u - n_k)) * HD + unit_dim(j));
+        else
 #pragma unroll
-      for (int p = 0; p < PASSES; ++p) {
-        const int i = p * PPT + sub;
-        if (i < lo || i >= hi) continue;
-        const int64_t at = ((row0 + i) * g.n_q + u) * HD;
-        float x[8];
-        turned(g.q, at, p, x);
-        store4_bf16(g.q_out + at + da, x);
-        store4_bf16(g.q_out + at + db, x + 4);
+          for (int k = 0; k < Few::kWords; ++k) x[j][e].w[k] = 0;
       }
-      continue;
-    }
-    if (!kept) return;
-    const bool is_v = u >= g.n_q + g.c.n_kv;
-    const int head = u - g.n_q - (is_v ? g.c.n_kv : 0);
-    const int64_t base = ((int64_t(page) * g.c.n_kv + head) << g.c.page_shift) + place0;  // the block's first slot
-    float* scale = (is_v ? g.c.v_scale : g.c.k_scale) + (base >> 4);
+  };
+  const int u_v = u0 > n_k ? u0 : n_k;
+  if (u_v >= u1) return;
+  Few xv[NU][8];
+  fetch_v(u_v, xv);
+  for (int u = u_v; u < u1; ++u) {
+    Few nv[NU][8];
+    if (u + 1 < u1) fetch_v(u + 1, nv);
+    const int head = u - n_k;
+    const int64_t base = slot_of(head);
+    float* scale = g.c.v_scale + (base >> 4);
     const float old = lo > 0 ? *scale : 0.f;
     float most = 0.f;
-    if (!is_v) {
-      float x[PASSES][8];
 #pragma unroll
-      for (int p = 0; p < PASSES; ++p) {
-        const int i = p * PPT + sub;
-        if (i < lo || i >= hi) continue;
-        turned(g.k, ((row0 + i) * g.c.n_kv + head) * HD, p, x[p]);
+    for (int j = 0; j < NU; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[p][e] = clamped(x[p][e]);
-          most = fmaxf(most, fabsf(x[p][e]));
+      for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (int k = 0; k < DV; ++k) most = fmaxf(most, fabsf(clamped(xv[j][e].at(k))));
+    const Scale sc = block_scale(max_wave(most), old, lo == 0);
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+      const int d = unit_dim(j), i0 = unit_key(j);
+      if (i0 >= hi || (i0 + 8 <= lo && sc.ratio == 1.f)) continue;
+      u32x4_t* at = reinterpret_cast<u32x4_t*>(g.c.v_codes + (base + i0) * HD + d * 8);
+      uint32_t w[2 * DV];
+#pragma unroll
+      for (int k = 0; k < DV / 2; ++k) {
+        u32x4_t o = {0, 0, 0, 0};
+        if (i0 < lo) o = at[k];
+        w[4 * k] = o[0], w[4 * k + 1] = o[1], w[4 * k + 2] = o[2], w[4 * k + 3] = o[3];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float held[DV];
+        const bool mine = i0 + e >= lo && i0 + e < hi;
+#pragma unroll
+        for (int k = 0; k < DV; ++k) {
+          const int word = 2 * k + e / 4, sh = 8 * (e % 4);
+          const float cv = code_of(clamped(xv[j][e].at(k)), sc.inv);
+          uint32_t byte = byte_of(cv);
+          if (i0 + e < lo) byte = sc.ratio == 1.f ? (w[word] >> sh) & 255u : recode(w[word] >> sh, sc.ratio);
+          w[word] = (w[word] & ~(255u << sh)) | (byte << sh);
+          held[k] = cv * sc.s;
+        }
+        if (g.v_held && mine) {
+          uint16_t* to = g.v_held + ((row0 + i0 + e) * g.c.n_kv + head) * HD + d;
+          if constexpr (DV == 4)
+            *reinterpret_cast<uint2*>(to) = uint2{pack_bf16x2(held[0], held[1]), pack_bf16x2(held[2], held[3])};
+          else *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(held[0], held[1]);
         }
       }
-      const Scale sc = block_scale(max_wave(most), old, lo == 0);
 #pragma unroll
-      for (int p = 0; p < PASSES; ++p) {
-        const int i = p * PPT + sub;
-        uint32_t* ca = reinterpret_cast<uint32_t*>(g.c.k_codes + (base + i) * HD + da);
-        uint32_t* cb = reinterpret_cast<uint32_t*>(g.c.k_codes + (base + i) * HD + db);
-        if (i < lo) {
-          if (sc.ratio == 1.f) continue;
-          const uint32_t oa = *ca, ob = *cb;
-          uint32_t wa = 0, wb = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            wa |= recode(oa >> (8 * e), sc.ratio) << (8 * e);
-            wb |= recode(ob >> (8 * e), sc.ratio) << (8 * e);
-          }
-          *ca = wa, *cb = wb;
-        } else if (i < hi) {
-          float held[8];
-          uint32_t wa = 0, wb = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float a = code_of(x[p][e], sc.inv), o = code_of(x[p][4 + e], sc.inv);
-            wa |= byte_of(a) << (8 * e);
-            wb |= byte_of(o) << (8 * e);
-            held[e] = a * sc.s;
-            held[4 + e] = o * sc.s;
-          }
-          *ca = wa, *cb = wb;
-          if (g.k_held) {
-            uint16_t* h = g.k_held + ((row0 + i) * g.c.n_kv + head) * HD;
-            store4_bf16(h + da, held);
-            store4_bf16(h + db, held + 4);
-          }
-        }
-      }
-      if (lane == 0 && (lo == 0 || sc.s != old)) *scale = sc.s;
-    } else {
-      constexpr int NU = HD / 64;  // a lane's units: two dims of eight keys
-      float x[NU][8][2];
-#pragma unroll
-      for (int j = 0; j < NU; ++j) {
-        const int n = lane + 64 * j, d = 2 * (n % (HD / 2)), i0 = 8 * (n / (HD / 2));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[j][e][0] = x[j][e][1] = 0.f;
-          if (i0 + e < lo || i0 + e >= hi) continue;
-          load2<F32>(g.v, ((row0 + i0 + e) * g.c.n_kv + head) * HD + d, x[j][e]);
-          x[j][e][0] = clamped(x[j][e][0]);
-          x[j][e][1] = clamped(x[j][e][1]);
-          most = fmaxf(most, fmaxf(fabsf(x[j][e][0]), fabsf(x[j][e][1])));
-        }
-      }
-      const Scale sc = block_scale(max_wave(most), old, lo == 0);
-#pragma unroll
-      for (int j = 0; j < NU; ++j) {
-        const int n = lane + 64 * j, d = 2 * (n % (HD / 2)), i0 = 8 * (n / (HD / 2));
-        if (i0 >= hi || (i0 + 8 <= lo && sc.ratio == 1.f)) continue;
-        u32x4_t* at = reinterpret_cast<u32x4_t*>(g.c.v_codes + (base + i0) * HD + d * 8);
-        u32x4_t w = {0, 0, 0, 0};
-        if (i0 < lo) w = *at;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int word = 2 * k + e / 4, sh = 8 * (e % 4);
-            const float cv = code_of(x[j][e][k], sc.inv);
-            uint32_t byte = byte_of(cv);
-            if (i0 + e < lo) byte = sc.ratio == 1.f ? (w[word] >> sh) & 255u : recode(w[word] >> sh, sc.ratio);
-            w[word] = (w[word] & ~(255u << sh)) | (byte << sh);
-            x[j][e][k] = cv * sc.s;
-          }
-          if (g.v_held && i0 + e >= lo && i0 + e < hi)
-            *reinterpret_cast<uint32_t*>(g.v_held + ((row0 + i0 + e) * g.c.n_kv + head) * HD + d) =
-                pack_bf16x2(x[j][e][0], x[j][e][1]);
-        }
-        *at = w;
-      }
-      if (lane == 0 && (lo == 0 || sc.s != old)) *scale = sc.s;
+      for (int k = 0; k < DV / 2; ++k) at[k] = u32x4_t{w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]};
     }
+    if (lane == 0 && (lo == 0 || sc.s != old)) *scale = sc.s;
+#pragma unroll
+    for (int j = 0; j < NU; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) xv[j][e] = nv[j][e];
   }
 }
 
@@ -292,7 +344,7 @@ int launch_hd(const Kv8AppendArgs& a, hipStream_t s) {
   const int want = int(fill < 1 ? 1 : fill < items ? fill : items);
   const int per = (items + want - 1) / want, groups = (items + per - 1) / per;
   const int64_t wgs = (a.B * blocks * groups + 3) / 4;
-  if (a.rot % 8 == 0)
+  if (a.rot % 16 == 0)
     kv8_append_kernel<HD, F32, true><<<dim3(uint32_t(wgs)), 256, 0, s>>>(a, int(blocks), groups, per);
   else
     kv8_append_kernel<HD, F32, false><<<dim3(uint32_t(wgs)), 256, 0, s>>>(a, int(blocks), groups, per);
