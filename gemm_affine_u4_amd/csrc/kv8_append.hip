@@ -25,13 +25,14 @@ namespace {
 constexpr int kBlock = 16;  // keys that share a scale
 constexpr float kLimit = 57344.0f;
 
-// N neighbouring values of an fp32 or bf16 array, as loaded.
+// N neighbouring values of an fp32 or bf16 array, as loaded: `at` values on from `p`, which all lanes share (a block's
+// rows lie within 2^24 values).
 template <bool F32, int N>
 struct Raw {
   static constexpr int kWords = F32 ? N : N / 2;
   uint32_t w[kWords];
-  __device__ __forceinline__ void load(const void* p, int64_t at) {
-    const uint32_t* from = reinterpret_cast<const uint32_t*>(static_cast<const char*>(p) + at * (F32 ? 4 : 2));
+  __device__ __forceinline__ void load(const char* p, uint32_t at) {
+    const uint32_t* from = reinterpret_cast<const uint32_t*>(p + at * (F32 ? 4u : 2u));
     if constexpr (kWords % 4 == 0) {
 #pragma unroll
       for (int i = 0; i < kWords; i += 4) {
@@ -94,7 +95,7 @@ __device__ __forceinline__ uint32_t recode(uint32_t byte, float ratio) {
 
 // VEC: rot a multiple of 16, a lane's dims are two runs of 8 that pair up; otherwise 16 neighbours.
 template <int HD, bool F32, bool VEC>
-__global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendArgs g, int blocks, int groups, int per_wave) {
+__global__ __launch_bounds__(256, HD == 256 && VEC ? 3 : 2) void kv8_append_kernel(Kv8AppendArgs g, int blocks, int groups, int per_wave) {
   constexpr int LPT = HD / 16, PPT = 64 / LPT, PASSES = kBlock / PPT;  // lanes of a token, tokens of a pass
   const int lane = threadIdx.x & 63;
   const uint32_t wid = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -118,6 +119,8 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendArgs g, int bl
   if (!kept) u1 = u1 < g.n_q ? u1 : g.n_q;
   auto slot_of = [&](int head) { return ((int64_t(page) * g.c.n_kv + head) << g.c.page_shift) + place0; };
 
+  constexpr int kSize = F32 ? 4 : 2;
+
   // ---- queries and keys
   const int li = lane % LPT, sub = lane / LPT;
   const int half = g.rot >> 1, pairs = g.rot >> 4;
@@ -125,134 +128,187 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendArgs g, int bl
   const int da = !VEC ? 16 * li : paired ? 8 * li : g.rot + 16 * (li - pairs);
   const int db = paired ? half + 8 * li : da + 8;
   auto live = [&](int p) { return p * PPT + sub >= lo && p * PPT + sub < hi; };
+  // A block's values stay in registers where they fit (with the next item's loads under way, and the angles);
+  // of 256 dims, or where pairs are taken one by one, keys are read and turned twice: for the scale, then for the codes.
+  constexpr bool HELD = HD < 256 && VEC;
   using Run = Raw<F32, 8>;
   const int u_k = u1 < n_k ? u1 : n_k;
   if (u0 < u_k) {
-    auto fetch = [&](int u, Run (&a)[PASSES], Run (&o)[PASSES]) {
-      const void* src = u < g.n_q ? g.q : g.k;
-      const int heads = u < g.n_q ? g.n_q : g.c.n_kv, head = u < g.n_q ? u : u - g.n_q;
+    auto heads_of = [&](int u) { return u < g.n_q ? g.n_q : g.c.n_kv; };
+    auto first_of = [&](int u) { return (row0 * heads_of(u) + (u < g.n_q ? u : u - g.n_q)) * HD; };
+    auto offset = [&](int u, int p) { return uint32_t(p * PPT + sub) * uint32_t(heads_of(u) * HD); };
+    auto fetch = [&](int u, int p, Run& a, Run& o) {
+      const char* from = static_cast<const char*>(u < g.n_q ? g.q : g.k) + first_of(u) * kSize;
+      a.load(from, offset(u, p) + da);
+      o.load(from, offset(u, p) + db);
+    };
+    int place[PASSES];  // in the table of angles, of each pass's token
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      place[p] = 0;
+      if (!g.rot || !live(p)) continue;
+      const int64_t pos = g.positions ? g.positions[row0 + p * PPT + sub] : k0 + p * PPT + sub;
+      place[p] = pos < 0 ? 0 : pos >= g.max_pos ? g.max_pos - 1 : int(pos);
+    }
+    auto angle_of = [&](int p) { return int64_t(place[p]) * g.rot; };
+    using Angles = Raw<true, 8>;
+    auto angles = [&](int64_t at, Angles& c, Angles& s) {
+      const float* cs = g.cos_sin + at + 8 * li;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) c.w[e] = __float_as_uint(cs[e]), s.w[e] = __float_as_uint(cs[half + e]);
+    };
+    auto widen = [&](const Run& a, const Run& o, float (&x)[16]) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = a.at(e), x[8 + e] = o.at(e);
+    };
+    auto turn = [&](float (&x)[16], const Angles& c, const Angles& s) {
+#pragma clang fp contract(off)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float a = x[e], o = x[8 + e], cc = c.at(e), ss = s.at(e);
+        const float ac = a * cc, os = o * ss, oc = o * cc, as = a * ss;
+        x[e] = ac - os;
+        x[8 + e] = oc + as;
+      }
+    };
+    // a pass's token, turned, from memory
+    auto turned = [&](int u, int p, float (&x)[16]) {
+#pragma clang fp contract(off)
+      Run a, o;
+      fetch(u, p, a, o);
+      widen(a, o, x);
+      if (!g.rot) return;
+      const int64_t angle = angle_of(p);
+      if constexpr (VEC) {
+        if (paired) {
+          Angles c, s;
+          angles(angle, c, s);
+          turn(x, c, s);
+        }
+      } else {
+        const void* src = u < g.n_q ? g.q : g.k;
+        const int64_t at = first_of(u) + offset(u, p);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int d = da + e;
+          if (d < g.rot) {
+            const int j = d < half ? d : d - half;
+            const float cc = g.cos_sin[angle + j], ss = g.cos_sin[angle + half + j];
+            const float o = load1<F32>(src, at + (d < half ? d + half : j));
+            const float xc = x[e] * cc, os = o * ss;
+            x[e] = d < half ? xc - os : xc + os;
+          }
+        }
+      }
+    };
+    auto put_q = [&](int u, int p, const float (&x)[16]) {
+      uint16_t* to = g.q_out + first_of(u);
+      store8_bf16(to + (offset(u, p) + da), x);
+      store8_bf16(to + (offset(u, p) + db), x + 8);
+    };
+    auto largest = [&](const float (&x)[16], float most) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(clamped(x[e])));
+      return most;
+    };
+    auto codes_at = [&](int64_t base, int p, int d) {
+      return reinterpret_cast<uint2*>(g.c.k_codes + base * HD + uint32_t((p * PPT + sub) * HD + d));
+    };
+    auto put_k = [&](int u, int p, int64_t base, const float (&x)[16], const Scale& sc) {
+      uint32_t w[4] = {0, 0, 0, 0};
+      float held[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float cv = code_of(clamped(x[e]), sc.inv);
+        w[e / 4] |= byte_of(cv) << (8 * (e % 4));
+        held[e] = cv * sc.s;
+      }
+      *codes_at(base, p, da) = uint2{w[0], w[1]};
+      *codes_at(base, p, db) = uint2{w[2], w[3]};
+      if (g.k_held) {
+        uint16_t* to = g.k_held + first_of(u);
+        store8_bf16(to + (offset(u, p) + da), held);
+        store8_bf16(to + (offset(u, p) + db), held + 8);
+      }
+    };
+    auto recode_k = [&](int p, int64_t base, float ratio) {  // a key that was there before
+      const uint2 oa = *codes_at(base, p, da), ob = *codes_at(base, p, db);
+      const uint32_t o[4] = {oa.x, oa.y, ob.x, ob.y};
+      uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < 16; ++e) w[e / 4] |= recode(o[e / 4] >> (8 * (e % 4)), ratio) << (8 * (e % 4));
+      *codes_at(base, p, da) = uint2{w[0], w[1]};
+      *codes_at(base, p, db) = uint2{w[2], w[3]};
+    };
+    auto scale_at = [&](int u) { return g.c.k_scale + (slot_of(u - g.n_q) >> 4); };
+    auto settle = [&](int u, float most) {  // the block's scale; the keys that were there before follow it
+      float* at = scale_at(u);
+      const float old = lo > 0 ? *at : 0.f;
+      const Scale sc = block_scale(max_wave(most), old, lo == 0);
+      if (sc.ratio != 1.f) {
+        const int64_t base = slot_of(u - g.n_q);
+        for (int p = 0; p < PASSES; ++p)
+          if (p * PPT + sub < lo) recode_k(p, base, sc.ratio);
+      }
+      if (lane == 0 && (lo == 0 || sc.s != old)) *at = sc.s;
+      return sc;
+    };
+    if constexpr (HELD) {
+      Run xa[PASSES], xb[PASSES];
+      Angles c[PASSES], s[PASSES];
 #pragma unroll
       for (int p = 0; p < PASSES; ++p)
         if (live(p)) {
-          const int64_t at = ((row0 + p * PPT + sub) * heads + head) * HD;
-          a[p].load(src, at + da);
-          o[p].load(src, at + db);
+          fetch(u0, p, xa[p], xb[p]);
+          if (paired) angles(angle_of(p), c[p], s[p]);
         }
-    };
-    Run xa[PASSES], xb[PASSES];
-    fetch(u0, xa, xb);
-    // angles of the lane's pairs, for each pass's token
-    Raw<true, 8> c[PASSES], s[PASSES];
-    int64_t angle[PASSES];
+      for (int u = u0; u < u_k; ++u) {
+        Run na[PASSES], nb[PASSES];
+        if (u + 1 < u_k) {
 #pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      angle[p] = 0;
-      if (!g.rot || !live(p)) continue;
-      const int i = p * PPT + sub;
-      int64_t pos = g.positions ? g.positions[row0 + i] : k0 + i;
-      pos = pos < 0 ? 0 : pos >= g.max_pos ? g.max_pos - 1 : pos;
-      angle[p] = pos * g.rot;
-      if (paired) {
-        const float* cs = g.cos_sin + angle[p] + 8 * li;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c[p].w[e] = __float_as_uint(cs[e]), s[p].w[e] = __float_as_uint(cs[half + e]);
-      }
-    }
-    for (int u = u0; u < u_k; ++u) {
-      Run na[PASSES], nb[PASSES];
-      if (u + 1 < u_k) fetch(u + 1, na, nb);
-      const bool is_q = u < g.n_q;
-      const int head = is_q ? u : u - g.n_q, heads = is_q ? g.n_q : g.c.n_kv;
-      float x[PASSES][16];
-#pragma unroll
-      for (int p = 0; p < PASSES; ++p) {
-#pragma clang fp contract(off)
-        if (!live(p)) continue;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[p][e] = xa[p].at(e), x[p][8 + e] = xb[p].at(e);
-        if constexpr (VEC) {
-          if (paired) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float a = x[p][e], o = x[p][8 + e], cc = c[p].at(e), ss = s[p].at(e);
-              const float ac = a * cc, os = o * ss, oc = o * cc, as = a * ss;
-              x[p][e] = ac - os;
-              x[p][8 + e] = oc + as;
-            }
-          }
-        } else {
-          const int64_t at = ((row0 + p * PPT + sub) * heads + head) * HD;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int d = da + e;
-            if (d < g.rot) {
-              const int j = d < half ? d : d - half;
-              const float cc = g.cos_sin[angle[p] + j], ss = g.cos_sin[angle[p] + half + j];
-              const float o = load1<F32>(is_q ? g.q : g.k, at + (d < half ? d + half : j));
-              const float xc = x[p][e] * cc, os = o * ss;
-              x[p][e] = d < half ? xc - os : xc + os;
-            }
-          }
+          for (int p = 0; p < PASSES; ++p)
+            if (live(p)) fetch(u + 1, p, na[p], nb[p]);
         }
-      }
-      if (is_q) {
+        float x[PASSES][16], most = 0.f;
 #pragma unroll
         for (int p = 0; p < PASSES; ++p)
           if (live(p)) {
-            uint16_t* to = g.q_out + ((row0 + p * PPT + sub) * heads + head) * HD;
-            store8_bf16(to + da, x[p]);
-            store8_bf16(to + db, x[p] + 8);
+            widen(xa[p], xb[p], x[p]);
+            if (paired) turn(x[p], c[p], s[p]);
+            if (u < g.n_q) put_q(u, p, x[p]);
+            else most = largest(x[p], most);
           }
-      } else {
-        const int64_t base = slot_of(head);
-        float* scale = g.c.k_scale + (base >> 4);
-        const float old = lo > 0 ? *scale : 0.f;
+        if (u >= g.n_q) {
+          const Scale sc = settle(u, most);
+#pragma unroll
+          for (int p = 0; p < PASSES; ++p)
+            if (live(p)) put_k(u, p, slot_of(u - g.n_q), x[p], sc);
+        }
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) xa[p] = na[p], xb[p] = nb[p];
+      }
+    } else {
+      for (int u = u0; u < u_k; ++u) {
         float most = 0.f;
 #pragma unroll
         for (int p = 0; p < PASSES; ++p)
           if (live(p)) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              x[p][e] = clamped(x[p][e]);
-              most = fmaxf(most, fabsf(x[p][e]));
-            }
+            float x[16];
+            turned(u, p, x);
+            if (u < g.n_q) put_q(u, p, x);
+            else most = largest(x, most);
           }
-        const Scale sc = block_scale(max_wave(most), old, lo == 0);
+        if (u >= g.n_q) {
+          const Scale sc = settle(u, most);
 #pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-          const int i = p * PPT + sub;
-          uint2* ca = reinterpret_cast<uint2*>(g.c.k_codes + (base + i) * HD + da);
-          uint2* cb = reinterpret_cast<uint2*>(g.c.k_codes + (base + i) * HD + db);
-          uint32_t w[4] = {0, 0, 0, 0};
-          if (i < lo) {
-            if (sc.ratio == 1.f) continue;
-            const uint2 oa = *ca, ob = *cb;
-            const uint32_t o[4] = {oa.x, oa.y, ob.x, ob.y};
-#pragma unroll
-            for (int e = 0; e < 16; ++e) w[e / 4] |= recode(o[e / 4] >> (8 * (e % 4)), sc.ratio) << (8 * (e % 4));
-          } else if (i < hi) {
-            float held[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float cv = code_of(x[p][e], sc.inv);
-              w[e / 4] |= byte_of(cv) << (8 * (e % 4));
-              held[e] = cv * sc.s;
+          for (int p = 0; p < PASSES; ++p)
+            if (live(p)) {
+              float x[16];
+              turned(u, p, x);
+              put_k(u, p, slot_of(u - g.n_q), x, sc);
             }
-            if (g.k_held) {
-              uint16_t* to = g.k_held + ((row0 + i) * g.c.n_kv + head) * HD;
-              store8_bf16(to + da, held);
-              store8_bf16(to + db, held + 8);
-            }
-          } else {
-            continue;
-          }
-          *ca = uint2{w[0], w[1]};
-          *cb = uint2{w[2], w[3]};
         }
-        if (lane == 0 && (lo == 0 || sc.s != old)) *scale = sc.s;
       }
-#pragma unroll
-      for (int p = 0; p < PASSES; ++p) xa[p] = na[p], xb[p] = nb[p];
     }
   }
 
@@ -262,12 +318,13 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendArgs g, int bl
   auto unit_dim = [&](int j) { return DV * ((lane + 64 * j) % (HD / DV)); };
   auto unit_key = [&](int j) { return 8 * ((lane + 64 * j) / (HD / DV)); };
   auto fetch_v = [&](int u, Few (&x)[NU][8]) {
+    const char* from = static_cast<const char*>(g.v) + (row0 * g.c.n_kv + (u - n_k)) * HD * kSize;
 #pragma unroll
     for (int j = 0; j < NU; ++j)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int i = unit_key(j) + e;
-        if (i >= lo && i < hi) x[j][e].load(g.v, ((row0 + i) * g.c.n_kv + (u - n_k)) * HD + unit_dim(j));
+        if (i >= lo && i < hi) x[j][e].load(from, uint32_t(i) * uint32_t(g.c.n_kv * HD) + unit_dim(j));
         else
 #pragma unroll
           for (int k = 0; k < Few::kWords; ++k) x[j][e].w[k] = 0;
@@ -275,11 +332,7 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendArgs g, int bl
   };
   const int u_v = u0 > n_k ? u0 : n_k;
   if (u_v >= u1) return;
-  Few xv[NU][8];
-  fetch_v(u_v, xv);
-  for (int u = u_v; u < u1; ++u) {
-    Few nv[NU][8];
-    if (u + 1 < u1) fetch_v(u + 1, nv);
+  auto item_v = [&](int u, const Few (&xv)[NU][8]) __attribute__((always_inline)) {
     const int head = u - n_k;
     const int64_t base = slot_of(head);
     float* scale = g.c.v_scale + (base >> 4);
@@ -296,7 +349,7 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendArgs g, int bl
     for (int j = 0; j < NU; ++j) {
       const int d = unit_dim(j), i0 = unit_key(j);
       if (i0 >= hi || (i0 + 8 <= lo && sc.ratio == 1.f)) continue;
-      u32x4_t* at = reinterpret_cast<u32x4_t*>(g.c.v_codes + (base + i0) * HD + d * 8);
+      u32x4_t* at = reinterpret_cast<u32x4_t*>(g.c.v_codes + base * HD + uint32_t(i0 * HD + d * 8));
       uint32_t w[2 * DV];
 #pragma unroll
       for (int k = 0; k < DV / 2; ++k) {
@@ -318,20 +371,33 @@ __global__ __launch_bounds__(256) void kv8_append_kernel(Kv8AppendArgs g, int bl
           held[k] = cv * sc.s;
         }
         if (g.v_held && mine) {
-          uint16_t* to = g.v_held + ((row0 + i0 + e) * g.c.n_kv + head) * HD + d;
+          uint16_t* to = g.v_held + (row0 * g.c.n_kv + head) * HD + (uint32_t(i0 + e) * uint32_t(g.c.n_kv * HD) + d);
           if constexpr (DV == 4)
             *reinterpret_cast<uint2*>(to) = uint2{pack_bf16x2(held[0], held[1]), pack_bf16x2(held[2], held[3])};
           else *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(held[0], held[1]);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int k = 0; k < DV / 2; ++k) at[k] = u32x4_t{w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]};
     }
     if (lane == 0 && (lo == 0 || sc.s != old)) *scale = sc.s;
+  };
+  Few xv[HD < 256 ? NU : 1][8];
+  if constexpr (HD < 256) fetch_v(u_v, xv);
+  for (int u = u_v; u < u1; ++u) {
+    Few nv[NU][8];
+    if constexpr (HD < 256) {
+      if (u + 1 < u1) fetch_v(u + 1, nv);
+      item_v(u, xv);
 #pragma unroll
-    for (int j = 0; j < NU; ++j)
+      for (int j = 0; j < NU; ++j)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) xv[j][e] = nv[j][e];
+        for (int e = 0; e < 8; ++e) xv[j][e] = nv[j][e];
+    } else {
+      fetch_v(u, nv);
+      item_v(u, nv);
+    }
   }
 }
 
@@ -339,8 +405,10 @@ template <int HD, bool F32>
 int launch_hd(const Kv8AppendArgs& a, hipStream_t s) {
   const int64_t blocks = (int64_t(a.max_q) + 14) / kBlock + 1;  // of a sequence, the first one begun anywhere
   const int items = a.n_q + 2 * a.c.n_kv;
-  // One item a wave up to 16 waves for each compute unit, then several, whose angles are read once.
-  const int64_t fill = int64_t(device_cus()) * 16 / (a.B * blocks);
+  // One item a wave up to 48 waves for each compute unit, then several, whose angles are read once (8192 tokens, 56
+  // items a block: 3 a wave 58 us, 8 of them 68).
+  const int64_t met = a.T / kBlock + a.B;  // blocks that tokens meet, about
+  const int64_t fill = int64_t(device_cus()) * 48 / met;
   const int want = int(fill < 1 ? 1 : fill < items ? fill : items);
   const int per = (items + want - 1) / want, groups = (items + per - 1) / per;
   const int64_t wgs = (a.B * blocks * groups + 3) / 4;
