@@ -64,8 +64,8 @@ __device__ __forceinline__ Tile tile_of(const LoraArgs& g, int64_t t0, int token
   return r;
 }
 
-// TT column tiles of 16 tokens, RT row tiles of 16 ranks.
-template <int TT, int RT>
+// TT column tiles of 16 tokens, RT row tiles of 16 ranks, KS steps of 32 inputs at a time.
+template <int TT, int RT, int KS>
 __global__ __launch_bounds__(kWaves * 64, 2) void lora_shrink_kernel(LoraArgs g, int row_groups, int splits, int shares) {
   const int lane = threadIdx.x & 63, n = lane & 15, hg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -76,15 +76,20 @@ __global__ __launch_bounds__(kWaves * 64, 2) void lora_shrink_kernel(LoraArgs g,
   if (share >= tile.count) return;
 
   const int units = g.K / 64, u0 = units * split / splits, u1 = units * (split + 1) / splits;
+  // the wave's steps: two of each fourth unit of 64
+  const int steps = u0 + wave < u1 ? (u1 - u0 - wave + kWaves - 1) / kWaves * 2 : 0;
+  auto input = [&](int q) { return (u0 + wave + (q >> 1) * kWaves) * 64 + (q & 1) * 32; };
   const uint16_t* xp[TT];
+  int index[TT];
 #pragma unroll
   for (int i = 0; i < TT; ++i) {
     const int64_t t = t0 + 16 * i + n;
     xp[i] = g.x + (t < g.T ? t : g.T - 1) * g.K + 8 * hg;
+    index[i] = __shfl(tile.index, 16 * i + n);
   }
   __shared__ f32x4_t s_acc[kWaves][TT * RT][64];
-  for (int at = share; at < tile.count; at += shares) {
-    const int id = __builtin_amdgcn_readlane(tile.list, at);
+  for (int slot = share; slot < tile.count; slot += shares) {
+    const int id = __builtin_amdgcn_readlane(tile.list, slot);
     const uint16_t* ap[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
@@ -96,21 +101,41 @@ __global__ __launch_bounds__(kWaves * 64, 2) void lora_shrink_kernel(LoraArgs g,
     for (int i = 0; i < TT; ++i)
 #pragma unroll
       for (int j = 0; j < RT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int u = u0 + wave; u < u1; u += kWaves) {
-      u32x4_t xv[2][TT], av[2][RT];
+    // KS steps at a time, the next ones' loads under way; columns of other adapters are not read
+    u32x4_t xv[2][KS][TT], av[2][KS][RT];
+    auto fetch = [&](int set, int q) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < KS; ++k) {
+        const int at = input(q + k < steps ? q + k : steps - 1);  // behind the last step that one again, not used
 #pragma unroll
-        for (int i = 0; i < RT; ++i) av[k][i] = *reinterpret_cast<const u32x4_t*>(ap[i] + u * 64 + 32 * k);
+        for (int i = 0; i < RT; ++i) av[set][k][i] = *reinterpret_cast<const u32x4_t*>(ap[i] + at);
 #pragma unroll
-        for (int i = 0; i < TT; ++i) xv[k][i] = *reinterpret_cast<const u32x4_t*>(xp[i] + u * 64 + 32 * k);
+        for (int i = 0; i < TT; ++i) {
+          xv[set][k][i] = u32x4_t{0, 0, 0, 0};
+          if (index[i] == slot) xv[set][k][i] = *reinterpret_cast<const u32x4_t*>(xp[i] + at);
+        }
       }
+    };
+    auto use = [&](int set, int q) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int k = 0; k < KS; ++k) {
+        if (q + k >= steps) continue;
 #pragma unroll
         for (int i = 0; i < TT; ++i)
 #pragma unroll
-          for (int j = 0; j < RT; ++j) acc[i][j] = mma(av[k][j], xv[k][i], acc[i][j]);
+          for (int j = 0; j < RT; ++j) acc[i][j] = mma(av[set][k][j], xv[set][k][i], acc[i][j]);
+      }
+    };
+    if (steps > 0) {
+      fetch(0, 0);
+      for (int q = 0;;) {
+        if (q + KS < steps) fetch(1, q + KS);
+        use(0, q);
+        if ((q += KS) >= steps) break;
+        if (q + KS < steps) fetch(0, q + KS);
+        use(1, q);
+        if ((q += KS) >= steps) break;
+      }
     }
 #pragma unroll
     for (int i = 0; i < TT; ++i)
@@ -125,7 +150,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void lora_shrink_kernel(LoraArgs g,
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) v += s_acc[w][e][lane];
       const int tt = 16 * (e / RT) + n, r = r0 + 16 * (e % RT) + 4 * hg;
-      if (__shfl(tile.index, tt) == at && r < R)
+      if (__shfl(tile.index, tt) == slot && r < R)
         *reinterpret_cast<f32x4_t*>(g.ws + (int64_t(split) * g.T + t0 + tt) * R + r) = v;
     }
     __syncthreads();
@@ -146,11 +171,47 @@ __device__ __forceinline__ float base_at(const void* p, int64_t at) {
   else return bf16_bits_to_f32(static_cast<const uint16_t*>(p)[at]);
 }
 
+// Four neighbours of h (the ranges' sums in order, times the adapter's factor) in three bf16 pieces.
+__device__ __forceinline__ void pieces4(const float* p, int64_t stride, int splits, float f, uint2 (&h)[3]) {
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+  int i = 0;
+  for (; i + 4 <= splits; i += 4) {
+    f32x4_t x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = *reinterpret_cast<const f32x4_t*>(p + (i + k) * stride);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v += x[k];
+  }
+  for (; i < splits; ++i) v += *reinterpret_cast<const f32x4_t*>(p + i * stride);
+  v *= f;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    h[k] = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    v -= f32x4_t{bf16_lo(h[k].x), bf16_hi(h[k].x), bf16_lo(h[k].y), bf16_hi(h[k].y)};
+  }
+}
+
+// Many tokens: the pieces once, for all blocks of the expanding launch.  to: bf16 [3][T][R].
+__global__ __launch_bounds__(256) void lora_join_kernel(LoraArgs g, uint16_t* to, int splits) {
+  const int R = g.n_parts * g.rank;
+  const int64_t n = g.T * R, at = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (at >= n) return;
+  const int id = g.ids[at / R];
+  if (uint32_t(id) >= uint32_t(g.n_adapters)) return;
+  uint2 h[3];
+  pieces4(g.ws + at, n, splits, g.scales ? g.scales[id] : 1.f, h);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) *reinterpret_cast<uint2*>(to + k * n + at) = h[k];
+}
+
 // VEC: every part's rows are a multiple of 16 and its arrays 16-byte aligned.
+// pieces: bf16 [3][T][R] where they were made by the launch before, else made here, in LDS.
 template <int TT, int RANK, bool BASE32, bool OUT32, bool VEC>
-__global__ __launch_bounds__(kWaves * 64) void lora_expand_kernel(LoraArgs g, int row_chunks, int splits, int shares) {
+__global__ __launch_bounds__(kWaves * 64) void lora_expand_kernel(LoraArgs g, const uint16_t* pieces, int row_chunks,
+                                                                  int splits, int shares) {
   using E = Expand<RANK>;
   constexpr int TOK = 16 * TT, ROW = RANK + 8;  // bf16 of a token's piece in LDS, 16 bytes of pad
+  constexpr bool MADE = TT > 1;
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, hg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t t0 = int64_t(blockIdx.x / row_chunks) * TOK;
@@ -171,75 +232,90 @@ __global__ __launch_bounds__(kWaves * 64) void lora_expand_kernel(LoraArgs g, in
   const Tile tile = tile_of(g, t0, TOK, lane);
   if (share > 0 && share >= tile.count) return;
 
-  // h of the tile's tokens that are this block's, times the adapter's factor, in three pieces
-  __shared__ __attribute__((aligned(16))) uint16_t s_h[3][TOK][ROW];
-  for (int e0 = 0; e0 < TOK * RANK / 4; e0 += kWaves * 64) {
-    const int e = e0 + tid, t = e / (RANK / 4), r = e % (RANK / 4) * 4;
-    const int index = __shfl(tile.index, t & 63), id = __shfl(tile.id, t & 63);
-    if (t >= TOK || index < 0 || index % shares != share) continue;
-    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-    const float* p = g.ws + (t0 + t) * R + part * RANK + r;
-    for (int i = 0; i < splits; ++i) v += *reinterpret_cast<const f32x4_t*>(p + int64_t(i) * g.T * R);
-    const float f = g.scales ? g.scales[id] : 1.f;
+  // Rows 4h + i of product j are outputs n0 + 16j + 4h + i: four lanes have 16 neighbours of a token.  Weights,
+  // and what is added to, are under way before anything is waited for.
+  const bool mine = n0 < N;
+  auto weights_of = [&](int at, u32x4_t (&w)[4][E::kLoads]) {
+    const int id = __builtin_amdgcn_readlane(tile.list, at);
+    const uint16_t* b = g.b + (int64_t(id) * total + first) * RANK;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float x = v[i] * f;
+    for (int j = 0; j < 4; ++j) {
+      const int row = n0 + 16 * j + n < N ? n0 + 16 * j + n : N - 1;
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const uint16_t h = f32_to_bf16_bits(x);
-        s_h[k][t][r + i] = h;
-        x -= bf16_bits_to_f32(h);
+      for (int l = 0; l < E::kLoads; ++l)
+        w[j][l] = *reinterpret_cast<const u32x4_t*>(b + int64_t(row) * RANK + 8 * ((4 * l + hg) % E::kChunks));
+    }
+  };
+  u32x4_t w[4][E::kLoads];
+  if (mine && share < tile.count) weights_of(share, w);
+  using BaseRaw = std::conditional_t<BASE32, u32x4_t, uint2>;
+  BaseRaw from[TT][4];
+  if constexpr (VEC) {
+    if (mine) {
+#pragma unroll
+      for (int i = 0; i < TT; ++i) {
+        const int64_t t = t0 + 16 * i + n;
+        const int index = __shfl(tile.index, 16 * i + n);
+        if (t >= g.T || (index < 0 ? share > 0 : index % shares != share)) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int64_t at = t * N + (n0 + 16 * j < N ? n0 + 16 * j : N - 16) + 4 * hg;
+          from[i][j] = *reinterpret_cast<const BaseRaw*>(static_cast<const char*>(base) + at * (BASE32 ? 4 : 2));
+        }
       }
     }
   }
-  __syncthreads();
-  if (n0 >= N) return;
 
-  // rows 4h + i of product j are outputs n0 + 16 h + 4 j + i: a lane ends with 16 neighbours
-  const int wrow = n0 + 16 * (n >> 2) + (n & 3);
+  // h of the tile's tokens that are this block's, in three pieces
+  __shared__ __attribute__((aligned(16))) uint16_t s_h[3][MADE ? 1 : TOK][ROW];
+  if constexpr (!MADE) {
+    for (int e0 = 0; e0 < TOK * RANK / 4; e0 += kWaves * 64) {
+      const int e = e0 + tid, t = e / (RANK / 4), r = e % (RANK / 4) * 4;
+      const int index = __shfl(tile.index, t & 63), id = __shfl(tile.id, t & 63);
+      if (t >= TOK || index < 0 || index % shares != share) continue;
+      uint2 h[3];
+      pieces4(g.ws + (t0 + t) * R + part * RANK + r, g.T * R, splits, g.scales ? g.scales[id] : 1.f, h);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) *reinterpret_cast<uint2*>(&s_h[k][t][r]) = h[k];
+    }
+    __syncthreads();
+  }
+  if (!mine) return;
+
   auto columns = [&](auto keep, const f32x4_t (&acc)[TT][4]) {
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
       const int64_t t = t0 + 16 * i + n;
-      const int o0 = n0 + 16 * hg;
       const int index = __shfl(tile.index, 16 * i + n);
-      if (t >= g.T || !keep(index) || o0 >= N) continue;
-      const int64_t at = t * N + o0;
-      if constexpr (VEC) {
+      if (t >= g.T || !keep(index)) continue;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 4; ++j) {
+        const int o = n0 + 16 * j + 4 * hg;
+        const int64_t at = t * N + o;
+        if constexpr (VEC) {
+          if (n0 + 16 * j >= N) continue;
           f32x4_t v;
           if constexpr (BASE32) {
-            v = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(base) + at + 4 * j);
+            v = __builtin_bit_cast(f32x4_t, from[i][j]);
           } else {
-            const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + at + 4 * j);
-            v = f32x4_t{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+            v = f32x4_t{bf16_lo(from[i][j].x), bf16_hi(from[i][j].x), bf16_lo(from[i][j].y), bf16_hi(from[i][j].y)};
           }
           v += acc[i][j];
-          if constexpr (OUT32) *reinterpret_cast<f32x4_t*>(static_cast<float*>(y) + at + 4 * j) = v;
+          if constexpr (OUT32) *reinterpret_cast<f32x4_t*>(static_cast<float*>(y) + at) = v;
           else
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + at + 4 * j) =
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + at) =
                 uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-        }
-      } else {
+        } else {
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (o0 + e < N) store_out(y, at + e, base_at<BASE32>(base, at + e) + acc[i][e >> 2][e & 3], OUT32);
+          for (int e = 0; e < 4; ++e)
+            if (o + e < N) store_out(y, at + e, base_at<BASE32>(base, at + e) + acc[i][j][e], OUT32);
+        }
       }
     }
   };
   f32x4_t acc[TT][4];
   for (int at = share; at < tile.count; at += shares) {
-    const int id = __builtin_amdgcn_readlane(tile.list, at);
-    const uint16_t* b = g.b + (int64_t(id) * total + first) * RANK;
-    u32x4_t w[4][E::kLoads];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int row = wrow + 4 * j < N ? wrow + 4 * j : N - 1;
-#pragma unroll
-      for (int l = 0; l < E::kLoads; ++l)
-        w[j][l] = *reinterpret_cast<const u32x4_t*>(b + int64_t(row) * RANK + 8 * ((4 * l + hg) % E::kChunks));
-    }
+    if (at != share) weights_of(at, w);
 #pragma unroll
     for (int i = 0; i < TT; ++i)
 #pragma unroll
@@ -250,7 +326,14 @@ __global__ __launch_bounds__(kWaves * 64) void lora_expand_kernel(LoraArgs g, in
 #pragma unroll
       for (int i = 0; i < TT; ++i) {
         u32x4_t h = {0, 0, 0, 0};
-        if (piece < 3) h = *reinterpret_cast<const u32x4_t*>(&s_h[piece < 3 ? piece : 0][16 * i + n][8 * k8]);
+        if (piece < 3) {
+          if constexpr (MADE) {
+            const int64_t t = t0 + 16 * i + n < g.T ? t0 + 16 * i + n : g.T - 1;
+            h = *reinterpret_cast<const u32x4_t*>(pieces + (piece * g.T + t) * R + part * RANK + 8 * k8);
+          } else {
+            h = *reinterpret_cast<const u32x4_t*>(&s_h[piece][16 * i + n][8 * k8]);
+          }
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = mma(w[j][m % E::kLoads], h, acc[i][j]);
       }
@@ -268,28 +351,46 @@ __global__ __launch_bounds__(kWaves * 64) void lora_expand_kernel(LoraArgs g, in
 
 // How a call is cut: a function of the sizes that its workspace is asked for with.
 struct Plan {
-  int tt, rt, row_groups, splits, shares;
+  int tt, rt, row_groups, splits, shares;  // column and row tiles of a shrinking block; shares of a tile's adapters
   int64_t tiles;
 };
+constexpr int kMany = 256;  // tokens: from here on tiles are larger, and h is joined by a launch of its own
 Plan plan_of(int64_t T, int64_t K, int64_t rank, int64_t n_parts) {
   Plan p;
-  const int64_t R = rank * n_parts;
-  p.tt = T > 256 ? 4 : 1;
-  p.rt = T > 256 && R > 16 ? (R > 32 ? 4 : 2) : 1;
+  const int64_t rows = (rank * n_parts + 15) / 16, cus = device_cus();
+  const bool many = T > kMany;
+  p.tt = many ? 4 : 1;
+  p.rt = rows % 4 == 0 ? 4 : rows % 3 == 0 ? 3 : rows % 2 == 0 ? 2 : 1;
   p.tiles = (T + 16 * p.tt - 1) / (16 * p.tt);
-  p.row_groups = int((R + 16 * p.rt - 1) / (16 * p.rt));
-  p.shares = p.tt == 1 ? int(T < 16 ? T < 1 ? 1 : T : 16) : 4;
-  const int64_t blocks = p.tiles * p.row_groups * (p.tt == 1 ? p.shares : 1), most = (K / 64 + kWaves - 1) / kWaves;
-  int64_t s = (4 * device_cus() + blocks - 1) / (blocks ? blocks : 1);
+  p.row_groups = int(rows / p.rt);
+  p.shares = many ? 4 : int(T < 16 ? T < 1 ? 1 : T : 16);
+  const int64_t blocks = p.tiles * p.row_groups * (many ? 1 : p.shares), most = (K / 64 + kWaves - 1) / kWaves;
+  // blocks for every place of the GPU: 2 of a unit (many tokens, whose registers allow no more) or 4
+  int64_t s = blocks ? (many ? 2 : 4) * cus / blocks : 1;
   s = s > most ? most : s;
   p.splits = int(s < 1 ? 1 : s > 64 ? 64 : s);
   return p;
 }
 
-template <int TT, int RT>
-void shrink(const LoraArgs& a, const Plan& p, hipStream_t s) {
-  lora_shrink_kernel<TT, RT><<<dim3(uint32_t(p.tiles * p.row_groups), uint32_t(p.splits * p.shares)), kWaves * 64, 0,
+template <int TT, int RT, int KS>
+void shrink_as(const LoraArgs& a, const Plan& p, hipStream_t s) {
+  lora_shrink_kernel<TT, RT, KS><<<dim3(uint32_t(p.tiles * p.row_groups), uint32_t(p.splits * p.shares)), kWaves * 64, 0,
                                s>>>(a, p.row_groups, p.splits, p.shares);
+}
+
+template <int TT, int KS>
+void shrink(const LoraArgs& a, const Plan& p, hipStream_t s) {
+  switch (p.rt) {
+    case 1: return shrink_as<TT, 1, KS>(a, p, s);
+    case 2: return shrink_as<TT, 2, KS>(a, p, s);
+    case 3: return shrink_as<TT, 3, KS>(a, p, s);
+    default: return shrink_as<TT, 4, KS>(a, p, s);
+  }
+}
+
+// Behind the ranges' sums in the workspace.
+uint16_t* pieces_of(const LoraArgs& a, const Plan& p) {
+  return reinterpret_cast<uint16_t*>(a.ws + int64_t(p.splits) * a.T * a.rank * a.n_parts);
 }
 
 template <int TT, int RANK, bool B32, bool O32>
@@ -301,9 +402,11 @@ void expand_v(const LoraArgs& a, const Plan& p, hipStream_t s) {
     vec = vec && a.rows[i] % 16 == 0 &&
           (reinterpret_cast<uintptr_t>(a.base[i]) | reinterpret_cast<uintptr_t>(a.y[i])) % 16 == 0;
   }
-  const dim3 grid(uint32_t(p.tiles * chunks), uint32_t(p.shares));
-  if (vec) lora_expand_kernel<TT, RANK, B32, O32, true><<<grid, kWaves * 64, 0, s>>>(a, chunks, p.splits, p.shares);
-  else lora_expand_kernel<TT, RANK, B32, O32, false><<<grid, kWaves * 64, 0, s>>>(a, chunks, p.splits, p.shares);
+  const int64_t tiles = (a.T + 16 * TT - 1) / (16 * TT);
+  const dim3 grid(uint32_t(tiles * chunks), uint32_t(p.shares));
+  const uint16_t* h = pieces_of(a, p);
+  if (vec) lora_expand_kernel<TT, RANK, B32, O32, true><<<grid, kWaves * 64, 0, s>>>(a, h, chunks, p.splits, p.shares);
+  else lora_expand_kernel<TT, RANK, B32, O32, false><<<grid, kWaves * 64, 0, s>>>(a, h, chunks, p.splits, p.shares);
 }
 template <int TT, int RANK>
 void expand_r(const LoraArgs& a, const Plan& p, hipStream_t s) {
@@ -325,24 +428,25 @@ void expand(const LoraArgs& a, const Plan& p, hipStream_t s) {
 
 bool lora_launches(int64_t T, const int32_t (&rows)[3]) {
   const int64_t chunks = (int64_t(rows[0]) + 255) / 256 + (int64_t(rows[1]) + 255) / 256 + (int64_t(rows[2]) + 255) / 256;
-  return ((T + 63) / 64 + 16) * chunks < int64_t(1) << 24;
+  return ((T + 31) / 32 + 16) * chunks < int64_t(1) << 24;
 }
 
 uint64_t lora_workspace(int64_t T, int64_t K, int64_t rank, int64_t n_parts) {
-  const uint64_t n = uint64_t(plan_of(T, K, rank, n_parts).splits) * uint64_t(T) * uint64_t(rank * n_parts) * 4;
+  const Plan p = plan_of(T, K, rank, n_parts);
+  const uint64_t n = uint64_t(T) * uint64_t(rank * n_parts) * (uint64_t(p.splits) * 4 + (p.tt > 1 ? 6 : 0));
   return n ? n : 256;
 }
 
 int launch_lora(const LoraArgs& a, hipStream_t s) {
   const Plan p = plan_of(a.T, a.K, a.rank, a.n_parts);
-  if (p.tt == 1) {
-    shrink<1, 1>(a, p, s);
+  if (a.T <= kMany) {
+    shrink<1, 4>(a, p, s);
     expand<1>(a, p, s);
   } else {
-    if (p.rt == 1) shrink<4, 1>(a, p, s);
-    else if (p.rt == 2) shrink<4, 2>(a, p, s);
-    else shrink<4, 4>(a, p, s);
-    expand<4>(a, p, s);
+    shrink<4, 1>(a, p, s);
+    const int64_t n = (a.T * a.rank * a.n_parts / 4 + 255) / 256;
+    lora_join_kernel<<<dim3(uint32_t(n)), 256, 0, s>>>(a, pieces_of(a, p), p.splits);
+    expand<2>(a, p, s);
   }
   return hipGetLastError() == hipSuccess ? 0 : 6;
 }

@@ -151,7 +151,7 @@ int qmm_spec_verify(const int32_t* draft, int64_t D, const int32_t* draft_start,
  *     QMM_OUT_F32).  base NULL, or base_p = y_p (both dtypes the same): y is updated in place.
  *   Tokens of one adapter that stand side by side (a request's prompt) share its weights' reads.
  * Sums are fp32; A x is taken on as three bf16 pieces (24 bits), so y is rounded once.
- * T up to 2^24, the sum of rows up to 2^24, n_adapters up to 65535, (T / 64 + 17) * (rows / 256 + 3)
+ * T up to 2^24, the sum of rows up to 2^24, n_adapters up to 65535, (T / 32 + 17) * (rows / 256 + 3)
  * below 2^24.
  * workspace: 256-byte aligned, at least qmm_lora_workspace_bytes of the same sizes (0 for sizes
  * out of range; always > 0 otherwise).
