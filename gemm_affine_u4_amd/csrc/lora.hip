@@ -37,32 +37,38 @@ __device__ __forceinline__ f32x4_t mma(u32x4_t a, u32x4_t b, f32x4_t c) {
 // another loop (seen in its output, and as a register stored too early).
 __device__ __forceinline__ void mma_settle(f32x4_t& c) { asm volatile("s_nop 7\n\ts_nop 7" : "+v"(c)); }
 
-// The distinct adapters of a tile of up to 64 tokens: lane t has token t.
+// The adapters of a tile of up to 64 tokens, lane t having token t, and which of them a block (a share of the tile)
+// takes.  Of few tokens share i takes token i's adapter if no token in front has the same one; of
+// many, where tiles of one adapter are the rule, each shares-th of the distinct ones.
+constexpr int kNone = -1, kNoToken = -2;
+template <int TT>
 struct Tile {
-  int id;     // of the lane's token, -1: none
-  int index;  // of it among the distinct ones
-  int list;   // lane i: the i-th distinct adapter
-  int count;
+  int id;  // of the lane's token
+  int list = 0, count = 0;  // lane i: the i-th distinct one (many tokens), or this block's only one
+  __device__ __forceinline__ Tile(const LoraArgs& g, int64_t t0, int lane, int share) {
+    id = kNoToken;
+    if (lane < 16 * TT && t0 + lane < g.T) {
+      id = g.ids[t0 + lane];
+      if (uint32_t(id) >= uint32_t(g.n_adapters)) id = kNone;
+    }
+    if constexpr (TT == 1) {
+      list = __builtin_amdgcn_readlane(id, share);
+      const uint64_t same = __ballot(id == list);
+      count = list != kNoToken && __ffsll(static_cast<unsigned long long>(same)) - 1 == share;
+    } else {
+      uint64_t left = __ballot(id != kNoToken);
+      while (left) {
+        const int next = __builtin_amdgcn_readlane(id, __ffsll(static_cast<unsigned long long>(left)) - 1);
+        left &= ~__ballot(id == next);
+        if (lane == count) list = next;
+        ++count;
+      }
+    }
+  }
+  // turns of this block: from(share) on in steps(shares) up to count
+  __device__ __forceinline__ static int from(int share) { return TT == 1 ? 0 : share; }
+  __device__ __forceinline__ int at(int turn) const { return __builtin_amdgcn_readlane(list, turn); }
 };
-__device__ __forceinline__ Tile tile_of(const LoraArgs& g, int64_t t0, int tokens, int lane) {
-  Tile r;
-  r.id = -1;
-  if (lane < tokens && t0 + lane < g.T) {
-    r.id = g.ids[t0 + lane];
-    if (uint32_t(r.id) >= uint32_t(g.n_adapters)) r.id = -1;
-  }
-  r.index = -1, r.list = 0, r.count = 0;
-  uint64_t left = __ballot(r.id >= 0);
-  while (left) {
-    const int id = __builtin_amdgcn_readlane(r.id, __ffsll(static_cast<unsigned long long>(left)) - 1);
-    const uint64_t same = __ballot(r.id == id);
-    if (r.id == id) r.index = r.count;
-    if (lane == r.count) r.list = id;
-    ++r.count;
-    left &= ~same;
-  }
-  return r;
-}
 
 // TT column tiles of 16 tokens, RT row tiles of 16 ranks, KS steps of 32 inputs at a time.
 template <int TT, int RT, int KS>
@@ -72,24 +78,26 @@ __global__ __launch_bounds__(kWaves * 64, 2) void lora_shrink_kernel(LoraArgs g,
   const int split = blockIdx.y % splits, share = blockIdx.y / splits;
   const int64_t t0 = int64_t(blockIdx.x / row_groups) * (16 * TT);
   const int R = g.n_parts * g.rank, r0 = int(blockIdx.x % row_groups) * (16 * RT);
-  const Tile tile = tile_of(g, t0, 16 * TT, lane);
-  if (share >= tile.count) return;
+  using T = Tile<TT>;
+  const T tile(g, t0, lane, share);
+  if (T::from(share) >= tile.count) return;
 
   const int units = g.K / 64, u0 = units * split / splits, u1 = units * (split + 1) / splits;
   // the wave's steps: two of each fourth unit of 64
   const int steps = u0 + wave < u1 ? (u1 - u0 - wave + kWaves - 1) / kWaves * 2 : 0;
   auto input = [&](int q) { return (u0 + wave + (q >> 1) * kWaves) * 64 + (q & 1) * 32; };
   const uint16_t* xp[TT];
-  int index[TT];
+  int ids[TT];
 #pragma unroll
   for (int i = 0; i < TT; ++i) {
     const int64_t t = t0 + 16 * i + n;
     xp[i] = g.x + (t < g.T ? t : g.T - 1) * g.K + 8 * hg;
-    index[i] = __shfl(tile.index, 16 * i + n);
+    ids[i] = __shfl(tile.id, 16 * i + n);
   }
   __shared__ f32x4_t s_acc[kWaves][TT * RT][64];
-  for (int slot = share; slot < tile.count; slot += shares) {
-    const int id = __builtin_amdgcn_readlane(tile.list, slot);
+  for (int turn = T::from(share); turn < tile.count; turn += shares) {
+    const int id = tile.at(turn);
+    if (id < 0) continue;
     const uint16_t* ap[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
@@ -101,8 +109,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void lora_shrink_kernel(LoraArgs g,
     for (int i = 0; i < TT; ++i)
 #pragma unroll
       for (int j = 0; j < RT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    // KS steps at a time, the next ones' loads under way; columns of other adapters are not read
-    u32x4_t xv[2][KS][TT], av[2][KS][RT];
+    // KS steps at a time, of many tokens the next ones' loads under way (of few a wave has no more than these);
+    // columns of other adapters are not read
+    constexpr int SETS = TT > 1 ? 2 : 1;
+    u32x4_t xv[SETS][KS][TT], av[SETS][KS][RT];
     auto fetch = [&](int set, int q) {
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
@@ -112,7 +122,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void lora_shrink_kernel(LoraArgs g,
 #pragma unroll
         for (int i = 0; i < TT; ++i) {
           xv[set][k][i] = u32x4_t{0, 0, 0, 0};
-          if (index[i] == slot) xv[set][k][i] = *reinterpret_cast<const u32x4_t*>(xp[i] + at);
+          if (ids[i] == id) xv[set][k][i] = *reinterpret_cast<const u32x4_t*>(xp[i] + at);
         }
       }
     };
@@ -126,7 +136,12 @@ __global__ __launch_bounds__(kWaves * 64, 2) void lora_shrink_kernel(LoraArgs g,
           for (int j = 0; j < RT; ++j) acc[i][j] = mma(av[set][k][j], xv[set][k][i], acc[i][j]);
       }
     };
-    if (steps > 0) {
+    if constexpr (SETS == 1) {
+      for (int q = 0; q < steps; q += KS) {
+        fetch(0, q);
+        use(0, q);
+      }
+    } else if (steps > 0) {
       fetch(0, 0);
       for (int q = 0;;) {
         if (q + KS < steps) fetch(1, q + KS);
@@ -150,7 +165,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void lora_shrink_kernel(LoraArgs g,
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) v += s_acc[w][e][lane];
       const int tt = 16 * (e / RT) + n, r = r0 + 16 * (e % RT) + 4 * hg;
-      if (__shfl(tile.index, tt) == slot && r < R)
+      if (__shfl(tile.id, tt) == id && r < R)
         *reinterpret_cast<f32x4_t*>(g.ws + (int64_t(split) * g.T + t0 + tt) * R + r) = v;
     }
     __syncthreads();
@@ -172,17 +187,22 @@ __device__ __forceinline__ float base_at(const void* p, int64_t at) {
 }
 
 // Four neighbours of h (the ranges' sums in order, times the adapter's factor) in three bf16 pieces.
+template <int N>
+__device__ __forceinline__ void add_ranges(const float* p, int64_t stride, int splits, int& i, f32x4_t& v) {
+  for (; i + N <= splits; i += N) {
+    f32x4_t x[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) x[k] = *reinterpret_cast<const f32x4_t*>(p + (i + k) * stride);
+#pragma unroll
+    for (int k = 0; k < N; ++k) v += x[k];
+  }
+}
 __device__ __forceinline__ void pieces4(const float* p, int64_t stride, int splits, float f, uint2 (&h)[3]) {
   f32x4_t v = {0.f, 0.f, 0.f, 0.f};
   int i = 0;
-  for (; i + 4 <= splits; i += 4) {
-    f32x4_t x[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] = *reinterpret_cast<const f32x4_t*>(p + (i + k) * stride);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v += x[k];
-  }
-  for (; i < splits; ++i) v += *reinterpret_cast<const f32x4_t*>(p + i * stride);
+  add_ranges<8>(p, stride, splits, i, v);
+  add_ranges<4>(p, stride, splits, i, v);
+  add_ranges<1>(p, stride, splits, i, v);
   v *= f;
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
@@ -207,7 +227,7 @@ __global__ __launch_bounds__(256) void lora_join_kernel(LoraArgs g, uint16_t* to
 // VEC: every part's rows are a multiple of 16 and its arrays 16-byte aligned.
 // pieces: bf16 [3][T][R] where they were made by the launch before, else made here, in LDS.
 template <int TT, int RANK, bool BASE32, bool OUT32, bool VEC>
-__global__ __launch_bounds__(kWaves * 64) void lora_expand_kernel(LoraArgs g, const uint16_t* pieces, int row_chunks,
+__global__ __launch_bounds__(kWaves * 64, TT == 1 && RANK <= 32 ? 4 : 2) void lora_expand_kernel(LoraArgs g, const uint16_t* pieces, int row_chunks,
                                                                   int splits, int shares) {
   using E = Expand<RANK>;
   constexpr int TOK = 16 * TT, ROW = RANK + 8;  // bf16 of a token's piece in LDS, 16 bytes of pad
@@ -229,36 +249,38 @@ __global__ __launch_bounds__(kWaves * 64) void lora_expand_kernel(LoraArgs g, co
   void* y = g.y[part];
   const int total = g.rows[0] + g.rows[1] + g.rows[2], R = g.n_parts * RANK;
 
-  const Tile tile = tile_of(g, t0, TOK, lane);
-  if (share > 0 && share >= tile.count) return;
+  using T = Tile<TT>;
+  const T tile(g, t0, lane, share);
+  if (T::from(share) >= tile.count) return;
+  const int id0 = tile.at(T::from(share));
 
   // Rows 4h + i of product j are outputs n0 + 16j + 4h + i: four lanes have 16 neighbours of a token.  Weights,
   // and what is added to, are under way before anything is waited for.
   const bool mine = n0 < N;
-  auto weights_of = [&](int at, u32x4_t (&w)[4][E::kLoads]) {
-    const int id = __builtin_amdgcn_readlane(tile.list, at);
+  constexpr int J = 4;  // products of 16 rows
+  auto weights_of = [&](int id, u32x4_t (&w)[J][E::kLoads]) {
     const uint16_t* b = g.b + (int64_t(id) * total + first) * RANK;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < J; ++j) {
       const int row = n0 + 16 * j + n < N ? n0 + 16 * j + n : N - 1;
 #pragma unroll
       for (int l = 0; l < E::kLoads; ++l)
         w[j][l] = *reinterpret_cast<const u32x4_t*>(b + int64_t(row) * RANK + 8 * ((4 * l + hg) % E::kChunks));
     }
   };
-  u32x4_t w[4][E::kLoads];
-  if (mine && share < tile.count) weights_of(share, w);
+  u32x4_t w[J][E::kLoads];
+  if (mine && id0 >= 0) weights_of(id0, w);
   using BaseRaw = std::conditional_t<BASE32, u32x4_t, uint2>;
-  BaseRaw from[TT][4];
+  BaseRaw from[TT][J];
   if constexpr (VEC) {
     if (mine) {
 #pragma unroll
       for (int i = 0; i < TT; ++i) {
         const int64_t t = t0 + 16 * i + n;
-        const int index = __shfl(tile.index, 16 * i + n);
-        if (t >= g.T || (index < 0 ? share > 0 : index % shares != share)) continue;
+        const int id = __shfl(tile.id, 16 * i + n);  // of many tokens all are taken on by one block, but for rare tiles
+        if (TT == 1 ? id != id0 : id == kNoToken) continue;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < J; ++j) {
           const int64_t at = t * N + (n0 + 16 * j < N ? n0 + 16 * j : N - 16) + 4 * hg;
           from[i][j] = *reinterpret_cast<const BaseRaw*>(static_cast<const char*>(base) + at * (BASE32 ? 4 : 2));
         }
@@ -271,8 +293,8 @@ __global__ __launch_bounds__(kWaves * 64) void lora_expand_kernel(LoraArgs g, co
   if constexpr (!MADE) {
     for (int e0 = 0; e0 < TOK * RANK / 4; e0 += kWaves * 64) {
       const int e = e0 + tid, t = e / (RANK / 4), r = e % (RANK / 4) * 4;
-      const int index = __shfl(tile.index, t & 63), id = __shfl(tile.id, t & 63);
-      if (t >= TOK || index < 0 || index % shares != share) continue;
+      const int id = __shfl(tile.id, t & 63);
+      if (t >= TOK || id != id0 || id < 0) continue;
       uint2 h[3];
       pieces4(g.ws + (t0 + t) * R + part * RANK + r, g.T * R, splits, g.scales ? g.scales[id] : 1.f, h);
 #pragma unroll
@@ -282,14 +304,13 @@ __global__ __launch_bounds__(kWaves * 64) void lora_expand_kernel(LoraArgs g, co
   }
   if (!mine) return;
 
-  auto columns = [&](auto keep, const f32x4_t (&acc)[TT][4]) {
+  auto columns = [&](int id, const f32x4_t (&acc)[TT][J]) {
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
       const int64_t t = t0 + 16 * i + n;
-      const int index = __shfl(tile.index, 16 * i + n);
-      if (t >= g.T || !keep(index)) continue;
+      if (__shfl(tile.id, 16 * i + n) != id) continue;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < J; ++j) {
         const int o = n0 + 16 * j + 4 * hg;
         const int64_t at = t * N + o;
         if constexpr (VEC) {
@@ -313,13 +334,18 @@ __global__ __launch_bounds__(kWaves * 64) void lora_expand_kernel(LoraArgs g, co
       }
     }
   };
-  f32x4_t acc[TT][4];
-  for (int at = share; at < tile.count; at += shares) {
-    if (at != share) weights_of(at, w);
+  f32x4_t acc[TT][J];
+  for (int turn = T::from(share); turn < tile.count; turn += shares) {
+    const int id = tile.at(turn);
+    if (turn != T::from(share) && id >= 0) weights_of(id, w);
 #pragma unroll
     for (int i = 0; i < TT; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < J; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    if (id < 0) {  // tokens without an adapter
+      if (base != y || BASE32 != OUT32) columns(id, acc);
+      continue;
+    }
 #pragma unroll
     for (int m = 0; m < E::kSteps; ++m) {
       const int c = 4 * m + hg, piece = c / E::kChunks, k8 = c % E::kChunks;
@@ -335,17 +361,10 @@ __global__ __launch_bounds__(kWaves * 64) void lora_expand_kernel(LoraArgs g, co
           }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = mma(w[j][m % E::kLoads], h, acc[i][j]);
+        for (int j = 0; j < J; ++j) acc[i][j] = mma(w[j][m % E::kLoads], h, acc[i][j]);
       }
     }
-    columns([&](int index) { return index == at; }, acc);
-  }
-  if (share == 0 && (base != y || BASE32 != OUT32)) {  // tokens without an adapter
-#pragma unroll
-    for (int i = 0; i < TT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    columns([&](int index) { return index < 0; }, acc);
+    columns(id, acc);
   }
 }
 
@@ -365,10 +384,10 @@ Plan plan_of(int64_t T, int64_t K, int64_t rank, int64_t n_parts) {
   p.row_groups = int(rows / p.rt);
   p.shares = many ? 4 : int(T < 16 ? T < 1 ? 1 : T : 16);
   const int64_t blocks = p.tiles * p.row_groups * (many ? 1 : p.shares), most = (K / 64 + kWaves - 1) / kWaves;
-  // blocks for every place of the GPU: 2 of a unit (many tokens, whose registers allow no more) or 4
-  int64_t s = blocks ? (many ? 2 : 4) * cus / blocks : 1;
+  // two blocks for each unit, whose waves' registers allow no more where tokens are many
+  int64_t s = blocks ? 2 * cus / blocks : 1;
   s = s > most ? most : s;
-  p.splits = int(s < 1 ? 1 : s > 64 ? 64 : s);
+  p.splits = int(s < 1 ? 1 : s > 16 ? 16 : s);
   return p;
 }
 
