@@ -36,6 +36,9 @@ __device__ __forceinline__ f32x4_t mma(u32x4_t a, u32x4_t b, f32x4_t c) {
 // straight code, but not where a loop's last product is stored to LDS behind the loop, inside
 // another loop (seen in its output, and as a register stored too early).
 __device__ __forceinline__ void mma_settle(f32x4_t& c) { asm volatile("s_nop 7\n\ts_nop 7" : "+v"(c)); }
+__device__ __forceinline__ void mma_settle(f32x4_t (&c)[4]) {
+  asm volatile("s_nop 7\n\ts_nop 7" : "+v"(c[0]), "+v"(c[1]), "+v"(c[2]), "+v"(c[3]));
+}
 
 // The adapters of a tile of up to 64 tokens, lane t having token t, and which of them a block (a share of the tile)
 // takes.  Of few tokens share i takes token i's adapter if no token in front has the same one; of
@@ -364,6 +367,8 @@ __global__ __launch_bounds__(kWaves * 64, TT == 1 && RANK <= 32 ? 4 : 2) void lo
         for (int j = 0; j < J; ++j) acc[i][j] = mma(w[j][m % E::kLoads], h, acc[i][j]);
       }
     }
+#pragma unroll
+    for (int i = 0; i < TT; ++i) mma_settle(acc[i]);
     columns(id, acc);
   }
 }
