@@ -3,16 +3,20 @@
 // Mathematics: h = A x, then y = base + s B h, with the adapter of each token.  Both products are
 // small (a rank of 8 to 128), so they are bound by the bytes of x, base, y and the adapters
 // in use; each adapter's weights are read once for a tile of tokens that use it.
-// Split.  Tokens go in tiles of 16 (few tokens) or 64 as they stand: a block finds the distinct
-// adapters of its tile and takes those of its share of them one after the other, each as a product of
+// Split.  Tokens go in tiles of 16 (up to 256 tokens in all) or, of more, of 64 to shrink and 32 to expand, as they
+// stand: a block finds the adapters of its tile and takes those that are its share, each as a product of
 // the adapter's weights with the whole tile, of which it keeps the columns of that adapter's tokens.
 // So nothing is sorted, requests that stand side by side share their weights' reads, and a
 // batch of many adapters is spread over blocks.
 //   shrink: weights' rows x tokens over a range of K; the block's waves take 64 inputs in turn and
 //     join in LDS; each range's sums go to the workspace.
-//   expand: adds the ranges' sums in order, times s, and takes them on as three bf16 pieces (24
-//     bits), which follow each other along the matrix product's k: for ranks up to 16 they fit
-//     in one or two instructions.  A lane ends with 16 neighbouring outputs of a token.
+//   join (more than 256 tokens): adds the ranges' sums in order, times s, and writes them as three bf16
+//     pieces (24 bits).  Of fewer tokens each expanding block does so itself: a launch costs more there.
+//   expand: the pieces follow each other along the matrix product's k: for ranks up to 16 they fit
+//     in one or two instructions.  A lane ends with 4 neighbouring outputs of a token, four lanes with 16.
+// Measured.  Rank 16, K 5120, parts of 5120, 1024 and 1024 rows: one token 8.0 us, 64 tokens of 48 adapters 19 us,
+// two launches, each of them one chain of loads.  Rank 64, K 13824, 5120 rows, 2211 tokens of prompts beside a fp32
+// projection: 126 us, of which shrinking 57 us, joining 5 us, expanding 64 us (183 MB, 2.9 TB/s).
 #include <hip/hip_runtime.h>
 
 #include "qmm_device.h"
@@ -78,9 +82,12 @@ template <int TT, int RT, int KS>
 __global__ __launch_bounds__(kWaves * 64, 2) void lora_shrink_kernel(LoraArgs g, int row_groups, int splits, int shares) {
   const int lane = threadIdx.x & 63, n = lane & 15, hg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int split = blockIdx.y % splits, share = blockIdx.y / splits;
-  const int64_t t0 = int64_t(blockIdx.x / row_groups) * (16 * TT);
-  const int R = g.n_parts * g.rank, r0 = int(blockIdx.x % row_groups) * (16 * RT);
+  // ranges of K side by side: with 8 of them each die, to which blocks go in turn, keeps its own range of the
+  // adapters' weights in its cache
+  const uint32_t block = blockIdx.x / uint32_t(splits);
+  const int split = int(blockIdx.x % uint32_t(splits)), share = blockIdx.y;
+  const int64_t t0 = int64_t(block / uint32_t(row_groups)) * (16 * TT);
+  const int R = g.n_parts * g.rank, r0 = int(block % uint32_t(row_groups)) * (16 * RT);
   using T = Tile<TT>;
   const T tile(g, t0, lane, share);
   if (T::from(share) >= tile.count) return;
@@ -112,48 +119,34 @@ __global__ __launch_bounds__(kWaves * 64, 2) void lora_shrink_kernel(LoraArgs g,
     for (int i = 0; i < TT; ++i)
 #pragma unroll
       for (int j = 0; j < RT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    // KS steps at a time, of many tokens the next ones' loads under way (of few a wave has no more than these);
-    // columns of other adapters are not read
-    constexpr int SETS = TT > 1 ? 2 : 1;
-    u32x4_t xv[SETS][KS][TT], av[SETS][KS][RT];
-    auto fetch = [&](int set, int q) {
+    // KS steps at a time: whole lines of 128 bytes; columns of other adapters are not read
+    u32x4_t xv[KS][TT], av[KS][RT];
+    auto fetch = [&](int q) {
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         const int at = input(q + k < steps ? q + k : steps - 1);  // behind the last step that one again, not used
 #pragma unroll
-        for (int i = 0; i < RT; ++i) av[set][k][i] = *reinterpret_cast<const u32x4_t*>(ap[i] + at);
+        for (int i = 0; i < RT; ++i) av[k][i] = *reinterpret_cast<const u32x4_t*>(ap[i] + at);
 #pragma unroll
         for (int i = 0; i < TT; ++i) {
-          xv[set][k][i] = u32x4_t{0, 0, 0, 0};
-          if (ids[i] == id) xv[set][k][i] = *reinterpret_cast<const u32x4_t*>(xp[i] + at);
+          xv[k][i] = u32x4_t{0, 0, 0, 0};
+          if (ids[i] == id) xv[k][i] = *reinterpret_cast<const u32x4_t*>(xp[i] + at);
         }
       }
     };
-    auto use = [&](int set, int q) {
+    auto use = [&](int q) {
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         if (q + k >= steps) continue;
 #pragma unroll
         for (int i = 0; i < TT; ++i)
 #pragma unroll
-          for (int j = 0; j < RT; ++j) acc[i][j] = mma(av[set][k][j], xv[set][k][i], acc[i][j]);
+          for (int j = 0; j < RT; ++j) acc[i][j] = mma(av[k][j], xv[k][i], acc[i][j]);
       }
     };
-    if constexpr (SETS == 1) {
-      for (int q = 0; q < steps; q += KS) {
-        fetch(0, q);
-        use(0, q);
-      }
-    } else if (steps > 0) {
-      fetch(0, 0);
-      for (int q = 0;;) {
-        if (q + KS < steps) fetch(1, q + KS);
-        use(0, q);
-        if ((q += KS) >= steps) break;
-        if (q + KS < steps) fetch(0, q + KS);
-        use(1, q);
-        if ((q += KS) >= steps) break;
-      }
+    for (int q = 0; q < steps; q += KS) {
+      fetch(q);
+      use(q);
     }
 #pragma unroll
     for (int i = 0; i < TT; ++i)
@@ -389,8 +382,10 @@ Plan plan_of(int64_t T, int64_t K, int64_t rank, int64_t n_parts) {
   p.row_groups = int(rows / p.rt);
   p.shares = many ? 4 : int(T < 16 ? T < 1 ? 1 : T : 16);
   const int64_t blocks = p.tiles * p.row_groups * (many ? 1 : p.shares), most = (K / 64 + kWaves - 1) / kWaves;
-  // two blocks for each unit, whose waves' registers allow no more where tokens are many
+  // Two blocks for each unit, whose registers hold no more where tokens are many.  There 8 or 16 ranges, a multiple
+  // of the dies, keep each die to its own ranges of the adapters' weights (8 ranges 126 us, 7 of them 130 us).
   int64_t s = blocks ? 2 * cus / blocks : 1;
+  if (many && s >= 6) s = s >= 12 ? 16 : 8;
   s = s > most ? most : s;
   p.splits = int(s < 1 ? 1 : s > 16 ? 16 : s);
   return p;
@@ -398,7 +393,7 @@ Plan plan_of(int64_t T, int64_t K, int64_t rank, int64_t n_parts) {
 
 template <int TT, int RT, int KS>
 void shrink_as(const LoraArgs& a, const Plan& p, hipStream_t s) {
-  lora_shrink_kernel<TT, RT, KS><<<dim3(uint32_t(p.tiles * p.row_groups), uint32_t(p.splits * p.shares)), kWaves * 64, 0,
+  lora_shrink_kernel<TT, RT, KS><<<dim3(uint32_t(p.tiles * p.row_groups * p.splits), uint32_t(p.shares)), kWaves * 64, 0,
                                s>>>(a, p.row_groups, p.splits, p.shares);
 }
 
@@ -467,7 +462,7 @@ int launch_lora(const LoraArgs& a, hipStream_t s) {
     shrink<1, 4>(a, p, s);
     expand<1>(a, p, s);
   } else {
-    shrink<4, 1>(a, p, s);
+    shrink<4, 2>(a, p, s);
     const int64_t n = (a.T * a.rank * a.n_parts / 4 + 255) / 256;
     lora_join_kernel<<<dim3(uint32_t(n)), 256, 0, s>>>(a, pieces_of(a, p), p.splits);
     expand<2>(a, p, s);
