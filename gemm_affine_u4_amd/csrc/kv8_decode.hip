@@ -15,6 +15,8 @@
 // that gets the scores of keys 8h .. 8h+7 of its column holds exactly the weights that the
 // second product wants from it: nothing crosses lanes between the two, and its eight keys
 // share their scales.
+// Measured (40 query and 8 KV heads of 128): 64 contexts of 100 to 16000 keys 174 us (5.6 TB/s), one of 517 keys
+// 9.8 us, most of it the chain from the table over keys and values to the join.
 #include <hip/hip_runtime.h>
 
 #include "kv8_attn.h"
@@ -39,7 +41,16 @@ struct Buf {
   float ks, vs;      // scales of the lane's keys (lane group's eight)
 };
 
-template <int HD, bool PG32, int NW>
+// A tile of codes, read once where a call's rows are one tile, so that it takes no cache from others; of several
+// row tiles' blocks, which run side by side, the later ones find it in the cache (64 sequences of 4000
+// keys, 4 heads x 128: 48 rows 133 -> 90 us; one row tile the other way, 64 long contexts: 184 -> 174 us).
+template <bool ONCE>
+__device__ __forceinline__ u32x4_t load_codes(const int8_t* p) {
+  if constexpr (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p));
+  else return *reinterpret_cast<const u32x4_t*>(p);
+}
+
+template <int HD, bool PG32, int NW, bool ONCE>
 __global__ __launch_bounds__(NW * 64, 2) void kv8_decode_kernel(Kv8AttnArgs g, int group, Attn8Plan plan) {
   using B = Buf<HD>;
   constexpr int NK = B::NK, NV = B::NV;
@@ -108,13 +119,12 @@ __global__ __launch_bounds__(NW * 64, 2) void kv8_decode_kernel(Kv8AttnArgs g, i
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int p = 0; p < NK; ++p)
-        x.k[u][p] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(kp + 4 * u * HD + 64 * p));
+      for (int p = 0; p < NK; ++p) x.k[u][p] = load_codes<ONCE>(kp + 4 * u * HD + 64 * p);
     x.ks = g.c.k_scale[rv >> 4];
     x.vs = g.c.v_scale[rv >> 4];
     const int8_t* vp = g.c.v_codes + rv * HD + 16 * n;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) x.v[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(vp + i * 256));
+    for (int i = 0; i < NV; ++i) x.v[i] = load_codes<ONCE>(vp + i * 256);
   };
 
   // Behind its last tile a wave loads that one again: were the loads conditional, the wait for
@@ -393,19 +403,19 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8AttnArgs g, int group,
   if (count > 1 && part == 0) attn_store4(g, row * HD + d, o, l);
 }
 
-template <int HD>
-int launch_hd(const Kv8AttnArgs& a, const Attn8Plan& p, hipStream_t s) {
+template <int HD, bool PG32, int NW>
+int launch_nw(const Kv8AttnArgs& a, const Attn8Plan& p, hipStream_t s) {
   const int group = a.n_q / a.c.n_kv;
   const int64_t rts = (int64_t(a.max_q) * group + 15) / 16;
   const dim3 grid(uint32_t(p.nsplit), uint32_t(a.c.n_kv * rts), uint32_t(a.B));
-  if (p.waves == 8) {
-    if (a.c.page_shift >= 5) kv8_decode_kernel<HD, true, 8><<<grid, 512, 0, s>>>(a, group, p);
-    else kv8_decode_kernel<HD, false, 8><<<grid, 512, 0, s>>>(a, group, p);
-  } else {
-    if (a.c.page_shift >= 5) kv8_decode_kernel<HD, true, 4><<<grid, 256, 0, s>>>(a, group, p);
-    else kv8_decode_kernel<HD, false, 4><<<grid, 256, 0, s>>>(a, group, p);
-  }
+  if (rts == 1) kv8_decode_kernel<HD, PG32, NW, true><<<grid, NW * 64, 0, s>>>(a, group, p);
+  else kv8_decode_kernel<HD, PG32, NW, false><<<grid, NW * 64, 0, s>>>(a, group, p);
   return hipGetLastError() == hipSuccess ? 0 : 6;
+}
+template <int HD>
+int launch_hd(const Kv8AttnArgs& a, const Attn8Plan& p, hipStream_t s) {
+  if (a.c.page_shift >= 5) return p.waves == 8 ? launch_nw<HD, true, 8>(a, p, s) : launch_nw<HD, true, 4>(a, p, s);
+  return p.waves == 8 ? launch_nw<HD, false, 8>(a, p, s) : launch_nw<HD, false, 4>(a, p, s);
 }
 
 template <int HD>
@@ -420,8 +430,17 @@ int join_hd(const Kv8AttnArgs& a, const Attn8Plan& p, hipStream_t s) {
   return hipGetLastError() == hipSuccess ? 0 : 6;
 }
 
-// Calls of up to this many rows per KV head run here, others as prompts.
-constexpr int64_t decode_rows(int64_t hd) { return hd == 256 ? 64 : 128; }
+// Which calls run here, others as prompts: those of few rows for each KV head, whose prompt blocks would be mostly empty,
+// and those of few row tiles in all, which as prompts would be few blocks.  Here and as prompts, us, contexts of 4000,
+// 4 KV heads a sequence:
+//   64 sequences x 128 dims   96 rows 145, 155   128 rows 184, 158
+//   16 sequences x 256 dims   30 rows 44, 54     48 rows 64, 59
+//    4 sequences x 256 dims  128 rows 43, 47    192 rows 61, 48
+//    4 sequences x 128 dims  256 rows 39, 47
+bool few_rows(int64_t rows, int64_t heads, int64_t hd) {
+  return rows <= (hd == 256 ? 16 : hd == 128 ? 96 : 128) ||
+         (rows <= 256 && (rows + 15) / 16 * heads <= (hd == 256 ? 128 : 256));
+}
 
 }  // namespace
 
@@ -432,7 +451,7 @@ Attn8Plan attn8_plan(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_
   int64_t seen = max_kv;
   if (window > 0 && window + max_q + sinks + 64 < max_kv) seen = window + max_q + sinks + 64;
   Attn8Plan p;
-  p.rows = rows <= decode_rows(hd) ? 16 : attn8_rows(hd);
+  p.rows = few_rows(rows, B * n_kv, hd) ? 16 : attn8_rows(hd);
   const int64_t blocks = B * n_kv * ((rows + p.rows - 1) / p.rows);
   int64_t ns;
   if (p.rows != 16) {
