@@ -97,8 +97,8 @@ int qmm_kv8_append(const qmm_kv8_cache* cache, const void* k, const void* v, int
  *   gate (nullable) [T][n_q_heads][head_dim] bf16: out is multiplied by 1 / (1 + exp(-gate)).
  * Scores, sums, maxima and the softmax are fp32, from exact codes and queries (of a query row,
  * values below 2^-24 of its largest lose digits).  A key's weight times its values' scale is rounded to
- * fp16: 2^-11 of it; where it is small, for few queries (up to 128 rows = queries x heads of a group, 64 at
- * head_dim 256) 2^-39 of the largest scale, for prompts 2^-36 of the row's largest such product.
+ * fp16: 2^-11 of it; where it is small, 2^-39 of the largest scale for few queries (up to 16 rows = max_q x heads of
+ * a group), 2^-36 of the row's largest such product for prompts (more than 256 rows), between them one of the two.
  * workspace: 256-byte aligned, at least qmm_kv8_attn_workspace_bytes of the same T, B, max_q,
  * heads, max_kv = max_pages * page_size, window and sinks (0 for sizes out of range; always > 0
  * otherwise).

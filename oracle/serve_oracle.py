@@ -98,7 +98,7 @@ def attention(q, cache, table, kv_len, q_len, scale, causal=True, window=0, sink
     rounding of p s, 2^-11 of W = sum p |v|, and where p s is below fp16's normal range its steps of 2^-24, half of one
     a key times codes up to 127: for few queries p s is held times 8 with the largest scale s at 2^11 or more, so
     that is 2^-25 / 2^14 = 2^-39 of the largest scale; for prompts with the row's largest p s at 2^11 or more, 2^-36 of
-    that; and the scores' error d (fp32 sums of hd + 8 terms, M = scale sum |q k|), which changes each
+    that (few = None: the larger of the two); and the scores' error d (fp32 sums of hd + 8 terms, M = scale sum |q k|), which changes each
     p by at most a factor e^(2 d) once normalised: (e^(2 d) - 1) W.  The hardware's exp2 (2^-22) and the
     normalising sum (2^-20) sit in the 2^-18 added to the relative part."""
     n_q, hd = q.shape[1], q.shape[2]
@@ -127,7 +127,9 @@ def attention(q, cache, table, kv_len, q_len, scale, causal=True, window=0, sink
             p /= p.sum(1, keepdims=True)
             o, w = p @ v, p @ np.abs(v)
             d = np.where(see[some], scale * (np.abs(x) @ np.abs(k).T), 0).max(1, keepdims=True) * (hd + 8) * 2.0 ** -24
-            low = 2.0 ** -39 * vs.max() if few else 2.0 ** -36 * (p * vs).max(1, keepdims=True)
+            low = 2.0 ** -36 * (p * vs).max(1, keepdims=True)
+            if few or few is None:
+                low = np.maximum(0 if few else low, 2.0 ** -39 * vs.max())
             e = w * (2.0 ** -11 + 2.0 ** -18 + np.expm1(2 * d)) + len(t) * 127 * low
             if gate is not None:
                 sig = 1 / (1 + np.exp(-gate[some, a]))

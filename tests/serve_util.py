@@ -48,3 +48,8 @@ def filled(rng, kv_lens, n_kv, hd, page, spare=2, scale_k=1.0, scale_v=1.0):
         if n:
             c.append(table[b], n, k, v)
     return c, table
+
+
+def few_rows(rows):
+    """The form that attention of so many rows per KV head takes: of few queries, prompts', or (None) either."""
+    return True if rows <= 16 else None if rows <= 256 else False

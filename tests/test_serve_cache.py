@@ -7,7 +7,7 @@ import gemm_affine_u4_amd as qmm
 from oracle import mix_oracle as mix
 from oracle import serve_oracle as srv
 from tests.gpu_util import Guarded, assert_within, bf16_bits_to_f64, dev, say
-from tests.serve_util import angles, bf16, filled, gpu_cache, ints, tables
+from tests.serve_util import angles, bf16, few_rows, filled, gpu_cache, ints, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -190,7 +190,7 @@ def check_attention(rng, q_lens, kv_lens, n_q, n_kv, hd, page, window=0, sinks=0
             continue
         ref, tol = srv.attention(qv[starts[b]:starts[b + 1]], c, table[b], kv, n, hd ** -0.5, causal, window, sinks,
                                  gv[starts[b]:starts[b + 1]] if gated else None,
-                                 few=max_q * n_q // n_kv <= (64 if hd == 256 else 128))
+                                 few=few_rows(max_q * n_q // n_kv))
         assert_within(got[starts[b]:starts[b] + m], ref[:m], tol[:m], f"{what} sequence {b} q {n} kv {kv}")
     return got_bits
 
@@ -382,10 +382,12 @@ def test_a_very_long_context(n):
 
 
 @pytest.mark.parametrize("hd,rows", [(64, 128), (64, 129), (128, 128), (128, 129), (256, 64), (256, 65), (128, 16),
-                                     (128, 17), (128, 33), (64, 65)])
+                                     (128, 17), (128, 33), (64, 65), (64, 256), (128, 257), (256, 255), (128, 96),
+                                     (128, 97), (256, 17)])
 def test_attention_where_the_kernels_meet(hd, rows):
     rng = np.random.default_rng([44, hd, rows])
     check_attention(rng, [rows, 5], [rows + 140, 70], 1, 1, hd, 16, gated=True)
+    check_attention(rng, [rows, 3], [rows + 77, 130], 40, 40, hd, 32)
     check_attention(rng, [rows], [rows - 9], 2, 2, hd, 32, window=50)
 
 
@@ -440,7 +442,7 @@ def test_a_cache_past_32_bit_offsets():
                          device="cuda")
         qmm.qmm_kv8_attn(dev(qb[first:]), g, dev(table), ints(n), out.t, ws, q_start=ints(0, m), max_q=m)
         torch.cuda.synchronize()
-        ref, tol = srv.attention(qv[first:], c, [1, 0], n, m, hd ** -0.5, few=m == 1)
+        ref, tol = srv.attention(qv[first:], c, [1, 0], n, m, hd ** -0.5, few=few_rows(m * n_q // n_kv))
         assert_within(bf16_bits_to_f64(out.values()), ref, tol, f"{m} queries")
 
 

@@ -66,6 +66,15 @@ def test_batches(V, probs, half):
         assert acc.max() > 0
 
 
+@pytest.mark.parametrize("V", [16383, 16384, 16385, 24576])
+@pytest.mark.parametrize("half", [False, True])
+def test_where_rows_take_two_launches(V, half):
+    rng = np.random.default_rng([9, V, half])
+    for at in (0, 3):
+        check(rng, [2, 0, 4, 1], V, True, half, at=at)
+        check(rng, [1, 3], V, False, half, at=at)
+
+
 def test_many_sequences_and_a_long_draft():
     rng = np.random.default_rng(1)
     tokens, acc = check(rng, rng.integers(0, 5, 300).tolist(), 500, True, False)
