@@ -56,9 +56,9 @@ __global__ __launch_bounds__(NW * 64, 2) void kv8_decode_kernel(Kv8AttnArgs g, i
   constexpr int NK = B::NK, NV = B::NV;
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, hg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int split = blockIdx.x;
+  const int split = attn8_split(plan);
   int b = blockIdx.z;
-  const int kvh = blockIdx.y % g.c.n_kv, rt = blockIdx.y / g.c.n_kv;
+  const int kvh = blockIdx.x, rt = blockIdx.y / plan.nsplit;
 
   const AttnSeq sq = attn_longest_first(g, b, lane);
   const int row0 = rt * 16, rows = sq.q_len * group - row0;
@@ -407,7 +407,7 @@ template <int HD, bool PG32, int NW>
 int launch_nw(const Kv8AttnArgs& a, const Attn8Plan& p, hipStream_t s) {
   const int group = a.n_q / a.c.n_kv;
   const int64_t rts = (int64_t(a.max_q) * group + 15) / 16;
-  const dim3 grid(uint32_t(p.nsplit), uint32_t(a.c.n_kv * rts), uint32_t(a.B));
+  const dim3 grid(uint32_t(a.c.n_kv), uint32_t(p.nsplit * rts), uint32_t(a.B));
   if (rts == 1) kv8_decode_kernel<HD, PG32, NW, true><<<grid, NW * 64, 0, s>>>(a, group, p);
   else kv8_decode_kernel<HD, PG32, NW, false><<<grid, NW * 64, 0, s>>>(a, group, p);
   return hipGetLastError() == hipSuccess ? 0 : 6;
@@ -462,8 +462,10 @@ Attn8Plan attn8_plan(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_
     p.nsplit = int(ns > 256 ? 256 : ns < 1 ? 1 : ns);
     return p;
   }
+  // Contexts are often much shorter than the table: few sequences are split however short (16 contexts of 1000 keys in
+  // tables of 16384, 8 heads x 128: 22.4 -> 15.4 us), many fill the GPU anyhow.
   p.shift = 5, p.keys = 1024;
-  while (p.keys > 128 && blocks * ((seen + p.keys - 1) / p.keys) <= cus / 2) p.keys /= 2;
+  while (p.keys > 128 && blocks * 1024 / p.keys < 2 * cus) p.keys /= 2;
   ns = 8 * cus / blocks < 4 ? 8 * cus / blocks : 4;
   if (ns < cus / blocks) ns = cus / blocks;
   if (seen <= 768 || seen <= 2 * p.keys) ns = 1;

@@ -61,9 +61,9 @@ __global__ __launch_bounds__(NW * 64, 1) void kv8_prefill_kernel(Kv8AttnArgs g, 
   constexpr int ROWS = NW * 32 * CT, OT = HD / 32, NS = HD / 16, NV = 2 * OT, PER = HD / 64;
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, hh = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int split = blockIdx.x;
+  const int split = attn8_split(plan);
   int b = blockIdx.z;
-  const int kvh = blockIdx.y % g.c.n_kv, rt = tiles - 1 - int(blockIdx.y) / g.c.n_kv;  // longest rows first
+  const int kvh = blockIdx.x, rt = tiles - 1 - int(blockIdx.y) / plan.nsplit;  // longest rows first
 
   const AttnSeq sq = attn_longest_first(g, b, lane);
   const int row0 = rt * ROWS, rows = sq.q_len * group - row0;
@@ -488,7 +488,7 @@ template <int HD>
 int launch(const Kv8AttnArgs& a, const Attn8Plan& p, hipStream_t s) {
   const int group = a.n_q / a.c.n_kv, tiles = int((int64_t(a.max_q) * group + p.rows - 1) / p.rows);
   kv8_prefill_kernel<HD>
-      <<<dim3(uint32_t(p.nsplit), uint32_t(a.c.n_kv * tiles), uint32_t(a.B)), NW * 64, 0, s>>>(a, group, p, tiles);
+      <<<dim3(uint32_t(a.c.n_kv), uint32_t(p.nsplit * tiles), uint32_t(a.B)), NW * 64, 0, s>>>(a, group, p, tiles);
   return hipGetLastError() == hipSuccess ? 0 : 6;
 }
 
