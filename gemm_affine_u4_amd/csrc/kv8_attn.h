@@ -15,7 +15,7 @@ struct Attn8Plan {
   int nsplit;  // at most this many splits of a block's keys ...
   int keys;    // ... of at least this many keys
 };
-constexpr int attn8_rows(int64_t hd) { return hd == 256 ? 128 : 256; }
+constexpr int attn8_rows(int64_t hd) { return hd == 128 ? 256 : 128; }
 Attn8Plan attn8_plan(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_t hd, int64_t max_kv, int64_t window,
                      int64_t sinks);
 

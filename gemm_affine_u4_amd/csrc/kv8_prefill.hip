@@ -12,11 +12,16 @@
 // matrix cores.
 //
 // Split.  A block of 4 waves takes (query, head) rows of one KV head (the heads of a group share the
-// tile) and walks the keys 64 at a time, in two steps of 32.  A wave keeps 64 rows (32 at 256 dims,
-// where registers end), their queries as operands and their outputs in registers: each LDS operand
-// serves two products, as reading it takes as long as one.  Keys and dims are the rows of the products,
+// tile) and walks the keys 64 at a time, in two steps of 32.  A wave keeps 64 rows at 128 dims, their queries as
+// operands and their outputs in registers: each LDS operand serves two products, as reading it takes as long as
+// one.  At 256 dims registers end at 32 rows; at 64 dims 32 rows leave room for two blocks a unit, which fill each
+// other's waits (four prompts of 2000 over 6000 keys, 14 / 2 heads: 315 us with 64 rows, 266).  Keys and dims are the rows of the products,
 // so that a lane's scores are its share of the next operand.  A step is ordered by hand: a wave issues
 // in order, so vector work is placed between matrix instructions, beside which it runs.
+// Measured: 806, 640 and 858 TFLOP/s at 128, 64 and 256 dims where blocks fill the GPU evenly (without the codes'
+// conversion 952 at 128 dims, without barriers 872).  Four ragged chunks of prompts behind 1500 to 8000 keys (40 / 8
+// heads x 128): 278 us, 655 TFLOP/s, a fifth of it waiting for the longest blocks; cutting those by
+// keys cost more than it brought (286 to 337 us), and so did blocks of 128 rows (355 us).
 #include <hip/hip_runtime.h>
 
 #include "kv8_attn.h"
@@ -56,8 +61,8 @@ constexpr int kRowK = HD + 8;
 constexpr int kRowV = kKeys + 8;
 
 template <int HD>
-__global__ __launch_bounds__(NW * 64, 1) void kv8_prefill_kernel(Kv8AttnArgs g, int group, Attn8Plan plan, int tiles) {
-  constexpr int CT = HD == 256 ? 1 : 2;  // column tiles of 32 rows
+__global__ __launch_bounds__(NW * 64, HD == 64 ? 2 : 1) void kv8_prefill_kernel(Kv8AttnArgs g, int group, Attn8Plan plan, int tiles) {
+  constexpr int CT = HD == 128 ? 2 : 1;  // column tiles of 32 rows
   constexpr int ROWS = NW * 32 * CT, OT = HD / 32, NS = HD / 16, NV = 2 * OT, PER = HD / 64;
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 31, hh = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
