@@ -145,8 +145,8 @@ __global__ __launch_bounds__(NW * 64, 2) void kv8_decode_kernel(Kv8AttnArgs g, i
   const int cj = (row0 + n) / group, ch = kvh * group + (row0 + n) % group;
   const int64_t qrow = (int64_t(sq.q0) + cj) * g.n_q + ch;
   int c_lo = 0, c_hi = sq.kv_len;
-  if (col_ok && g.causal) {
-    const int64_t p = int64_t(sq.first) + cj;
+  if (g.causal) {  // columns without a row see what the last row does
+    const int64_t p = int64_t(sq.first) + (row0 + (col_ok ? n : rows - 1)) / group;
     c_hi = p < 0 ? 0 : int(p) + 1;
     c_lo = g.window > 0 && p - g.window + 1 > 0 ? int(p - g.window + 1) : 0;
   }
@@ -207,8 +207,6 @@ __global__ __launch_bounds__(NW * 64, 2) void kv8_decode_kernel(Kv8AttnArgs g, i
     const bool masked = w.key + kTile > u_hi || (w.key < u_lo && w.key + kTile > sinks) || !w.ok0 || !w.ok1;
     const int tb = w.key + 8 * hg;
     float vs = x.vs;
-    // keys that are not there may have any scale, NaN among them
-    if (masked) vs = (hg < 2 ? w.ok0 : w.ok1) && tb < sq.kv_len ? vs : 0.f;
     float sc[8];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -231,6 +229,7 @@ __global__ __launch_bounds__(NW * 64, 2) void kv8_decode_kernel(Kv8AttnArgs g, i
         vis |= see ? 1u << i : 0u;
         sc[i] = see ? sc[i] : -INFINITY;
       }
+      if (!vis) vs = 0.f;  // keys that are not there, or not seen any more, may have any scale, NaN among them
     }
     float mx = fmaxf(fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])), fmaxf(fmaxf(sc[4], sc[5]), fmaxf(sc[6], sc[7])));
     if (__any(mx > m || vs >= vtop)) {

@@ -64,7 +64,7 @@ typedef struct qmm_kv8_cache {
  * anew: scale = need.  Otherwise it holds earlier keys: its scale stays if need is not above it,
  * else it becomes the larger of need and 1.25 scale, and the codes of the earlier keys
  * become rint(c * (old scale / new scale)).  c = rint(x * (1/scale)) clamped to +-127 (0 where the
- * scale is 0).  A scale that grows, grows by a quarter: so the roundings of a key whose block
+ * scale is not above 2^-127).  A scale that grows, grows by a quarter: so the roundings of a key whose block
  * fills token by token add up to 2.5 steps at most.  Slots of a block behind its last key hold any codes.
  * T and max_q up to 2^24, B up to 65535, B * (max_q / 16 + 2) below 2^26.
  */

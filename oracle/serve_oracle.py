@@ -57,8 +57,8 @@ class Cache:
                 with np.errstate(invalid="ignore"):
                     s = need if begins else np.where(need <= old, old, np.maximum(need, old * np.float32(1.25)))
                 s = s.astype(np.float32)
-                with np.errstate(divide="ignore", invalid="ignore"):
-                    inv = np.where(s > 0, np.float32(1) / s, np.float32(0)).astype(np.float32)
+                with np.errstate(divide="ignore", invalid="ignore", over="ignore"):
+                    inv = np.where(s > np.float32(2.0 ** -127), np.float32(1) / s, np.float32(0)).astype(np.float32)
                     ratio = (old / s).astype(np.float32)
                 for h in range(self.n_kv):
                     if not begins and s[h] != old[h]:

@@ -134,6 +134,38 @@ def test_append_positions_default_to_places():
         assert torch.equal(x, y)
 
 
+def test_append_of_the_smallest_values():
+    """Blocks whose scale has no finite reciprocal hold zeros; just above that, and beside larger ones, they do not."""
+    rng = np.random.default_rng(8)
+    n, n_kv, hd, page = 33, 5, 128, 16
+    k, v = (rng.standard_normal((n, n_kv, hd)).astype(np.float32) for _ in range(2))
+    for h, s in enumerate((1e-40, 1e-37, 1e-35, 1.0, 0.0)):
+        k[:, h] *= np.float32(s)
+        v[:, h] *= np.float32(s)
+    table, pages = tables(rng, [n], page)
+    c = srv.Cache(pages, n_kv, page, hd, rng)
+    g = gpu_cache(c)
+    qmm.qmm_kv8_append(g, dev(k), dev(v), dev(table), ints(n), q_start=ints(0, n), max_q=n)
+    torch.cuda.synchronize()
+    c.append(table[0], n, k, v)
+    same_cache(c, g, table, [n])
+
+
+def test_append_with_a_max_q_far_above_the_tokens():
+    rng = np.random.default_rng(9)
+    n_kv, hd, page, B = 8, 64, 16, 60
+    table, pages = tables(rng, [3] * B, page)
+    c = srv.Cache(pages, n_kv, page, hd, rng)
+    g = gpu_cache(c)
+    k, v = (rng.standard_normal((3 * B, n_kv, hd)).astype(np.float32) for _ in range(2))
+    qmm.qmm_kv8_append(g, dev(k), dev(v), dev(table), dev(np.full(B, 3, np.int32)),
+                       q_start=dev(np.arange(B + 1, dtype=np.int32) * 3), max_q=1 << 22)
+    torch.cuda.synchronize()
+    for b in range(B):
+        c.append(table[b], 3, k[3 * b:3 * b + 3], v[3 * b:3 * b + 3])
+    same_cache(c, g, table, [3] * B)
+
+
 def test_append_token_by_token_then_take_back():
     """Blocks that fill token by token, drafts taken back by a shorter length and written over."""
     rng = np.random.default_rng(7)
@@ -444,6 +476,38 @@ def test_a_cache_past_32_bit_offsets():
         torch.cuda.synchronize()
         ref, tol = srv.attention(qv[first:], c, [1, 0], n, m, hd ** -0.5, few=few_rows(m * n_q // n_kv))
         assert_within(bf16_bits_to_f64(out.values()), ref, tol, f"{m} queries")
+
+
+@pytest.mark.parametrize("q_len", [1, 4, 40])
+@pytest.mark.parametrize("hd,bad", [(128, np.nan), (128, 1e30), (256, np.nan), (64, np.inf)])
+def test_blocks_behind_the_window_may_have_any_scale(q_len, hd, bad):
+    """A server may have given pages away that no row sees any more, while the table still names them."""
+    rng = np.random.default_rng([49, q_len, hd])
+    for kv, window, sinks in ((300, 60, 0), (300, 47, 5), (97, 33, 16)):
+        c, table = filled(rng, [kv], 2, hd, 16)
+        want = check_attention(rng, [q_len], [kv], 8, 2, hd, 16, window=window, sinks=sinks, c=c, table=table)
+        for t in range(-(-sinks // 16), (kv - q_len - window + 1) // 16):
+            c.k_scale[table[0, t]] = c.v_scale[table[0, t]] = bad
+        out = bf16_bits_to_f64(check_given_away(rng, q_len, kv, hd, window, sinks, c, table))
+        assert np.all(np.isfinite(out))
+
+
+def check_given_away(rng, q_len, kv, hd, window, sinks, c, table):
+    """Outputs with those blocks' scales as they are and with ones: the same bits."""
+    qb, _ = bf16(rng.standard_normal((q_len, 8, hd)))
+    got = []
+    for clean in (False, True):
+        if clean:
+            for s in (c.k_scale, c.v_scale):
+                s[~(np.abs(s) < 1e20)] = 1.0
+        out = torch.empty(q_len, 8, hd, dtype=torch.bfloat16, device="cuda")
+        need = qmm.qmm_kv8_attn_workspace_bytes(q_len, 1, q_len, 8, 2, hd, table.shape[1] * 16, window, sinks)
+        qmm.qmm_kv8_attn(dev(qb), gpu_cache(c), dev(table), ints(kv), out, torch.empty(need, dtype=torch.uint8, device="cuda"),
+                         q_start=ints(0, q_len), max_q=q_len, window=window, sinks=sinks)
+        torch.cuda.synchronize()
+        got.append(out.view(torch.int16).cpu().numpy().view(np.uint16))
+    assert np.array_equal(got[0], got[1])
+    return got[0]
 
 
 def test_two_sequences_share_their_first_pages():
