@@ -15,8 +15,8 @@
 //   expand: the pieces follow each other along the matrix product's k: for ranks up to 16 they fit
 //     in one or two instructions.  A lane ends with 4 neighbouring outputs of a token, four lanes with 16.
 // Measured.  Rank 16, K 5120, parts of 5120, 1024 and 1024 rows: one token 8.0 us, 64 tokens of 48 adapters 19 us,
-// two launches, each of them one chain of loads.  Rank 64, K 13824, 5120 rows, 2211 tokens of prompts beside a fp32
-// projection: 126 us, of which shrinking 57 us, joining 5 us, expanding 64 us (183 MB, 2.9 TB/s).
+// two launches, each of them one chain of loads.  Rank 64, K 13824, 5120 rows, 4464 tokens of prompts beside a fp32
+// projection: 121 us, of which shrinking 56 us, joining 5 us, expanding 61 us (183 MB, 3.0 TB/s).
 #include <hip/hip_runtime.h>
 
 #include "qmm_device.h"
@@ -371,7 +371,9 @@ struct Plan {
   int tt, rt, row_groups, splits, shares;  // column and row tiles of a shrinking block; shares of a tile's adapters
   int64_t tiles;
 };
-constexpr int kMany = 256;  // tokens: from here on tiles are larger, and h is joined by a launch of its own
+// Tokens from which on tiles are larger, and h is joined by a launch of its own.  300 tokens of prompts of 100 so 18 and
+// 22 us (rank 16 and 64), as few 31 and 37; 300 of as many requests 72 and 65, as few 54 and 69.
+constexpr int kMany = 256;
 Plan plan_of(int64_t T, int64_t K, int64_t rank, int64_t n_parts) {
   Plan p;
   const int64_t rows = (rank * n_parts + 15) / 16, cus = device_cus();
@@ -380,7 +382,9 @@ Plan plan_of(int64_t T, int64_t K, int64_t rank, int64_t n_parts) {
   p.rt = rows % 4 == 0 ? 4 : rows % 3 == 0 ? 3 : rows % 2 == 0 ? 2 : 1;
   p.tiles = (T + 16 * p.tt - 1) / (16 * p.tt);
   p.row_groups = int(rows / p.rt);
-  p.shares = many ? 4 : int(T < 16 ? T < 1 ? 1 : T : 16);
+  // of tiles' adapters: blocks without one cost a start (4464 tokens of 5 prompts: 4 shares 126 us, one 121), but a tile's
+  // adapters in turn take long where tiles are few (1000 tokens, each its own: 146 and 192 us; 4000: 510 and 471)
+  p.shares = !many ? int(T < 16 ? T < 1 ? 1 : T : 16) : T > 2048 ? 1 : 4;
   const int64_t blocks = p.tiles * p.row_groups * (many ? 1 : p.shares), most = (K / 64 + kWaves - 1) / kWaves;
   // Two blocks for each unit, whose registers hold no more where tokens are many.  There 8 or 16 ranges, a multiple
   // of the dies, keep each die to its own ranges of the adapters' weights (8 ranges 126 us, 7 of them 130 us).

@@ -91,6 +91,15 @@ def test_prompts(rank, rows, T):
     check(rng, rng.integers(0, 40, T), 40, rank, 128, rows, False, False)
 
 
+@pytest.mark.parametrize("rank,T", [(16, 2048), (16, 2049), (64, 2500), (8, 2111)])
+def test_thousands_of_tokens_of_mixed_adapters(rank, T):
+    rng = np.random.default_rng([31, rank, T])
+    runs = rng.integers(1, 90, T)
+    ids = np.repeat(rng.integers(-1, 41, T), runs)[:T]
+    check(rng, ids, 40, rank, 256, [272, 40], True, False, rows_checked=80)
+    check(rng, rng.integers(-1, 41, T), 40, rank, 192, [96], False, True, rows_checked=80)
+
+
 def test_long_inputs_and_every_tile_full_of_adapters():
     rng = np.random.default_rng(6)
     check(rng, np.arange(64), 64, 16, 13824, [96], True, True, rows_checked=8)
