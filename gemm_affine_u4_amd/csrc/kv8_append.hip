@@ -97,7 +97,8 @@ __device__ __forceinline__ uint32_t recode(uint32_t byte, float ratio) {
 
 // VEC: rot a multiple of 16, a lane's dims are two runs of 8 that pair up; otherwise 16 neighbours.
 template <int HD, bool F32, bool VEC>
-__global__ __launch_bounds__(256, HD == 256 && VEC ? 3 : 2) void kv8_append_kernel(Kv8AppendArgs g, int blocks, int groups, int per_wave) {
+__global__ __launch_bounds__(256, HD == 256 && VEC ? 3 : 2) void kv8_append_kernel(Kv8AppendArgs g, int blocks,
+                                                                                   int groups, int per_wave) {
   constexpr int LPT = HD / 16, PPT = 64 / LPT, PASSES = kBlock / PPT;  // lanes of a token, tokens of a pass
   const int lane = threadIdx.x & 63;
   const uint32_t wid = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -105,7 +106,8 @@ __global__ __launch_bounds__(256, HD == 256 && VEC ? 3 : 2) void kv8_append_kern
   const int b = int(unit / uint32_t(blocks));
   if (b >= g.B) return;
   const AttnSeq sq = attn_seq(g, b);
-  const int64_t k0 = ((int64_t(sq.first) >> 4) + unit % uint32_t(blocks)) * kBlock;  // the block's first key (it may lie below 0)
+  // the block's first key (it may lie below 0)
+  const int64_t k0 = ((int64_t(sq.first) >> 4) + unit % uint32_t(blocks)) * kBlock;
   const int64_t end = int64_t(sq.first) + sq.q_len;
   const int lo = int(sq.first > k0 ? sq.first - k0 : 0), hi = int(end < k0 + kBlock ? end - k0 : kBlock);
   if (lo >= hi) return;

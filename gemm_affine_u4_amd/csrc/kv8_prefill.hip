@@ -15,7 +15,8 @@
 // tile) and walks the keys 64 at a time, in two steps of 32.  A wave keeps 64 rows at 128 dims, their queries as
 // operands and their outputs in registers: each LDS operand serves two products, as reading it takes as long as
 // one.  At 256 dims registers end at 32 rows; at 64 dims 32 rows leave room for two blocks a unit, which fill each
-// other's waits (four prompts of 2000 over 6000 keys, 14 / 2 heads: 315 us with 64 rows, 266).  Keys and dims are the rows of the products,
+// other's waits (four prompts of 2000 over 6000 keys, 14 / 2 heads: 315 us with 64 rows, 266).  Keys and dims are the
+// rows of the products,
 // so that a lane's scores are its share of the next operand.  A step is ordered by hand: a wave issues
 // in order, so vector work is placed between matrix instructions, beside which it runs.
 // Measured: 806, 640 and 858 TFLOP/s at 128, 64 and 256 dims where blocks fill the GPU evenly (without the codes'

@@ -79,7 +79,8 @@ struct Tile {
 
 // TT column tiles of 16 tokens, RT row tiles of 16 ranks, KS steps of 32 inputs at a time.
 template <int TT, int RT, int KS>
-__global__ __launch_bounds__(kWaves * 64, 2) void lora_shrink_kernel(LoraArgs g, int row_groups, int splits, int shares) {
+__global__ __launch_bounds__(kWaves * 64, 2) void lora_shrink_kernel(LoraArgs g, int row_groups, int splits,
+                                                                     int shares) {
   const int lane = threadIdx.x & 63, n = lane & 15, hg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // ranges of K side by side: with 8 of them each die, to which blocks go in turn, keeps its own range of the
@@ -223,8 +224,8 @@ __global__ __launch_bounds__(256) void lora_join_kernel(LoraArgs g, uint16_t* to
 // VEC: every part's rows are a multiple of 16 and its arrays 16-byte aligned.
 // pieces: bf16 [3][T][R] where they were made by the launch before, else made here, in LDS.
 template <int TT, int RANK, bool BASE32, bool OUT32, bool VEC>
-__global__ __launch_bounds__(kWaves * 64, TT == 1 && RANK <= 32 ? 4 : 2) void lora_expand_kernel(LoraArgs g, const uint16_t* pieces, int row_chunks,
-                                                                  int splits, int shares) {
+__global__ __launch_bounds__(kWaves * 64, TT == 1 && RANK <= 32 ? 4 : 2) void lora_expand_kernel(
+    LoraArgs g, const uint16_t* pieces, int row_chunks, int splits, int shares) {
   using E = Expand<RANK>;
   constexpr int TOK = 16 * TT, ROW = RANK + 8;  // bf16 of a token's piece in LDS, 16 bytes of pad
   constexpr bool MADE = TT > 1;
@@ -397,8 +398,8 @@ Plan plan_of(int64_t T, int64_t K, int64_t rank, int64_t n_parts) {
 
 template <int TT, int RT, int KS>
 void shrink_as(const LoraArgs& a, const Plan& p, hipStream_t s) {
-  lora_shrink_kernel<TT, RT, KS><<<dim3(uint32_t(p.tiles * p.row_groups * p.splits), uint32_t(p.shares)), kWaves * 64, 0,
-                               s>>>(a, p.row_groups, p.splits, p.shares);
+  const dim3 grid(uint32_t(p.tiles * p.row_groups * p.splits), uint32_t(p.shares));
+  lora_shrink_kernel<TT, RT, KS><<<grid, kWaves * 64, 0, s>>>(a, p.row_groups, p.splits, p.shares);
 }
 
 template <int TT, int KS>
