@@ -16,7 +16,7 @@
 //     in one or two instructions.  A lane ends with 4 neighbouring outputs of a token, four lanes with 16.
 // Measured.  Rank 16, K 5120, parts of 5120, 1024 and 1024 rows: one token 8.0 us, 64 tokens of 48 adapters 19 us,
 // two launches, each of them one chain of loads.  Rank 64, K 13824, 5120 rows, 4464 tokens of prompts beside a fp32
-// projection: 121 us, of which shrinking 56 us, joining 5 us, expanding 61 us (183 MB, 3.0 TB/s).
+// projection: 121 us, of which shrinking 57 us, joining 5 us, expanding 59 us (183 MB, 3.1 TB/s).
 #include <hip/hip_runtime.h>
 
 #include "qmm_device.h"

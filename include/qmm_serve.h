@@ -92,6 +92,8 @@ int qmm_kv8_append(const qmm_kv8_cache* cache, const void* k, const void* v, int
  *   causal = 1: query j of n (0-based) of a sequence stands at p = kv_len - n + j and sees
  *     keys t <= p, with window > 0 only t > p - window and t < sinks (sinks > 0 needs a window).
  *   causal = 0 (window must be 0): every query sees all keys.
+ *   What is stored for keys that no query sees does not matter (pages behind a window may have
+ *   been given away while the table still names them).
  *   A query that sees no key gives zeros.  scale > 0 and finite; |q| below 2^100 and q . k
  *   below 2^126.
  *   gate (nullable) [T][n_q_heads][head_dim] bf16: out is multiplied by 1 / (1 + exp(-gate)).
