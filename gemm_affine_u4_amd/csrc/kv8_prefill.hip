@@ -89,8 +89,8 @@ __global__ __launch_bounds__(NW * 64, HD == 64 ? 2 : 1) void kv8_prefill_kernel(
     const int r = wave * 32 * CT + 32 * c + n, j = (row0 + r) / group;
     const bool ok = r < rows;
     c_lo[c] = 0, c_hi[c] = sq.kv_len;
-    if (ok && g.causal) {
-      const int64_t p = int64_t(sq.first) + j;
+    if (g.causal) {  // columns without a row see what the last row does
+      const int64_t p = int64_t(sq.first) + (ok ? j : (row0 + rows - 1) / group);
       c_hi[c] = p < 0 ? 0 : int(p) + 1;
       c_lo[c] = g.window > 0 && p - g.window + 1 > 0 ? int(p - g.window + 1) : 0;
     }
