@@ -30,6 +30,7 @@ __device__ __forceinline__ int attn8_split(const Attn8Plan& p) { return int((blo
 struct Attn8Tiles {
   int sink, first, count;  // count: splits of the block's keys
   int begin, end;
+  int lo, hi;  // every key from lo to hi - 1, and of the first `sinks` before lo, is seen by some row
   __device__ __forceinline__ int at(int v) const { return v < sink ? v : v - sink + first; }
 };
 __device__ __forceinline__ Attn8Tiles attn8_tiles(const Kv8AttnArgs& g, const AttnSeq& s, int row0, int rows, int group,
@@ -53,6 +54,7 @@ __device__ __forceinline__ Attn8Tiles attn8_tiles(const Kv8AttnArgs& g, const At
   c = c > p.nsplit ? p.nsplit : c < 1 ? 1 : c;
   const int per = (tiles + c - 1) / c;
   r.count = per > 0 ? (tiles + per - 1) / per : 1;
+  r.lo = int(lo), r.hi = int(hi);
   r.begin = split * per;
   r.end = r.begin + per < tiles ? r.begin + per : tiles;
   return r;

@@ -384,9 +384,12 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8AttnArgs g, int group,
 #pragma unroll 8
     for (int s = part; s < count; s += S) {
       const int64_t at = s * R0 + row;
-      const float f = exp2_hw((pm[at * 2] - mm) * qs);
+      const float x = (pm[at * 2] - mm) * qs, f = exp2_hw(x);
       const float4 v = *reinterpret_cast<const float4*>(po + at * HD + d);
-      l = fmaf(pm[at * 2 + 1], f, l);
+      // prompts' maxima hold the values' scales, which alone may lie 2^136 apart: such outputs vanish, their weights do not
+      float sum = pm[at * 2 + 1], w = f;
+      if (x < -120.f) w = exp2_hw(0.5f * x), sum *= w;
+      l = fmaf(sum, w, l);
       o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
     }
   }

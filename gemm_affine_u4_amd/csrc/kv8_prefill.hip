@@ -6,7 +6,9 @@
 // one multiply-add and one exponential, m being the running maximum of that exponent: so the weights
 // that are rounded to fp16 (2^-11) are those of the output's own terms, and off by 2^-36 of the largest
 // one where they are below 2^-25 of it.  The sum of the weights alone is that of each block's, in fp32,
-// over its s_v.
+// over its s_v.  Scales may be anything (append stores 0 and 2^-127 to 2^9): those below 2^-80 of the largest one that
+// the block's rows have met are taken as that, so that weights stay within fp32, and sums and outputs are held in a unit
+// that leaves them within fp32 for scales up to 2^88.
 //
 // Bound: the vector unit (7 issue slots a score, the exponential being 4, and 1.3 a code) beside the
 // matrix cores.
@@ -37,7 +39,6 @@ constexpr float kFloor = -1e30f;  // maximum of a row that has seen no key
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 4.f;     // a row's reference maximum may lag by 2^4,
 constexpr float kShift = 11.f;    // weights are 2^11 of it: below 2^15, within fp16's range
-constexpr float kTiny = 0x1p-100f;  // scales of blocks of zeros, whose values are 0 at any scale
 
 // Scores: keys (LDS operands) x queries.  The compiler would keep every product's result in accumulation
 // registers, and queries in turn spilled: scores are wanted by the vector unit, outputs (and queries, which
@@ -51,6 +52,17 @@ __device__ __forceinline__ void score_more(f32x16_t& d, f16x8_t k, f16x8_t q) {
 }
 // Wait states between a score product and the vector unit's read (12 are needed).
 __device__ __forceinline__ void score_settle(f32x16_t& d) { asm volatile("s_nop 15" : "+v"(d)); }
+
+// The largest of a wave's values, within the vector unit (row_shr:1, 2, 4, 8, row_bcast:15, 31).
+template <int CTRL>
+__device__ __forceinline__ float max_with(float x) {
+  const int w = int(__float_as_uint(x));
+  return fmaxf(x, __uint_as_float(uint32_t(__builtin_amdgcn_update_dpp(w, w, CTRL, 0xf, 0xf, false))));
+}
+__device__ __forceinline__ float max_wave(float x) {
+  x = max_with<0x118>(max_with<0x114>(max_with<0x112>(max_with<0x111>(x))));
+  return __uint_as_float(uint32_t(__builtin_amdgcn_readlane(int(__float_as_uint(max_with<0x143>(max_with<0x142>(x)))), 63)));
+}
 
 template <int N>
 using Int = std::integral_constant<int, N>;
@@ -134,9 +146,9 @@ __global__ __launch_bounds__(NW * 64, HD == 64 ? 2 : 1) void kv8_prefill_kernel(
   const int psh = g.c.page_shift, pmask = (1 << psh) - 1;
   const int32_t* __restrict__ table = g.table + int64_t(b) * g.max_pages;
   const int last_key = sq.kv_len > 0 ? sq.kv_len - 1 : 0;
-  auto key_of = [&](int v) { return int64_t(pl.at(v + (lane >> 2))) * kKeys + 16 * (lane & 3); };
+  auto key_of = [&](int v) { return pl.at(v + (lane >> 2)) * kKeys + 16 * (lane & 3); };  // below 2^31 some tiles ahead
   auto page_of = [&](int v) {
-    const int64_t k = key_of(v);
+    const int k = key_of(v);
     return table[(k < last_key ? k : last_key) >> psh];
   };
   const uint32_t n_pages = uint32_t(g.c.n_pages);
@@ -146,7 +158,7 @@ __global__ __launch_bounds__(NW * 64, HD == 64 ? 2 : 1) void kv8_prefill_kernel(
   int lw = pl.begin, l_next = 0;
   int64_t l_row = 0;
   auto rows_of = [&](int v, int page) {
-    return ((int64_t(uint32_t(page) < n_pages ? page : 0) * g.c.n_kv + kvh) << psh) + (int(key_of(v)) & pmask);
+    return ((int64_t(uint32_t(page) < n_pages ? page : 0) * g.c.n_kv + kvh) << psh) + (key_of(v) & pmask);
   };
   auto place = [&](int v, int t16) {  // that of 16 keys of tile v
     const int i = 4 * (v - lw) + t16;
@@ -156,33 +168,38 @@ __global__ __launch_bounds__(NW * 64, HD == 64 ? 2 : 1) void kv8_prefill_kernel(
   };
   // the window of the tiles that are computed: the scales of lane i's 16 keys, the logarithm and the
   // reciprocal of the values' one; whether any of the keys is there
-  int sw = pl.begin, s_page = 0;
+  int sw = pl.begin;
   float s_ks = 0.f, s_lv = 0.f, s_iv = 0.f, n_ks = 0.f, n_vs = 0.f;
   uint64_t there = 0;
   auto fetch_scales = [&](int v, int page) {  // of the window from v on
-    const int64_t k = key_of(v);
-    const bool ok = uint32_t(page) < n_pages && k < sq.kv_len;
+    const int k = key_of(v);
+    // only blocks that some row sees: others' scales may be anything
+    const bool ok = uint32_t(page) < n_pages && k < pl.hi && (k + 16 > pl.lo || k < sinks);
     n_ks = 0.f, n_vs = 0.f;
     if (ok) {
-      const int64_t at = (((int64_t(page) * g.c.n_kv + kvh) << psh) + (int(k) & pmask)) >> 4;
+      const int64_t at = (((int64_t(page) * g.c.n_kv + kvh) << psh) + (k & pmask)) >> 4;
       n_ks = g.c.k_scale[at];
       n_vs = g.c.v_scale[at];
     }
     return __ballot(ok);
   };
   uint64_t n_there = 0;
+  // Of a sum: up to 2^15 2^128 for each key (scales count as 2^-128 at least) stays below 2^127, and 2^11 / 2^88 above 2^-126.
+  const float unit = __uint_as_float(uint32_t(127 - 18 - 32 + __builtin_clz(sq.kv_len | 1)) << 23);
+  float v_top = 0x1p-48f;  // the largest value scale so far
   auto take_scales = [&]() {
-    const float vs = fmaxf(n_vs, kTiny);
+    v_top = max_wave(fmaxf(n_vs, v_top));
+    const float vs = fmaxf(n_vs, v_top * 0x1p-80f);
     s_ks = n_ks;
-    s_lv = __builtin_amdgcn_logf(vs);
-    s_iv = 1.f / vs;
+    s_lv = vs < 0x1p-100f ? __builtin_amdgcn_logf(vs * 0x1p64f) - 64.f : __builtin_amdgcn_logf(vs);  // of normal numbers
+    s_iv = unit / vs;
     there = n_there;
   };
 
   // a lane's share of a tile's codes: 16 dims of a key, two dims of 8 keys
   constexpr int KL = HD / 16, UK = 64 / KL;  // lanes of a key, keys of a wave's load
   const int k_key = lane / KL, k_dim = 16 * (lane % KL);
-  const uint32_t k_off = uint32_t(k_key * HD + k_dim);
+  const uint32_t k_off = uint32_t(16 * lane);
   u32x4_t ck[2][PER], cv[2][PER];  // of the next two tiles
   auto load_k = [&](int set, int i, int v) {
     const int key = UK * (wave + NW * i);  // of the tile
@@ -192,7 +209,7 @@ __global__ __launch_bounds__(NW * 64, HD == 64 ? 2 : 1) void kv8_prefill_kernel(
   auto load_v = [&](int set, int i, int v) {
     const int unit = wave + NW * i;  // of 1 KB: 128 / HD octets of keys
     const int8_t* from = g.c.v_codes + place(v, unit * 64 / HD) * HD + unit * 1024 % (16 * HD);
-    cv[set][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(from + uint32_t(16 * lane)));
+    cv[set][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(from + k_off));
   };
   // Codes into LDS, four at a time: word a of the lane's share (of all loads).
   constexpr int WORDS = 4 * PER;
@@ -285,9 +302,9 @@ __global__ __launch_bounds__(NW * 64, HD == 64 ? 2 : 1) void kv8_prefill_kernel(
       static_for<CT>([&](auto cx) {
         constexpr int c = decltype(cx)::value;
         const float top = fmaxf(m[c], fmaxf(mx[c], __shfl_xor(mx[c], 32)));
-        const float fac = exp2_hw(m[c] - top);
+        const float half = exp2_hw(0.5f * (m[c] - top)), fac = half * half;
         m[c] = top;
-        l[c] *= fac;
+        l[c] = l[c] * half * half;  // scales alone may move a maximum by 2^136, where outputs vanish and sums do not
 #pragma unroll
         for (int i = 0; i < OT; ++i) acc[c][i] *= fac;
       });
@@ -398,10 +415,10 @@ __global__ __launch_bounds__(NW * 64, HD == 64 ? 2 : 1) void kv8_prefill_kernel(
   };
 
   if (pl.begin < pl.end) {
-    s_page = page_of(pl.begin);
-    l_row = rows_of(pl.begin, s_page);
+    const int page = page_of(pl.begin);
+    l_row = rows_of(pl.begin, page);
     l_next = page_of(pl.begin + 16);
-    n_there = fetch_scales(pl.begin, s_page);
+    n_there = fetch_scales(pl.begin, page);
     static_for<PER>([&](auto i) {
       load_k(0, i, pl.begin);
       load_v(0, i, pl.begin);
@@ -444,9 +461,8 @@ __global__ __launch_bounds__(NW * 64, HD == 64 ? 2 : 1) void kv8_prefill_kernel(
         l_row = rows_of(lw, l_next);
         l_next = page_of(lw + 16);
       }
-      // the next window's scales: its pages, then they, some tiles before it begins
-      if (v - sw == 4) s_page = page_of(sw + 16);
-      if (v - sw == 9) n_there = fetch_scales(sw + 16, s_page);
+      // the next window's scales, some tiles before it begins (the loads' window moves on 4 tiles later)
+      if (v - sw == 9) n_there = fetch_scales(sw + 16, l_next);
       if (v - sw == 15) {
         sw += 16;
         take_scales();
@@ -476,7 +492,8 @@ __global__ __launch_bounds__(NW * 64, HD == 64 ? 2 : 1) void kv8_prefill_kernel(
     for (int i = 0; i < OT; ++i)
 #pragma unroll
       for (int a = 0; a < 4; ++a) {
-        const float4 o = {acc[c][i][4 * a], acc[c][i][4 * a + 1], acc[c][i][4 * a + 2], acc[c][i][4 * a + 3]};
+        const float4 o = {acc[c][i][4 * a] * unit, acc[c][i][4 * a + 1] * unit, acc[c][i][4 * a + 2] * unit,
+                          acc[c][i][4 * a + 3] * unit};
         const int d = 32 * i + 8 * a + 4 * hh;
         if (pl.count == 1) attn_store4(g, qrow * HD + d, o, sum);
         else *reinterpret_cast<float4*>(po + (split * R0 + qrow) * HD + d) = o;

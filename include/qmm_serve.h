@@ -101,6 +101,9 @@ int qmm_kv8_append(const qmm_kv8_cache* cache, const void* k, const void* v, int
  * values below 2^-24 of its largest lose digits).  A key's weight times its values' scale is rounded to
  * fp16: 2^-11 of it; where it is small, 2^-39 of the largest scale for few queries (up to 16 rows = max_q x heads of
  * a group), 2^-36 of the row's largest such product for prompts (more than 256 rows), between them one of the two.
+ * At the ends of the range: few queries are off by 2^-140 at least; prompts take value scales below 2^-80 of the largest
+ * one that any of a sequence's queries sees as that, so that values of such blocks beside much larger ones are off
+ * by up to 127 * 2^-80 of the largest scale, and value scales are up to 2^88 (qmm_kv8_append's are below 2^9).
  * workspace: 256-byte aligned, at least qmm_kv8_attn_workspace_bytes of the same T, B, max_q,
  * heads, max_kv = max_pages * page_size, window and sinks (0 for sizes out of range; always > 0
  * otherwise).

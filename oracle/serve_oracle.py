@@ -100,11 +100,16 @@ def attention(q, cache, table, kv_len, q_len, scale, causal=True, window=0, sink
     that is 2^-25 / 2^14 = 2^-39 of the largest scale; for prompts with the row's largest p s at 2^11 or more, 2^-36 of
     that (few = None: the larger of the two); and the scores' error d (fp32 sums of hd + 8 terms, M = scale sum |q k|), which changes each
     p by at most a factor e^(2 d) once normalised: (e^(2 d) - 1) W.  The hardware's exp2 (2^-22) and the
-    normalising sum (2^-20) sit in the 2^-18 added to the relative part."""
+    normalising sum (2^-20) sit in the 2^-18 added to the relative part.
+
+    At the ends of the scales' range: few queries lift scales by at most 2^112, so that a step is 2^-140 at least;
+    prompts take a scale below 2^-80 of the largest one that any of the rows sees (the key's block may be one of
+    zeros) as 2^-80 of that, which moves an output by up to 127 times as much.  The last 2^-133 are a step of the
+    smallest bf16 numbers."""
     n_q, hd = q.shape[1], q.shape[2]
     group = n_q // cache.n_kv
     out = np.zeros((q_len, n_q, hd))
-    tol = np.full((q_len, n_q, hd), 1e-30)
+    tol = np.full((q_len, n_q, hd), 2.0 ** -133)
     t = np.arange(kv_len)
     ids = np.asarray(table)[t // cache.page] if kv_len else np.zeros(0, int)
     there = (ids >= 0) & (ids < cache.n_pages)
@@ -128,14 +133,15 @@ def attention(q, cache, table, kv_len, q_len, scale, causal=True, window=0, sink
             o, w = p @ v, p @ np.abs(v)
             d = np.where(see[some], scale * (np.abs(x) @ np.abs(k).T), 0).max(1, keepdims=True) * (hd + 8) * 2.0 ** -24
             low = 2.0 ** -36 * (p * vs).max(1, keepdims=True)
+            raised = 0 if few else 2.0 ** -80 * vs[see.any(0)].max()
             if few or few is None:
-                low = np.maximum(0 if few else low, 2.0 ** -39 * vs.max())
-            e = w * (2.0 ** -11 + 2.0 ** -18 + np.expm1(2 * d)) + len(t) * 127 * low
+                low = np.maximum(0 if few else low, max(2.0 ** -39 * vs[see.any(0)].max(), 2.0 ** -140))
+            e = w * (2.0 ** -11 + 2.0 ** -18 + np.expm1(2 * d)) + len(t) * 127 * low + 127 * raised
             if gate is not None:
                 sig = 1 / (1 + np.exp(-gate[some, a]))
                 o, e = o * sig, e * sig + np.abs(o * sig) * 2.0 ** -20
             out[some, a] = o
-            tol[some, a] = e + (np.abs(o) + e) * 2.0 ** -8 + 1e-30
+            tol[some, a] = e + (np.abs(o) + e) * 2.0 ** -8 + 2.0 ** -133
     return out, tol
 
 
