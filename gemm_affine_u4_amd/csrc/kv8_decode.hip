@@ -26,7 +26,7 @@ namespace qmm {
 namespace {
 
 constexpr int kTile = 32;         // keys of a wave's step
-constexpr float kFloor = -1e30f;  // maximum of a row that has seen no key yet
+constexpr float kFloor = -1e38f;  // maximum of a row that has seen no key yet
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ f32x4_t mma16(f16x8_t a, f16x8_t b, f32x4_t c) {

@@ -8,7 +8,9 @@
 // one where they are below 2^-25 of it.  The sum of the weights alone is that of each block's, in fp32,
 // over its s_v.  Scales may be anything (append stores 0 and 2^-127 to 2^9): those below 2^-80 of the largest one that
 // the block's rows have met are taken as that, so that weights stay within fp32, and sums and outputs are held in a unit
-// that leaves them within fp32 for scales up to 2^88.
+// that leaves them within fp32 for scales up to 2^88.  And so that it holds for scores of any size: from 2^22 on (as a
+// bound, taken from the scales of keys) fp32 maxima lie too far from exact products, and a row takes its scores rounded
+// and all exponents from an offset of its own.
 //
 // Bound: the vector unit (7 issue slots a score, the exponential being 4, and 1.3 a code) beside the
 // matrix cores.
@@ -35,10 +37,11 @@ namespace {
 
 constexpr int kKeys = 64;
 constexpr int NW = 4;             // waves of a block
-constexpr float kFloor = -1e30f;  // maximum of a row that has seen no key
+constexpr float kFloor = -3e38f;  // maximum of a row that has seen no key
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 4.f;     // a row's reference maximum may lag by 2^4,
 constexpr float kShift = 11.f;    // weights are 2^11 of it: below 2^15, within fp16's range
+constexpr float kWild = 0x1p22f;  // exponents from which a rounded maximum lies too far from their exact products for that
 
 // Scores: keys (LDS operands) x queries.  The compiler would keep every product's result in accumulation
 // registers, and queries in turn spilled: scores are wanted by the vector unit, outputs (and queries, which
@@ -62,6 +65,20 @@ __device__ __forceinline__ float max_with(float x) {
 __device__ __forceinline__ float max_wave(float x) {
   x = max_with<0x118>(max_with<0x114>(max_with<0x112>(max_with<0x111>(x))));
   return __uint_as_float(uint32_t(__builtin_amdgcn_readlane(int(__float_as_uint(max_with<0x143>(max_with<0x142>(x)))), 63)));
+}
+
+// A lane's number and the one 32 lanes on (of the wave's halves, in that order): the larger, and the sum.
+__device__ __forceinline__ float2 halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return float2{__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
+__device__ __forceinline__ float max_halves(float x) {
+  const float2 v = halves(x);
+  return fmaxf(v.x, v.y);
+}
+__device__ __forceinline__ float sum_halves(float x) {
+  const float2 v = halves(x);
+  return v.x + v.y;
 }
 
 template <int N>
@@ -90,6 +107,10 @@ __global__ __launch_bounds__(NW * 64, HD == 64 ? 2 : 1) void kv8_prefill_kernel(
   if (split >= pl.count) return;
 
   __shared__ __attribute__((aligned(16))) _Float16 s_k[2][kKeys * kRowK<HD>], s_v[2][HD * kRowV];
+
+  // Where exponents may be wild, scores are rounded and a row's maximum and exponents are held from an offset of its own.
+  __shared__ float s_off[CT][NW * 64];
+  static_for<CT>([&](auto cx) { s_off[decltype(cx)::value][wave * 64 + lane] = 0.f; });
 
   // the lane's rows, and the keys that they see
   int c_lo[CT], c_hi[CT], u_lo = 0, u_hi = sq.kv_len;  // u: that all rows of the wave see
@@ -120,7 +141,7 @@ __global__ __launch_bounds__(NW * 64, HD == 64 ? 2 : 1) void kv8_prefill_kernel(
 #pragma unroll
       for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(raw[e][i])), fabsf(bf16_hi(raw[e][i]))));
     }
-    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    mx = max_halves(mx);
     const int ex = mx > 0.f ? int((__float_as_uint(mx) >> 23) & 255) - 127 : 0;
     const int sh = 7 - ex;
     qs[c] = fminf(g.scale * kLog2e * ldexpf(1.f, -sh), 1e35f);
@@ -186,8 +207,12 @@ __global__ __launch_bounds__(NW * 64, HD == 64 ? 2 : 1) void kv8_prefill_kernel(
   uint64_t n_there = 0;
   // Of a sum: up to 2^15 2^128 for each key (scales count as 2^-128 at least) stays below 2^127, and 2^11 / 2^88 above 2^-126.
   const float unit = __uint_as_float(uint32_t(127 - 18 - 32 + __builtin_clz(sq.kv_len | 1)) << 23);
+  // the key scale from which exponents may be wild (as bits, which are ordered as the numbers are)
+  uint32_t wild_from = 0;
+  uint32_t wild = 0;       // 4: they may be, from here on
   float v_top = 0x1p-48f;  // the largest value scale so far
   auto take_scales = [&]() {
+    wild |= __any(__float_as_uint(n_ks) > wild_from) ? 4 : 0;
     v_top = max_wave(fmaxf(n_vs, v_top));
     const float vs = fmaxf(n_vs, v_top * 0x1p-80f);
     s_ks = n_ks;
@@ -251,8 +276,8 @@ __global__ __launch_bounds__(NW * 64, HD == 64 ? 2 : 1) void kv8_prefill_kernel(
   struct Facts {
     float ks[2], lv[2], iv[2];  // of its two blocks of 16 keys
     int key;                    // the first one
-    uint32_t blocks;            // those that are there
-    bool masked;                // some row does not see all of them
+    uint32_t blocks;            // those that are there; bit 2: wild
+    bool masked;                // some row does not see all of them, or wild
   };
   auto facts = [&](int v, int half) {
     Facts f;
@@ -263,7 +288,7 @@ __global__ __launch_bounds__(NW * 64, HD == 64 ? 2 : 1) void kv8_prefill_kernel(
       f.lv[k] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s_lv), i + k));
       f.iv[k] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s_iv), i + k));
     }
-    f.blocks = uint32_t(there >> i) & 3;
+    f.blocks = (uint32_t(there >> i) & 3) | wild;
     f.key = pl.at(v) * kKeys + 32 * half;
     f.masked = f.key + 32 > u_hi || (f.key < u_lo && f.key + 32 > sinks) || f.blocks != 3;
     return f;
@@ -292,6 +317,15 @@ __global__ __launch_bounds__(NW * 64, HD == 64 ? 2 : 1) void kv8_prefill_kernel(
         }
         kq[c][0] = kq[c][1] = 1.f;
         ad[c][0] = ad[c][1] = 0.f;
+        if (f.blocks & 4) {
+          float& off = s_off[c][wave * 64 + lane];  // the largest rounded score where not 0
+          const float top = fmaxf(off != 0.f ? off : m[c], max_halves(mx[c]));
+          m[c] += off - top;
+          off = top;
+          mx[c] -= top;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[c][e] -= top;
+        }
       });
     }
     static_for<CT>([&](auto cx) {
@@ -301,7 +335,7 @@ __global__ __launch_bounds__(NW * 64, HD == 64 ? 2 : 1) void kv8_prefill_kernel(
     if (__any(run)) {
       static_for<CT>([&](auto cx) {
         constexpr int c = decltype(cx)::value;
-        const float top = fmaxf(m[c], fmaxf(mx[c], __shfl_xor(mx[c], 32)));
+        const float top = fmaxf(m[c], max_halves(mx[c]));
         const float half = exp2_hw(0.5f * (m[c] - top)), fac = half * half;
         m[c] = top;
         l[c] = l[c] * half * half;  // scales alone may move a maximum by 2^136, where outputs vanish and sums do not
@@ -427,6 +461,9 @@ __global__ __launch_bounds__(NW * 64, HD == 64 ? 2 : 1) void kv8_prefill_kernel(
       load_k(1, i, pl.begin + 1);
       load_v(1, i, pl.begin + 1);
     });
+    float q_top = qs[0];  // codes and queries multiply to 2^15 for each dim at most
+    static_for<CT>([&](auto cx) { q_top = fmaxf(q_top, qs[decltype(cx)::value]); });
+    wild_from = uint32_t(__builtin_amdgcn_readfirstlane(int(__float_as_uint(kWild / (HD * 0x1p15f) / max_wave(q_top)))));
     take_scales();
     static_for<WORDS>([&](auto a) { unpack_k(0, a, 0); });
     static_for<WORDS>([&](auto a) { unpack_v(0, a, 0); });
@@ -484,7 +521,8 @@ __global__ __launch_bounds__(NW * 64, HD == 64 ? 2 : 1) void kv8_prefill_kernel(
   float* po = static_cast<float*>(g.ws);
   static_for<CT>([&](auto cx) {
     constexpr int c = decltype(cx)::value;
-    const float sum = l[c] + __shfl_xor(l[c], 32);
+    const float off = s_off[c][wave * 64 + lane], fold = off != 0.f ? exp2_hw(m[c]) : 1.f;
+    const float sum = sum_halves(l[c]) * fold, scale = unit * fold;
     const int r = wave * 32 * CT + 32 * c + n;
     if (r >= rows) return;
     const int64_t qrow = (int64_t(sq.q0) + (row0 + r) / group) * g.n_q + kvh * group + (row0 + r) % group;
@@ -492,15 +530,15 @@ __global__ __launch_bounds__(NW * 64, HD == 64 ? 2 : 1) void kv8_prefill_kernel(
     for (int i = 0; i < OT; ++i)
 #pragma unroll
       for (int a = 0; a < 4; ++a) {
-        const float4 o = {acc[c][i][4 * a] * unit, acc[c][i][4 * a + 1] * unit, acc[c][i][4 * a + 2] * unit,
-                          acc[c][i][4 * a + 3] * unit};
+        const float4 o = {acc[c][i][4 * a] * scale, acc[c][i][4 * a + 1] * scale, acc[c][i][4 * a + 2] * scale,
+                          acc[c][i][4 * a + 3] * scale};
         const int d = 32 * i + 8 * a + 4 * hh;
         if (pl.count == 1) attn_store4(g, qrow * HD + d, o, sum);
         else *reinterpret_cast<float4*>(po + (split * R0 + qrow) * HD + d) = o;
       }
     if (pl.count > 1 && hh == 0) {
       float* pm = po + plan.nsplit * R0 * HD;
-      pm[(split * R0 + qrow) * 2] = m[c];
+      pm[(split * R0 + qrow) * 2] = off != 0.f ? off : m[c];
       pm[(split * R0 + qrow) * 2 + 1] = sum;
       if (split == 0) pm[plan.nsplit * R0 * 2 + qrow] = 1.f;  // maxima are in powers of two
     }

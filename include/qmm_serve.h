@@ -94,8 +94,8 @@ int qmm_kv8_append(const qmm_kv8_cache* cache, const void* k, const void* v, int
  *   causal = 0 (window must be 0): every query sees all keys.
  *   What is stored for keys that no query sees does not matter (pages behind a window may have
  *   been given away while the table still names them).
- *   A query that sees no key gives zeros.  scale > 0 and finite; |q| below 2^100 and q . k
- *   below 2^126.
+ *   A query that sees no key gives zeros.  scale > 0 and finite; |q| and the scales of keys below 2^100, q . k
+ *   and scale * q . k below 2^126.
  *   gate (nullable) [T][n_q_heads][head_dim] bf16: out is multiplied by 1 / (1 + exp(-gate)).
  * Scores, sums, maxima and the softmax are fp32, from exact codes and queries (of a query row,
  * values below 2^-24 of its largest lose digits).  A key's weight times its values' scale is rounded to

@@ -140,3 +140,66 @@ def test_prompts_behind_a_long_run_of_zero_values(hd, tail, others):
             # the weights' fp16 and the output's bf16; sums of 600000 weights, all positive, in fp32 in an order that adds
             # 8 at a time: 600000 / 8 roundings of 2^-24 of the sum at most
             assert np.all(np.abs(got[j, a] - o) <= mag * (2.0 ** -11 + 75000 * 2.0 ** -24) + np.abs(o) * 2.0 ** -8 + 1e-12), (j, a)
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("q_len", [1, 3, 70])
+def test_a_single_visible_key_whatever_its_score(hd, q_len):
+    """A row that sees one key has its value, whether the score is far below or above 0."""
+    rng = np.random.default_rng([66, hd, q_len])
+    n = 90
+    table, pages = tables(rng, [n], 16)
+    c = srv.Cache(pages, 1, 16, hd, rng)
+    k = rng.uniform(1e3, 2e3, (n, 1, hd)).astype(np.float32)
+    v = rng.standard_normal((n, 1, hd)).astype(np.float32)
+    c.append(table[0], n, k, v)
+    t = np.arange(n - q_len, n)
+    want = c.get(table[0, t // 16], t % 16, 0)[1]
+    for size, loud in ((1e24, 1), (1e29, 1), (-1e24, 1), (-1e29, 1), (1e-3, 1e30), (-1e-3, 1e30)):
+        qb, _ = bf16(size * rng.uniform(0.5, 1, (q_len, 4, hd)))
+        out = Guarded((q_len, 4, hd), False)
+        need = qmm.qmm_kv8_attn_workspace_bytes(q_len, 1, q_len, 4, 1, hd, table.shape[1] * 16, 1)
+        g = gpu_cache(c)
+        g.tensors[1].mul_(loud)  # key scales that a caller's own cache may hold
+        qmm.qmm_kv8_attn(dev(qb), g, dev(table), ints(n), out.t, torch.empty(need, dtype=torch.uint8, device="cuda"),
+                         q_start=ints(0, q_len), max_q=q_len, window=1)
+        torch.cuda.synchronize()
+        # one weight of fp16 (2^-11), the sum's exponential (2^-18) and the output's rounding
+        assert_within(bf16_bits_to_f64(out.values()), np.broadcast_to(want[:, None], (q_len, 4, hd)),
+                      np.abs(want[:, None]) * (2.0 ** -8 + 2.0 ** -10) + 1e-30, f"{q_len} queries of {size}")
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("q_len", [1, 3, 70])
+@pytest.mark.parametrize("size", [1e8, 1e9, 1e12, 1e20, 1e28])
+def test_rows_whose_largest_score_stands_alone(hd, q_len, size):
+    """Keys are multiples of one direction, so that scores are far apart and the nearest one is the answer, above and
+    below 0, whatever comes before it."""
+    rng = np.random.default_rng([67, hd, q_len])
+    n = 700
+    table, pages = tables(rng, [n], 32)
+    c = srv.Cache(pages, 1, 32, hd, rng)
+    steps = rng.permutation(np.arange(1, 126))[np.arange(n) % 125].astype(np.float32)  # whole codes, all different in 125
+    k = np.tile(steps[:, None, None], (1, 1, hd))
+    c.append(table[0], n, k, rng.standard_normal((n, 1, hd)).astype(np.float32))
+    c.k_codes[:] = 0
+    for i in range(n):
+        c.k_codes[table[0, i // 32], 0, i % 32] = steps[i]
+    c.k_scale[:] = 1.0
+    first = n - q_len
+    for sign in (1.0, -1.0):
+        qb, _ = bf16(np.full((q_len, 4, hd), sign * size))
+        out = Guarded((q_len, 4, hd), False)
+        need = qmm.qmm_kv8_attn_workspace_bytes(q_len, 1, q_len, 4, 1, hd, table.shape[1] * 32, 125)
+        qmm.qmm_kv8_attn(dev(qb), gpu_cache(c), dev(table), ints(n), out.t,
+                         torch.empty(need, dtype=torch.uint8, device="cuda"), q_start=ints(0, q_len), max_q=q_len, window=125)
+        torch.cuda.synchronize()
+        t = np.arange(n)
+        best = []
+        for j in range(q_len):
+            see = np.flatnonzero((t <= first + j) & (t > first + j - 125))
+            best.append(see[np.argmax(sign * steps[see])])
+        best = np.array(best)
+        want = c.get(table[0, best // 32], best % 32, 0)[1]
+        assert_within(bf16_bits_to_f64(out.values()), np.broadcast_to(want[:, None], (q_len, 4, hd)),
+                      np.abs(want[:, None]) * (2.0 ** -8 + 2.0 ** -10) + 1e-30, f"{q_len} queries of {sign * size}")
