@@ -159,6 +159,15 @@ def test_workspace_bytes():
     assert qmm.qmm_lora_workspace_bytes(4, 100, 8) == 0 and qmm.qmm_lora_workspace_bytes(4, 64, 8, 4) == 0
 
 
+@pytest.mark.parametrize("B,max_q,max_kv,window", [(1, 1, 131072, 0), (4, 3, 20000, 4000), (1, 90, 9000, 0),
+                                                   (64, 1, 64, 0)])
+def test_workspace_bytes_of_no_tokens(B, max_q, max_kv, window):
+    """A step without tokens is one of valid sizes: some bytes, and a call with as many enqueues nothing."""
+    need = qmm.qmm_kv8_attn_workspace_bytes(0, B, max_q, 4, 2, 128, max_kv, window, 0)
+    assert 0 < need <= qmm.qmm_kv8_attn_workspace_bytes(1, B, max_q, 4, 2, 128, max_kv, window, 0)
+    assert attn(T=0, B=B, max_q=max_q, max_pages=max_kv // 32, window=window, sinks=0, ws_bytes=need) == 0
+
+
 def test_python_side_refuses_host_tensors():
     shapes = qmm.kv8_cache_shapes(2, 1, 32, 64)
     t = [torch.zeros(s, dtype=torch.int8 if "codes" in n else torch.float32) for n, s in shapes.items()]
