@@ -671,7 +671,7 @@ uint64_t kv4_attn_workspace(int64_t T, int64_t B, int64_t max_q, int64_t n_q, in
                             int64_t max_kv) {
   const uint64_t ns = uint64_t(attn_plan(B, max_q, n_q, n_kv, hd, max_kv).nsplit);
   // of a row: each split's output, maximum and sum; the factor of its scores
-  return ns > 1 ? uint64_t(T) * uint64_t(n_q) * (ns * uint64_t(hd + 2) + 1) * 4 : 256;
+  return ns > 1 && T > 0 ? uint64_t(T) * uint64_t(n_q) * (ns * uint64_t(hd + 2) + 1) * 4 : 256;
 }
 
 int launch_kv4_attn(const Kv4AttnArgs& a, hipStream_t s) {

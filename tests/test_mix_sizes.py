@@ -39,3 +39,12 @@ def test_more_delta_rule_prompts_than_a_launch_has_threads_for_are_refused():
     assert qmm.qmm_gdn_workspace_bytes(1 << 20, 65535, 17, 8, 48, 128, 128) == 0
     assert qmm.qmm_gdn_workspace_bytes(1 << 20, 65535, 16, 8, 48, 128, 128) > 0  # token by token
     assert gdn(T=1 << 20, B=65535, max_len=17, Hk=8, Hv=48, n_slots=1, q=B0 + (1 << 40)) == S["QMM_ERR_SHAPE"]
+
+
+def test_calls_without_tokens_have_a_workspace():
+    """Valid sizes, so not the 0 of sizes out of range, however long the table is."""
+    for B, max_q, max_kv in ((1, 1, 131072), (4, 3, 20000), (1, 90, 9000), (64, 1, 64)):
+        need = qmm.qmm_kv4_attn_workspace_bytes(0, B, max_q, 4, 2, 128, max_kv)
+        assert 0 < need <= qmm.qmm_kv4_attn_workspace_bytes(1, B, max_q, 4, 2, 128, max_kv)
+    for B, max_len in ((1, 1), (3, 100), (64, 1 << 20)):
+        assert qmm.qmm_gdn_workspace_bytes(0, B, max_len, 2, 4, 128, 128) > 0
