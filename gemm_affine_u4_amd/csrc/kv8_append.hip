@@ -414,7 +414,7 @@ int launch_hd(const Kv8AppendArgs& a, hipStream_t s) {
   const int64_t met = a.T / kBlock + a.B;  // blocks that tokens meet, about
   const int64_t fill = int64_t(device_cus()) * 48 / met;
   // (and a grid's workgroups fit where max_q is far above what sequences have)
-  const int64_t fits = ((int64_t(1) << 26) - 1) / (a.B * blocks), most = fits < items ? fits : items;
+  const int64_t fits = ((int64_t(1) << 26) - 4) / (a.B * blocks), most = fits < items ? fits : items;
   const int want = int(fill < 1 || most < 1 ? 1 : fill < most ? fill : most);
   const int per = (items + want - 1) / want, groups = (items + per - 1) / per;
   const int64_t wgs = (a.B * blocks * groups + 3) / 4;

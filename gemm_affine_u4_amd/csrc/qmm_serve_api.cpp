@@ -18,6 +18,9 @@ constexpr int64_t kMaxSeqs = 65535;  // a grid dimension
 // Keys of a page table: the kernels number keys in 32 bits and look up some tiles ahead.
 constexpr int64_t kMaxKeys = (int64_t(1) << 31) - (1 << 16);
 
+// Blocks of 16 keys that an append may meet: a wave each, four in a workgroup, of a launch of less than 2^32 threads.
+constexpr int64_t kMaxBlocks = (int64_t(1) << 26) - 4;
+
 bool type_ok(int t) { return t == QMM_OUT_BF16 || t == QMM_OUT_F32; }
 size_t type_bytes(int t) { return t == QMM_OUT_F32 ? 4 : 2; }
 bool hd_ok(int64_t hd) { return hd == 64 || hd == 128 || hd == 256; }
@@ -79,7 +82,7 @@ int qmm_kv8_append(const qmm_kv8_cache* cache, const void* k, const void* v, int
   if (!k || !v || !kv_lens || !page_table || (!cos_sin && (q || positions)) || (q && !q_out)) return QMM_ERR_NULL;
   if (!type_ok(in_dtype)) return QMM_ERR_ENUM;
   const int64_t hd = cache->head_dim, n_kv = cache->n_kv_heads;
-  if (!batch_ok(T, B, max_q) || (!q_start && (T != B || max_q != 1)) || B * (max_q / 16 + 2) >= int64_t(1) << 26 ||
+  if (!batch_ok(T, B, max_q) || (!q_start && (T != B || max_q != 1)) || B * (max_q / 16 + 2) > kMaxBlocks ||
       max_pages < 1 || max_pages > kMaxKeys / cache->page_size || (q && (n_q_heads < 1 || n_q_heads > kMaxHeads)) ||
       (cos_sin && (rot_dim < 2 || rot_dim % 2 || rot_dim > hd || max_pos < 1 || max_pos > kMaxI32)))
     return QMM_ERR_SHAPE;

@@ -66,7 +66,7 @@ typedef struct qmm_kv8_cache {
  * become rint(c * (old scale / new scale)).  c = rint(x * (1/scale)) clamped to +-127 (0 where the
  * scale is not above 2^-127).  A scale that grows, grows by a quarter: so the roundings of a key whose block
  * fills token by token add up to 2.5 steps at most.  Slots of a block behind its last key hold any codes.
- * T and max_q up to 2^24, B up to 65535, B * (max_q / 16 + 2) below 2^26.
+ * T and max_q up to 2^24, B up to 65535, B * (max_q / 16 + 2) up to 2^26 - 4.
  */
 int qmm_kv8_append(const qmm_kv8_cache* cache, const void* k, const void* v, int64_t T, int in_dtype,
                    const int32_t* q_start, const int32_t* kv_lens, const int32_t* page_table, int64_t B,

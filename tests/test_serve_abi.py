@@ -105,6 +105,13 @@ def test_append_refuses(bad, want):
     assert append(**bad) == S["QMM_ERR_" + want]
 
 
+def test_append_of_more_blocks_than_a_launch_has_threads_for_is_refused():
+    """A wave for each block of 16 keys that a sequence may meet, four waves of 64 in a workgroup, below 2^32 threads."""
+    for B, max_q in ((8191, 131058), (1, (1 << 24)), (65535, 16 * 1021 + 2), (65532, 16 * 1022 + 2)):
+        threads = (B * ((max_q + 14) // 16 + 1) + 3) // 4 * 256
+        assert append(T=0, B=B, max_q=max_q, max_pages=1) == (S["QMM_ERR_SHAPE"] if threads >= 1 << 32 else 0), (B, max_q)
+
+
 @pytest.mark.parametrize("bad, want", [
     (dict(q=None), "NULL"), (dict(kv_lens=None), "NULL"), (dict(table=None), "NULL"), (dict(ws=None), "NULL"),
     (dict(out=None), "NULL"), (dict(causal=2), "ENUM"), (dict(window=-1), "SHAPE"), (dict(causal=0, sinks=0), "SHAPE"),
