@@ -186,7 +186,7 @@ def verify(draft, start, target, q, u, max_draft):
 def lora(x, a, b, ids, base, scales, out_eps):
     """One part: x [T, K], a [adapters, r, K], b [adapters, N, r], base [T, N], all fp64.  Returns (y, tol).
 
-    The tolerance: fp32 sums of K + 80 terms (the matrix cores', four waves' and up to 64 ranges') in h, carried
+    The tolerance: fp32 sums of K + 20 terms (the matrix cores', four waves' and up to 16 ranges') in h, carried
     through |b|; 3 r + 8 more in the second product, whose pieces hold 24 bits; the sum with base; the output's
     rounding out_eps |y|."""
     x, a, b, base = (np.asarray(t, np.float64) for t in (x, a, b, base))
@@ -200,5 +200,5 @@ def lora(x, a, b, ids, base, scales, out_eps):
         s = 1.0 if scales is None else float(scales[i])
         h, hm = a[i] @ x[t], np.abs(a[i]) @ np.abs(x[t])
         y[t] += s * (b[i] @ h)
-        tol[t] += abs(s) * (np.abs(b[i]) @ (hm * (a.shape[2] + 80) * u + np.abs(h) * (3 * a.shape[1] + 8) * u))
+        tol[t] += abs(s) * (np.abs(b[i]) @ (hm * (a.shape[2] + 20) * u + np.abs(h) * (3 * a.shape[1] + 8) * u))
     return y, tol + (np.abs(y) + tol) * out_eps

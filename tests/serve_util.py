@@ -53,3 +53,20 @@ def filled(rng, kv_lens, n_kv, hd, page, spare=2, scale_k=1.0, scale_v=1.0):
 def few_rows(rows):
     """The form that attention of so many rows per KV head takes: of few queries, prompts', or (None) either."""
     return True if rows <= 16 else None if rows <= 256 else False
+
+
+def whole_adapters(rng, T, K, rank, rows, n_ad):
+    """Adapters whose h = A x are whole numbers of 24 bits times a power of two, and whose B passes one of them on to each
+    output: every product and sum is exact in fp32, so that y shows all bits that h is carried with.
+    Returns x, a, b (of fp32, exact in bf16), ids and y in fp64."""
+    ids = rng.integers(0, n_ad, T).astype(np.int32)
+    at = np.sort(rng.choice(K, 3, replace=False))  # the three inputs that count
+    x = np.zeros((T, K), np.float32)
+    x[:, at] = rng.choice([-1.0, 1.0], (T, 1)) * 2.0 ** rng.integers(-20, 20, (T, 1)) * np.array([65536.0, 256.0, 1.0])
+    a = np.zeros((n_ad, rank, K), np.float32)
+    a[:, :, at[0]] = rng.integers(128, 256, (n_ad, rank))
+    a[:, :, at[1:]] = rng.integers(0, 256, (n_ad, rank, 2))
+    b = np.zeros((n_ad, rows, rank), np.float32)
+    b[:, np.arange(rows), np.arange(rows) % rank] = 2.0 ** rng.integers(-6, 6, (n_ad, rows))
+    h = np.einsum("tk,trk->tr", x[:, at].astype(np.float64), a[ids][:, :, at])
+    return x, a, b, ids, np.einsum("tr,tnr->tn", h, b[ids])

@@ -11,6 +11,7 @@ import torch
 
 import gemm_affine_u4_amd as qmm
 from oracle import serve_oracle as srv
+from tests.serve_util import bf16, whole_adapters
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 S = qmm.STATUS
@@ -286,3 +287,22 @@ def test_lora_oracle():
     y, _ = srv.lora(x, a, b, [1, -1, 0], base, [2.0, 0.5], 0)
     assert np.allclose(y[0], base[0] + 0.5 * b[1] @ a[1] @ x[0]) and np.all(y[1] == base[1])
     assert np.allclose(y[2], base[2] + 2 * b[0] @ a[0] @ x[2])
+
+
+def test_adapters_that_show_all_bits_of_h():
+    """Of the inputs that the GPU's adapters are held against: three bf16 pieces of h give the outputs, two do not, and the
+    oracle's bound for any inputs would not have told them apart."""
+    x, a, b, ids, want = whole_adapters(np.random.default_rng(5), 40, 64, 8, 24, 3)
+    for t in (x, a, b):
+        assert np.array_equal(bf16(t)[1], t)
+    ref, tol = srv.lora(x, a, b, ids, np.zeros(want.shape), None, 2.0 ** -24)
+    assert np.array_equal(ref, want)
+    for pieces in (3, 2):
+        h, left = np.zeros((40, 8)), np.einsum("tk,trk->tr", x.astype(np.float64), a[ids])
+        for _ in range(pieces):
+            p = bf16(left)[1]
+            h, left = h + p, left - p
+        y = np.einsum("tr,tnr->tn", h, b[ids])
+        off = np.abs(y - want) > np.abs(want) * 2.0 ** -24
+        assert not off.any() if pieces == 3 else off.mean() > 0.9
+        assert np.all(np.abs(y - want) <= tol)

@@ -7,7 +7,7 @@ import gemm_affine_u4_amd as qmm
 import synth
 from oracle import serve_oracle as srv
 from tests.gpu_util import Guarded, assert_within, bf16_bits_to_f64, dev, dev_weight
-from tests.serve_util import bf16
+from tests.serve_util import bf16, whole_adapters
 
 pytestmark = pytest.mark.gpu
 
@@ -190,6 +190,21 @@ def test_in_a_graph_and_on_another_stream(T):
             qmm.qmm_lora(x, a, b, ids, y, ws, base=base)
             torch.cuda.synchronize()
             assert torch.equal(o, want) and torch.equal(y, want)
+
+
+@pytest.mark.parametrize("rank", [8, 32, 128])
+@pytest.mark.parametrize("T,K", [(1, 64), (20, 2048), (300, 2048), (3000, 512)])
+def test_all_bits_of_h(T, K, rank):
+    """h is taken on with 24 bits: outputs of exact products and sums are right to half a step of fp32."""
+    rng = np.random.default_rng([33, T, rank])
+    rows = 272
+    x, a, b, ids, want = whole_adapters(rng, T, K, rank, rows, 5)
+    y = Guarded((T, rows), True)
+    y.t.zero_()
+    ws = torch.empty(qmm.qmm_lora_workspace_bytes(T, K, rank), dtype=torch.uint8, device="cuda")
+    qmm.qmm_lora(dev(bf16(x)[0]), dev(bf16(a)[0]), dev(bf16(b)[0]), dev(ids), y.t, ws)
+    torch.cuda.synchronize()
+    assert_within(y.values(), want, np.abs(want) * 2.0 ** -24, "whole numbers")
 
 
 def test_beside_the_quantized_projection():
