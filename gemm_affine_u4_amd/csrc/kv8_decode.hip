@@ -445,8 +445,12 @@ int join_hd(const Kv8AttnArgs& a, const Attn8Plan& p, hipStream_t s) {
 //   16 sequences x 256 dims   30 rows 44, 54     48 rows 64, 59
 //    4 sequences x 256 dims  128 rows 43, 47    192 rows 61, 48
 //    4 sequences x 128 dims  256 rows 39, 47
+//   64 sequences x 64 dims    48 rows 61, 80    64 rows 74, 78    96 rows 98, 84   128 rows 119, 84
+//   32 sequences x 64 dims    64 rows 44, 48    80 rows 53, 50
+//   16 sequences x 64 dims    64 rows 27, 31    96 rows 36, 34   128 rows 43, 36
+//    4 sequences x 64 dims   128 rows 19, 24   256 rows 27, 26
 bool few_rows(int64_t rows, int64_t heads, int64_t hd) {
-  return rows <= (hd == 256 ? 16 : hd == 128 ? 96 : 128) ||
+  return rows <= (hd == 256 ? 16 : hd == 128 ? 96 : 64) ||
          (rows <= 256 && (rows + 15) / 16 * heads <= (hd == 256 ? 128 : 256));
 }
 
