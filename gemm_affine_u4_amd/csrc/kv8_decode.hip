@@ -480,11 +480,16 @@ Attn8Plan attn8_plan(int64_t B, int64_t max_q, int64_t n_q, int64_t n_kv, int64_
   while (p.keys > 128 && blocks * 1024 / p.keys < 2 * cus) p.keys /= 2;
   ns = 8 * cus / blocks < 4 ? 8 * cus / blocks : 4;
   if (ns < cus / blocks) ns = cus / blocks;
+  // (a second launch joins them: one token of 40 / 8 heads x 128 in splits and without: 320 keys 10.8, 8.8 us; 512 10.7, 9.9;
+  // 768 11.4, 11.2; 1024 11.1, 12.7; 16 of them: 512 10.3, 10.4; 768 14.0, 11.8; 1024 15.0, 14.4; 1500 17.7, 19.0)
   if (seen <= 768 || seen <= 2 * p.keys) ns = 1;
   const int64_t most = (seen + p.keys - 1) / p.keys;
   ns = ns > most ? most : ns;
   p.nsplit = int(ns > 256 ? 256 : ns < 1 ? 1 : ns);
-  p.waves = blocks * p.nsplit <= cus / 2 ? 8 : 4;
+  // 8 waves where they halve a chain of several steps and nothing else could (one token, 4 and 8 waves, us; 40 / 8 heads x
+  // 128: 200 keys 8.0, 8.5; 400 10.1, 10.0; 517 11.0, 10.1; 760 12.1, 11.3; split: 1200 11.1, 11.6; 4000 12.5, 13.0.
+  // 14 / 2 heads x 64: 517 keys 8.6, 7.8; 24 / 4 x 256: 400 15.1, 15.7; 517 16.9, 16.3; 760 18.7, 18.9; 4000 14.6, 16.2)
+  p.waves = p.nsplit == 1 && seen > 448 && blocks <= cus / 2 ? 8 : 4;
   return p;
 }
 
