@@ -644,6 +644,7 @@ def qmm_kv8_attn(q, cache, page_table, kv_lens, out, workspace, q_start=None, ma
                  causal: bool = True, window: int = 0, sinks: int = 0, gate=None, stream=None) -> None:
     """Attention of q [T, n_q, head_dim] (bf16) over the cache of B sequences: page_table int32
     [B, max_pages], kv_lens int32 [B], q_start int32 [B + 1] (None: one query a sequence); out as q.
+    Prompts and sequences of few queries are faster in calls of their own (the call is cut by max_q).
     window: only the last `window` keys are seen, and the first `sinks` ones.  scale: head_dim ** -0.5
     unless given; gate (as q): out is multiplied by its sigmoid."""
     st = (_SERVE or _serve()).attn(q, cache._c, page_table, kv_lens, out, workspace, q_start, max_q, scale,

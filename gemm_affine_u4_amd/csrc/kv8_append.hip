@@ -12,8 +12,10 @@
 // eight rotation pairs, so that a pair needs one load of each value and of its angle; a wave's items
 // follow each other over the heads, and the angles stay in registers.  For values a lane holds 4 dims
 // (2 of 64) of eight neighbouring keys, which are its 32 bytes of codes.
-// Measured (40 query and 8 KV heads of 128): 64 single tokens 5.1 us, prompts of 256 MB in and out 57 us (4.4 TB/s); 24 and
-// 4 heads of 256, fp32, 92 MB at odd places: 31 us.
+// Measured (40 query and 8 KV heads of 128): 16 single tokens 5.1 us, 64 of them 7.1, prompts of 256 MB in and out 57 us
+// (4.4 TB/s); 24 and 4 heads of 256, fp32, 92 MB at odd places: 31 us, as nothing of the next head is under way there.  With
+// rotated dims that are no multiple of 16 pairs are turned one by one, at 256 dims out of scratch (104 registers): the
+// same chunks with 56 dims rotated 148 us, of bf16 209 (64 dims 22).
 #include <hip/hip_runtime.h>
 
 #include "kv4_attn.h"
@@ -132,8 +134,9 @@ __global__ __launch_bounds__(256, HD == 256 && VEC ? 3 : 2) void kv8_append_kern
   const int da = !VEC ? 16 * li : paired ? 8 * li : g.rot + 16 * (li - pairs);
   const int db = paired ? half + 8 * li : da + 8;
   auto live = [&](int p) { return p * PPT + sub >= lo && p * PPT + sub < hi; };
-  // A block's values stay in registers where they fit (with the next item's loads under way, and the angles);
-  // of 256 dims, or where pairs are taken one by one, keys are read and turned twice: for the scale, then for the codes.
+  // A block's values stay in registers where they fit with the next item's loads under way, and the angles.  Of 256 dims, or
+  // where pairs are taken one by one, no loads are under way, angles are read for every head, and keys (not queries or
+  // values) are read and turned twice: for the scale, then for the codes.
   constexpr bool HELD = HD < 256 && VEC;
   using Run = Raw<F32, 8>;
   const int u_k = u1 < n_k ? u1 : n_k;

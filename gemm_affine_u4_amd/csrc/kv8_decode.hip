@@ -16,7 +16,8 @@
 // second product wants from it: nothing crosses lanes between the two, and its eight keys
 // share their scales.
 // Measured (40 query and 8 KV heads of 128): 64 contexts of 100 to 16000 keys 174 us (5.6 TB/s), one of 517 keys
-// 9.8 us, most of it the chain from the table over keys and values to the join.
+// 9.7 us, most of it the chain from the table over keys and values to the join.  At 256 dims 6 to 8 registers spill (28 to 36
+// bytes of scratch): 24 and 4 heads, 64 contexts of 100 to 16000 keys 194 us (4.9 TB/s).
 #include <hip/hip_runtime.h>
 
 #include "kv8_attn.h"
@@ -196,7 +197,8 @@ __global__ __launch_bounds__(NW * 64, 2) void kv8_decode_kernel(Kv8AttnArgs g, i
 
   f32x4_t acc[NV][2];  // in units of 1 / lift
   float m = kFloor, l = 0.f;
-  // All value scales met so far are below vtop, a power of two; lift brings that to 2^12.
+  // All value scales met so far are below vtop, a power of two; lift brings that to 2^12 (fp32 ends there: where all scales
+  // are below 2^-100, weights times scales are off by up to 2^-140).
   float vtop = 0x1p-100f, lift = 0x1p112f;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -439,8 +441,10 @@ int join_hd(const Kv8AttnArgs& a, const Attn8Plan& p, hipStream_t s) {
 }
 
 // Which calls run here, others as prompts: those of few rows for each KV head, whose prompt blocks would be mostly empty,
-// and those of few row tiles in all, which as prompts would be few blocks.  Here and as prompts, us, contexts of 4000,
-// 4 KV heads a sequence:
+// and those of few row tiles in all, which as prompts would be few blocks.  One rule for all sequences of a call: single tokens
+// beside a prompt run in blocks of 128 or 256 rows, unsplit (63 of them on 100 to 8000 keys and a prompt of 512 on 2048, one
+// call and two: 40 / 8 heads x 128 723 and 176 us, 24 / 4 x 256 1281 and 202, 14 / 2 x 64 187 and 48).
+// Here and as prompts, us, contexts of 4000, 4 KV heads a sequence:
 //   64 sequences x 128 dims   96 rows 145, 155   128 rows 184, 158
 //   16 sequences x 256 dims   30 rows 44, 54     48 rows 64, 59
 //    4 sequences x 256 dims  128 rows 43, 47    192 rows 61, 48

@@ -12,20 +12,21 @@
 // bound, taken from the scales of keys) fp32 maxima lie too far from exact products, and a row takes its scores rounded
 // and all exponents from an offset of its own.
 //
-// Bound: the vector unit (7 issue slots a score, the exponential being 4, and 1.3 a code) beside the
-// matrix cores.
+// Bound: one wave a SIMD (three at 64 dims) that issues its vector work (7 slots a score, the exponential being 4, and 1.3 a
+// code) and its matrix instructions in turn, and waits for LDS and two barriers a tile alone: neither unit is full
+// (prompts of 128 dims: vector unit 33 % busy, matrix cores 27 %).
 //
 // Split.  A block of 4 waves takes (query, head) rows of one KV head (the heads of a group share the
 // tile) and walks the keys 64 at a time, in two steps of 32.  A wave keeps 64 rows at 128 dims, their queries as
 // operands and their outputs in registers: each LDS operand serves two products, as reading it takes as long as
-// one.  At 256 dims registers end at 32 rows; at 64 dims 32 rows leave room for two blocks a unit, which fill each
-// other's waits (four prompts of 2000 over 6000 keys, 14 / 2 heads: 315 us with 64 rows, 266).  Keys and dims are the
+// one.  At 256 dims registers end at 32 rows; at 64 dims 32 rows leave room for three blocks a unit (168 registers), which
+// fill each other's waits (four prompts of 2000 over 6000 keys, 14 / 2 heads: 315 us with 64 rows, 263).  Keys and dims are the
 // rows of the products,
 // so that a lane's scores are its share of the next operand.  A step is ordered by hand: a wave issues
 // in order, so vector work is placed between matrix instructions, beside which it runs.
-// Measured: 806, 640 and 858 TFLOP/s at 128, 64 and 256 dims where blocks fill the GPU evenly (without the codes'
-// conversion 952 at 128 dims, without barriers 872).  Four ragged chunks of prompts behind 1500 to 8000 keys (40 / 8
-// heads x 128): 278 us, 655 TFLOP/s, a fifth of it waiting for the longest blocks; cutting those by
+// Measured: 815, 673 and 870 TFLOP/s at 128, 64 and 256 dims where blocks fill the GPU evenly (at 128 dims once 952 without
+// the codes' conversion, 872 without barriers, of 806).  Four ragged chunks of prompts behind 1500 to 8000 keys (40 / 8
+// heads x 128): 270 us, 676 TFLOP/s: 376 blocks on 256 units, so that a second round is half empty; cutting all blocks by
 // keys cost more than it brought (286 to 337 us), and so did blocks of 128 rows (355 us).
 #include <hip/hip_runtime.h>
 

@@ -14,9 +14,10 @@
 //     pieces (24 bits).  Of fewer tokens each expanding block does so itself: a launch costs more there.
 //   expand: the pieces follow each other along the matrix product's k: for ranks up to 16 they fit
 //     in one or two instructions.  A lane ends with 4 neighbouring outputs of a token, four lanes with 16.
-// Measured.  Rank 16, K 5120, parts of 5120, 1024 and 1024 rows: one token 8.0 us, 64 tokens of 48 adapters 19 us,
+// Measured.  Rank 16, K 5120, parts of 5120, 1024 and 1024 rows: one token 8.5 us, 64 tokens of 48 adapters 16 us,
 // two launches, each of them one chain of loads.  Rank 64, K 13824, 5120 rows, 4464 tokens of prompts beside a fp32
-// projection: 121 us, of which shrinking 57 us, joining 5 us, expanding 59 us (183 MB, 3.1 TB/s).
+// projection: 120 us, of which shrinking 57 us, joining 5 us, expanding 58 us (183 MB, 3.1 TB/s).  Both launches have two blocks
+// a unit there: shrinking by its 64 KB of LDS (560 blocks for 512 places), expanding by its 174 registers.
 #include <hip/hip_runtime.h>
 
 #include "qmm_device.h"
@@ -387,7 +388,7 @@ Plan plan_of(int64_t T, int64_t K, int64_t rank, int64_t n_parts) {
   // adapters in turn take long where tiles are few (1000 tokens, each its own: 146 and 192 us; 4000: 510 and 471)
   p.shares = !many ? int(T < 16 ? T < 1 ? 1 : T : 16) : T > 2048 ? 1 : 4;
   const int64_t blocks = p.tiles * p.row_groups * (many ? 1 : p.shares), most = (K / 64 + kWaves - 1) / kWaves;
-  // Two blocks for each unit, whose registers hold no more where tokens are many.  There 8 or 16 ranges, a multiple
+  // Two blocks for each unit, whose LDS holds no more where tokens and ranks are many.  There 8 or 16 ranges, a multiple
   // of the dies, keep each die to its own ranges of the adapters' weights (8 ranges 126 us, 7 of them 130 us).
   int64_t s = blocks ? 2 * cus / blocks : 1;
   if (many && s >= 6) s = s >= 12 ? 16 : 8;

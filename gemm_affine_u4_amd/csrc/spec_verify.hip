@@ -5,9 +5,9 @@
 // distributed as the target's whatever the drafts' distribution is.  Products of two fp32
 // values are exact in 64 bits; sums are 64-bit, so that a number within 2^-50 or so of a border between
 // two tokens is all that their order could move.
-// Bound: HBM, one row of p and one of q a sequence (64 sequences x 152001 fp32 entries with draft probabilities: 21 us, of it
+// Bound: HBM, one row of p and one of q a sequence (64 sequences x 152001 fp32 entries with draft probabilities: 19 us, of it
 // the sums 14 at 5.6 TB/s and the pick 6), and for few sequences the round trips to memory that depend on each other:
-// the sequence's drafts, their probabilities, the row, and the launches (5 drafts of one sequence, 32000 entries: 8.8 us).
+// the sequence's drafts, their probabilities, the row, and the launches (5 drafts of one sequence, 32000 entries: 9.1 us).
 // Split: a block takes kChunk entries of a sequence's row, finds by itself how many of its drafts are
 // kept (a few gathered numbers) and writes the chunk's sums; a second launch, a block a sequence,
 // finds by a scan of the chunks' sums in which of them the number falls, and in that one by a
